@@ -473,6 +473,137 @@ int kda_commit_ex(void* state_pool, int64_t slot_stride, int64_t n_slots, const 
                   const float* corr, const void* kg, const float* A_log, const float* dt_bias,
                   float lower_bound, int32_t state_bf16, int32_t kg_fp16, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The paged key/value cache of softmax-attention layers that stand between
+ * the recurrent layers of a model: pages for a step's tokens, the write of
+ * their keys and values, and causal attention over the cache.  The pages of
+ * the reference have no counterpart; head dimension 128, bf16 or fp16.
+ * ---------------------------------------------------------------------------
+ *
+ * kda_kv_pages - who owns which page (device arrays, int32).  Request b's
+ * token at position p lives in page block_table[b][p / page_size], row
+ * p % page_size; its slot is page * page_size + row.
+ *   kv_lens      [n_req] tokens cached per request
+ *   block_table  row b at block_table + b * table_stride, table_cols columns;
+ *                entries past a request's pages are not read
+ *   free_pages   [n_pages], a stack: free_pages[0 .. *free_count - 1] are
+ *                free, the next page taken is the last of them
+ */
+typedef struct kda_kv_pages {
+  int32_t* kv_lens;
+  int32_t* block_table;
+  int64_t table_stride;
+  int32_t* free_pages;
+  int32_t* free_count;
+  int32_t n_req, table_cols;
+  int32_t n_pages;   /* pages of the cache */
+  int32_t page_size; /* 16, 32, 64, 128 or 256 tokens */
+} kda_kv_pages;
+
+/*
+ * kda_kv_extend - take the pages that each request's new_lens[b] new tokens
+ * need and lay the step out.  Pages go to the requests in order, and within
+ * a request to ascending columns.  A request whose pages no longer fit the
+ * free list, and every later one that needs a page, is not admitted: it keeps
+ * its kv_lens and its row, and its tokens get slot -1 (one that fits its last
+ * page is admitted even then).
+ *   pages       kv_lens grows by new_lens for admitted requests; their rows,
+ *               free_pages and *free_count are updated in place
+ *   new_lens    device int32 [n_req], >= 0
+ *   cu_seqlens  device int32 [n_req + 1], written: exclusive sums of new_lens
+ *               (the packed layout of the step's tokens, admitted or not)
+ *   slot_map    device int32 [max_tokens], written: each token's slot or -1,
+ *               -1 past the last token
+ *   step_lens   device int32 [n_req], written: the admitted requests' new
+ *               kv_lens, 0 for the others (what attention takes as kv_lens)
+ * A negative new_lens (counted as 0), a kv_lens outside its row and a request
+ * that outgrows table_cols set KDA_ERR_DEVICE_INDEX and are not admitted.
+ * More tokens than max_tokens (those past it get no slot), a page outside
+ * [0, n_pages) (slot -1) and a *free_count outside [0, n_pages] (clamped) set
+ * it too.
+ */
+int kda_kv_extend(const kda_kv_pages* pages, const int32_t* new_lens, int32_t* cu_seqlens,
+                  int32_t* slot_map, int32_t max_tokens, int32_t* step_lens, void* stream);
+
+/*
+ * kda_kv_truncate - keep the first keep_lens[b] tokens of each request and
+ * hand the pages past them back: rejected drafts, finished requests (0).
+ * Pages return to the stack in descending (request, column) order, so a
+ * truncate to the former lengths undoes a kda_kv_extend exactly.  Returned
+ * table entries become -1; keep_lens[b] >= kv_lens[b] changes nothing; a
+ * negative one, or a kv_lens outside its row, sets KDA_ERR_DEVICE_INDEX and
+ * leaves the request alone; a stack that would pass n_pages sets it too, and
+ * the pages past it are not handed back.
+ */
+int kda_kv_truncate(const kda_kv_pages* pages, const int32_t* keep_lens, void* stream);
+
+/*
+ * kda_kv_cache - the pages' storage: element (page, row, head, c) of k at
+ * k + page * k_stride_page + row * k_stride_tok + head * k_stride_head + c,
+ * v likewise (elements; token-major, head-major or interleaved pages).
+ * 16-byte aligned, strides positive multiples of 8.
+ */
+typedef struct kda_kv_cache {
+  void* k; int64_t k_stride_page, k_stride_tok, k_stride_head;
+  void* v; int64_t v_stride_page, v_stride_tok, v_stride_head;
+  int32_t dtype;   /* KDA_DTYPE_BF16 or KDA_DTYPE_FP16: cache, q, k, v and out */
+  int32_t n_pages, page_size, hkv;
+} kda_kv_cache;
+
+/*
+ * kda_kv_append - write k and v [t_total, Hkv, 128] (token and head strides in
+ * elements, multiples of 8, 16-byte aligned) to the slots slot_map[t].  A
+ * negative slot skips the token; a slot past the cache sets
+ * KDA_ERR_DEVICE_INDEX and skips it.  Two tokens on one slot race.
+ */
+int kda_kv_append(const kda_kv_cache* cache, const void* k, int64_t k_stride_tok, int64_t k_stride_head,
+                  const void* v, int64_t v_stride_tok, int64_t v_stride_head, const int32_t* slot_map,
+                  int32_t t_total, void* stream);
+
+/*
+ * kda_paged_attention - causal softmax attention of a step's tokens over the
+ * paged cache, which holds them already.  Request b owns the packed tokens
+ * cu_seqlens[b] .. cu_seqlens[b+1]-1, the last of its kv_lens[b] cached
+ * tokens: token i stands at position p = kv_lens[b] - n_b + i.  Query head h
+ * reads key head h / (Hq/Hkv).  Position p sees the keys
+ *   j <= p, and with window > 0: j > p - window or j < sinks,
+ * in pages that the request has (a negative block_table entry hides its
+ * keys).  With s_j = scale <q, k_j> over the visible j:
+ *   out = sum_j e^{s_j} v_j / sum_j e^{s_j},   lse = ln sum_j e^{s_j}
+ * and out = 0, lse = -inf where that sum is 0: a token that sees nothing
+ * (p < 0 among them).
+ * What is hidden has no influence, whatever it holds (NaN and infinities
+ * included).  One call serves single tokens, short windows and prompt chunks
+ * in any mix.
+ *   q           [t_total, Hq, 128], strides as kda_kv_append's k
+ *   out         [t_total, Hq, 128] contiguous, 16-byte aligned, written;
+ *               tokens past cu_seqlens[n_req] are left alone
+ *   lse         fp32 [t_total, Hq] or NULL, written
+ *   cu_seqlens  device int32 [n_req + 1], kv_lens device int32 [n_req]
+ *   block_table device int32, row b at b * table_stride, table_cols columns
+ *   scale       > 0, finite (128^-0.5 usual)
+ *   window      0: no window; > 0: the last ``window`` positions, its own
+ *               among them
+ *   sinks       >= 0: with a window, the first positions that stay visible
+ *   workspace   16-byte aligned, kda_paged_attention_workspace_bytes() bytes, whose first
+ *               KDA_ATTENTION_ZEROED_BYTES are zero before the first call;
+ *               every call leaves them zero.  Calls that overlap on the GPU
+ *               need workspaces of their own.
+ * An entry >= n_pages that a token would see, a kv_lens outside
+ * [0, table_cols * page_size] and cu_seqlens that decrease or leave
+ * [0, t_total] set KDA_ERR_DEVICE_INDEX: the page is hidden, the length
+ * clamped, the request skipped.
+ */
+#define KDA_ATTENTION_ZEROED_BYTES 4096
+size_t kda_paged_attention_workspace_bytes(void);
+int kda_paged_attention(const kda_kv_cache* cache, const void* q, int64_t q_stride_tok,
+                        int64_t q_stride_head, int32_t hq, int32_t t_total, void* out, float* lse,
+                        const int32_t* cu_seqlens, const int32_t* kv_lens, const int32_t* block_table,
+                        int64_t table_stride, int32_t table_cols, int32_t n_req, float scale,
+                        int32_t window, int32_t sinks, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
 /* Thread-local text of the last error returned on this thread ("" if none).
  * kda_last_error_message is the same function under the name the serving
  * contract uses; kda_last_error is kept for existing callers. */

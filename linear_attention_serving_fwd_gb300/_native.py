@@ -30,7 +30,9 @@ EXPORTS = ("kda_chunk_workspace_bytes", "kda_chunk_fwd", "kda_decode", "kda_veri
            "kda_last_error", "kda_last_error_message", "kda_device_status", "kda_trace_enable", "kda_trace_read",
            "kda_version", "kda_chunk_fwd_noalloc", "kda_commit", "kda_chunk_fwd_ex",
            "kda_decode_steps", "kda_verify_ex", "kda_commit_ex", "kda_chunk_fwd_host",
-           "kda_chunk_fwd_host_workspace_bytes", "kda_conv_scratch_bytes", "kda_selftest_wait_timeout")
+           "kda_chunk_fwd_host_workspace_bytes", "kda_conv_scratch_bytes", "kda_selftest_wait_timeout",
+           "kda_kv_extend", "kda_kv_truncate", "kda_kv_append", "kda_paged_attention",
+           "kda_paged_attention_workspace_bytes")
 
 
 class KdaActivations(ctypes.Structure):
@@ -60,6 +62,26 @@ class KdaConv(ctypes.Structure):
         ("state_indices", ctypes.c_void_p), ("has_initial_state", ctypes.c_void_p),
         ("num_accepted", ctypes.c_void_p),
         ("scratch", ctypes.c_void_p), ("scratch_bytes", ctypes.c_size_t),
+    ]
+
+
+class KdaKvPages(ctypes.Structure):
+    _fields_ = [
+        ("kv_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+        ("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_void_p),
+        ("n_req", ctypes.c_int32), ("table_cols", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+    ]
+
+
+class KdaKvCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("k_stride_page", ctypes.c_int64), ("k_stride_tok", ctypes.c_int64),
+        ("k_stride_head", ctypes.c_int64),
+        ("v", ctypes.c_void_p), ("v_stride_page", ctypes.c_int64), ("v_stride_tok", ctypes.c_int64),
+        ("v_stride_head", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("hkv", ctypes.c_int32),
     ]
 
 
@@ -100,6 +122,18 @@ def _declare(lib):
     lib.kda_commit.restype = ctypes.c_int
     lib.kda_commit_ex.argtypes = [P, I64, I64, P, P, I32, I32, I32, P, P, P, P, ctypes.c_float, I32, I32, P]
     lib.kda_commit_ex.restype = ctypes.c_int
+    KP, KC = ctypes.POINTER(KdaKvPages), ctypes.POINTER(KdaKvCache)
+    lib.kda_kv_extend.argtypes = [KP, P, P, P, I32, P, P]
+    lib.kda_kv_extend.restype = ctypes.c_int
+    lib.kda_kv_truncate.argtypes = [KP, P, P]
+    lib.kda_kv_truncate.restype = ctypes.c_int
+    lib.kda_kv_append.argtypes = [KC, P, I64, I64, P, I64, I64, P, I32, P]
+    lib.kda_kv_append.restype = ctypes.c_int
+    lib.kda_paged_attention_workspace_bytes.argtypes = []
+    lib.kda_paged_attention_workspace_bytes.restype = SZ
+    lib.kda_paged_attention.argtypes = [KC, P, I64, I64, I32, I32, P, P, P, P, P, I64, I32, I32,
+                                        ctypes.c_float, I32, I32, P, SZ, P]
+    lib.kda_paged_attention.restype = ctypes.c_int
     lib.kda_last_error.argtypes = []
     lib.kda_last_error.restype = ctypes.c_char_p
     lib.kda_last_error_message.argtypes = []

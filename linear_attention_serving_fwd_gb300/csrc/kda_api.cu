@@ -214,6 +214,8 @@ void set_last_error(int code, const char* msg) {
   g_last_error = msg;
 }
 
+unsigned* device_error_word() { return error_word_ptr(); }
+
 void trace_begin(const char* name, cudaStream_t stream) {
   if (!g_trace_on) return;
   std::lock_guard<std::mutex> lk(g_trace_mu);

@@ -1,0 +1,244 @@
+// Pages for a step's tokens (extend), their return (truncate) and the write
+// of keys and values to their slots (append).
+#include "kda_kv.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int PT = 1024;  // threads: one request each per round
+
+// Inclusive sums of two values over the block, and both totals.
+struct Scan2 {
+  long long a, b, total_a, total_b;
+};
+__device__ __forceinline__ Scan2 block_scan2(long long a, long long b, long long (*sums)[2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, a, s), y = __shfl_up_sync(0xffffffffu, b, s);
+    if (lane >= s) {
+      a += x;
+      b += y;
+    }
+  }
+  __syncthreads();  // the previous call's sums have been read
+  if (lane == 31) {
+    sums[warp][0] = a;
+    sums[warp][1] = b;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    long long x = sums[lane][0], y = sums[lane][1];
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, x, s), v = __shfl_up_sync(0xffffffffu, y, s);
+      if (lane >= s) {
+        x += u;
+        y += v;
+      }
+    }
+    sums[lane][0] = x;
+    sums[lane][1] = y;
+  }
+  __syncthreads();
+  if (warp > 0) {
+    a += sums[warp - 1][0];
+    b += sums[warp - 1][1];
+  }
+  return {a, b, sums[31][0], sums[31][1]};
+}
+
+// Last i in [0, n) with off[i] <= x (off non-decreasing, off[0] <= x): the
+// owner of element x when off holds exclusive sums.
+__device__ __forceinline__ int owner(const int* off, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (off[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int clamped_count(const KvPagesParams& p, bool report) {
+  const int c = *p.free_count;
+  if (c < 0 || c > p.n_pages) {
+    if (report) set_error(p.err, ERR_INDEX);
+    return c < 0 ? 0 : p.n_pages;
+  }
+  return c;
+}
+
+// One thread per request and round: page counts and token counts are summed
+// over the block, then the round's tokens and pages are spread over all
+// threads, each finding its request in the sums.
+__global__ void __launch_bounds__(PT) kv_extend_kernel(KvPagesParams p) {
+  __shared__ long long sums[32][2];
+  __shared__ int tok_off[PT], page_off[PT], r_len[PT], r_have[PT];  // r_have < 0: not admitted
+  const int t = threadIdx.x, page = 1 << p.page_shift;
+  const int count = clamped_count(p, t == 0);
+  long long tok_base = 0, page_base = 0, taken = 0;
+  if (t == 0) p.cu_seqlens[0] = 0;
+  for (int r0 = 0; r0 < p.n_req; r0 += PT) {
+    const int b = r0 + t, n_round = min(PT, p.n_req - r0);
+    long long n_new = 0, add = 0;
+    int len = 0, have = 0;
+    bool valid = false;
+    if (b < p.n_req) {
+      len = p.kv_lens[b];
+      n_new = p.lens[b];
+      valid = n_new >= 0 && len >= 0 && len <= (p.table_cols << p.page_shift);
+      if (n_new < 0) n_new = 0;
+      if (valid) {
+        have = (len + page - 1) >> p.page_shift;
+        const long long need = (len + n_new + page - 1) >> p.page_shift;
+        valid = need <= p.table_cols;
+        add = valid ? need - have : 0;
+      }
+      if (!valid) set_error(p.err, ERR_INDEX);
+    }
+    const Scan2 s = block_scan2(n_new, add, sums);
+    const bool fits = valid && (add == 0 || page_base + s.b <= count);
+    const long long my_tok = tok_base + s.a - n_new;
+    if (b < p.n_req) {
+      // sums past int32 are out of max_tokens' range as well
+      p.cu_seqlens[b + 1] = (int)min(tok_base + s.a, 0x7fffffffLL);
+      p.step_lens[b] = fits ? (int)(len + n_new) : 0;
+      if (fits) p.kv_lens[b] = (int)(len + n_new);
+      if (tok_base + s.a > p.max_tokens && n_new > 0) set_error(p.err, ERR_INDEX);
+    }
+    tok_off[t] = (int)min(my_tok, 0x7fffffffLL);
+    page_off[t] = (int)(s.b - add);
+    r_len[t] = len;
+    r_have[t] = fits ? have : -1;
+    // admitted pages are a prefix of the sums: the first refusal ends it
+    const long long mine = fits && add > 0 ? page_base + s.b : 0;
+    __syncthreads();
+    const long long tok_end = min(tok_base + s.total_a, (long long)p.max_tokens);
+    const int pages_end = (int)min(s.total_b, max(0LL, count - page_base));
+    for (int i = t; i < pages_end; i += PT) {
+      const int r = owner(page_off, n_round, i);
+      if (r_have[r] < 0) continue;
+      const int col = r_have[r] + i - page_off[r];
+      p.table[(int64_t)(r0 + r) * p.table_stride + col] = p.free_pages[count - 1 - (page_base + i)];
+    }
+    for (long long i = tok_base + t; i < tok_end; i += PT) {
+      const int r = owner(tok_off, n_round, (int)i);
+      int slot = -1;
+      if (r_have[r] >= 0) {
+        const int pos = r_len[r] + (int)i - tok_off[r], col = pos >> p.page_shift;
+        const long long at = page_base + page_off[r] + col - r_have[r];
+        const int pg = col < r_have[r] ? p.table[(int64_t)(r0 + r) * p.table_stride + col] : p.free_pages[count - 1 - at];
+        slot = (pg << p.page_shift) + (pos & (page - 1));
+        if (pg < 0 || pg >= p.n_pages) {
+          set_error(p.err, ERR_INDEX);
+          slot = -1;
+        }
+      }
+      p.slot_map[i] = slot;
+    }
+    long long top = mine;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+    __syncthreads();
+    if ((t & 31) == 0) sums[t >> 5][0] = top;
+    __syncthreads();
+    for (int i = 0; i < 32; ++i) taken = max(taken, sums[i][0]);
+    tok_base += s.total_a;
+    page_base += s.total_b;
+  }
+  for (long long i = tok_base + t; i < p.max_tokens; i += PT) p.slot_map[i] = -1;
+  if (t == 0) *p.free_count = count - (int)taken;
+}
+
+// Requests from the last to the first, one per thread and round.
+__global__ void __launch_bounds__(PT) kv_truncate_kernel(KvPagesParams p) {
+  __shared__ long long sums[32][2];
+  __shared__ int page_off[PT], r_have[PT];
+  const int t = threadIdx.x, page = 1 << p.page_shift;
+  const int count = clamped_count(p, t == 0);
+  long long base = 0;
+  for (int r0 = 0; r0 < p.n_req; r0 += PT) {
+    const int b = p.n_req - 1 - (r0 + t), n_round = min(PT, p.n_req - r0);
+    long long drop = 0;
+    int have = 0;
+    if (b >= 0) {
+      const int len = p.kv_lens[b], keep = p.lens[b];
+      if (keep < 0 || len < 0 || len > (p.table_cols << p.page_shift)) {
+        set_error(p.err, ERR_INDEX);
+      } else if (keep < len) {
+        have = (len + page - 1) >> p.page_shift;
+        drop = have - ((keep + page - 1) >> p.page_shift);
+        p.kv_lens[b] = keep;
+      }
+    }
+    const Scan2 s = block_scan2(0, drop, sums);
+    page_off[t] = (int)(s.b - drop);
+    r_have[t] = have;
+    __syncthreads();
+    for (long long i = t; i < s.total_b; i += PT) {
+      const int r = owner(page_off, n_round, (int)i);
+      const int col = r_have[r] - 1 - ((int)i - page_off[r]);
+      int32_t* entry = p.table + (int64_t)(p.n_req - 1 - (r0 + r)) * p.table_stride + col;
+      const long long at = count + base + i;
+      if (at < p.n_pages) {
+        p.free_pages[at] = *entry;
+        *entry = -1;
+      } else {
+        set_error(p.err, ERR_INDEX);
+      }
+    }
+    base += s.total_b;
+    __syncthreads();
+  }
+  if (t == 0) *p.free_count = (int)min(count + base, (long long)p.n_pages);
+}
+
+// One 16-byte piece of a key and of a value row per thread and step.
+__global__ void __launch_bounds__(256) kv_append_kernel(KvAppendParams p) {
+  const int64_t pieces = (int64_t)p.t_total * p.hkv * (D / 8);
+  const int64_t rows = (int64_t)p.n_pages << p.page_shift;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < pieces; i += gridDim.x * 256ll) {
+    const int c = (int)(i % (D / 8)) * 8;
+    const int64_t th = i / (D / 8);
+    const int h = (int)(th % p.hkv), t = (int)(th / p.hkv);
+    const int slot = p.slot_map[t];
+    if (slot < 0) continue;
+    if (slot >= rows) {
+      set_error(p.err, ERR_INDEX);
+      continue;
+    }
+    const int64_t pg = slot >> p.page_shift, row = slot & ((1 << p.page_shift) - 1);
+    const int4 kx = *reinterpret_cast<const int4*>(p.k + t * p.k_st + h * p.k_sh + c);
+    const int4 vx = *reinterpret_cast<const int4*>(p.v + t * p.v_st + h * p.v_sh + c);
+    *reinterpret_cast<int4*>(p.kc + pg * p.kc_sp + row * p.kc_st + h * p.kc_sh + c) = kx;
+    *reinterpret_cast<int4*>(p.vc + pg * p.vc_sp + row * p.vc_st + h * p.vc_sh + c) = vx;
+  }
+}
+
+}  // namespace
+
+int launch_kv_extend(const KvPagesParams& p, cudaStream_t stream) {
+  trace_begin("kv_extend", stream);
+  kv_extend_kernel<<<1, PT, 0, stream>>>(p);
+  trace_end(stream);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+int launch_kv_truncate(const KvPagesParams& p, cudaStream_t stream) {
+  trace_begin("kv_truncate", stream);
+  kv_truncate_kernel<<<1, PT, 0, stream>>>(p);
+  trace_end(stream);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+int launch_kv_append(const KvAppendParams& p, cudaStream_t stream) {
+  const int64_t pieces = (int64_t)p.t_total * p.hkv * (D / 8);
+  const int64_t blocks = (pieces + 255) / 256;
+  trace_begin("kv_append", stream);
+  kv_append_kernel<<<(unsigned)(blocks < 152 * 32 ? blocks : 152 * 32), 256, 0, stream>>>(p);
+  trace_end(stream);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace kda

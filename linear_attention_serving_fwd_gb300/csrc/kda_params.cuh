@@ -126,6 +126,9 @@ struct ChunkParams {
 void trace_begin(const char* name, cudaStream_t stream);
 void trace_end(cudaStream_t stream);
 
+// The current device's error word (null when it cannot be resolved).
+unsigned* device_error_word();
+
 // Set the thread-local text that kda_last_error() returns.
 void set_last_error(int code, const char* msg);
 

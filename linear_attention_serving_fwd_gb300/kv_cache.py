@@ -1,0 +1,175 @@
+"""The paged key/value cache of softmax-attention layers: the handles that a
+serving program keeps, and the calls of include/kda.h on them.
+
+A step of such a program is: :func:`kda_kv_extend` takes pages for its new
+tokens, each layer writes its keys and values with :func:`kda_kv_append` and
+runs :func:`kda_paged_attention`; :func:`kda_kv_truncate` hands the pages of
+rejected drafts and finished requests back.  Argument marshalling only.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import _native
+
+D = 128
+_DTYPES = {torch.bfloat16: _native.KDA_DTYPE_BF16, torch.float16: _native.KDA_DTYPE_FP16}
+
+
+def _stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _int32(t, name, numel=None):
+    if t.dtype != torch.int32 or not t.is_contiguous() or not t.is_cuda:
+        raise TypeError(f"{name} must be a contiguous int32 CUDA tensor.")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} entries (got {t.numel()}).")
+    return t.data_ptr()
+
+
+def _table(t, n_req):
+    if t.dtype != torch.int32 or not t.is_cuda:
+        raise TypeError("block_table must be an int32 CUDA tensor.")
+    if t.dim() != 2 or t.shape[0] != n_req or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"block_table must be [{n_req}, columns] with contiguous rows (got {tuple(t.shape)}).")
+    return t.data_ptr()
+
+
+def _rows(t, name, dtype, heads=None):
+    """[T, H, 128] of the cache's type; a size-1 dimension's stride is free."""
+    if t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor of the cache's dtype {dtype} (got {t.dtype} on {t.device}).")
+    if t.dim() != 3 or t.shape[2] != D or t.stride(2) != 1 or (heads is not None and t.shape[1] != heads):
+        want = "H" if heads is None else heads
+        raise ValueError(f"{name} must be [T, {want}, 128] with a contiguous last dimension (got {tuple(t.shape)}).")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+
+
+class KvPages:
+    """Who owns which page: ``kv_lens`` [n_req], ``block_table`` [n_req,
+    columns], the stack ``free_pages`` [n_pages] and its height ``free_count``
+    [1], all int32 CUDA tensors that :func:`kda_kv_extend` and
+    :func:`kda_kv_truncate` update in place.  :meth:`empty` makes a pool in
+    which every page is free."""
+
+    def __init__(self, kv_lens, block_table, free_pages, free_count, page_size: int):
+        n = kv_lens.numel()
+        g = self._struct = _native.KdaKvPages()
+        g.kv_lens = _int32(kv_lens, "kv_lens")
+        g.block_table, g.table_stride = _table(block_table, n), block_table.stride(0)
+        g.free_pages, g.free_count = _int32(free_pages, "free_pages"), _int32(free_count, "free_count", 1)
+        g.n_req, g.table_cols, g.n_pages, g.page_size = n, block_table.shape[1], free_pages.numel(), page_size
+        self.kv_lens, self.block_table = kv_lens, block_table
+        self.free_pages, self.free_count, self.page_size = free_pages, free_count, page_size
+        self._ref = ctypes.byref(g)
+
+    @classmethod
+    def empty(cls, n_req: int, columns: int, n_pages: int, page_size: int, device="cuda") -> "KvPages":
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.zeros(n_req, **i32), torch.full((n_req, columns), -1, **i32),
+                   torch.arange(n_pages - 1, -1, -1, **i32), torch.full((1,), n_pages, **i32), page_size)
+
+
+class KvCache:
+    """The pages' storage: ``k`` and ``v`` as [n_pages, page_size, Hkv, 128]
+    CUDA tensors of any strides that are multiples of 8 elements with a
+    contiguous last dimension (a permuted view of head-major pages, halves of
+    one tensor), bf16 or fp16."""
+
+    def __init__(self, k, v):
+        if k.dtype not in _DTYPES or v.dtype != k.dtype:
+            raise TypeError("the cache must be torch.bfloat16 or torch.float16, k and v alike.")
+        if k.dim() != 4 or k.shape != v.shape or k.shape[3] != D or k.stride(3) != 1 or v.stride(3) != 1:
+            raise ValueError("k and v must be [n_pages, page_size, Hkv, 128] alike with a contiguous last dimension.")
+        if not k.is_cuda or v.device != k.device:
+            raise ValueError("k and v must be CUDA tensors on one device.")
+        c = self._struct = _native.KdaKvCache()
+        for name, t in (("k", k), ("v", v)):
+            setattr(c, name, t.data_ptr())
+            for dim, what in ((0, "page"), (1, "tok"), (2, "head")):
+                # the stride of a dimension of size 1 is never used
+                setattr(c, f"{name}_stride_{what}", t.stride(dim) if t.shape[dim] > 1 else D)
+        c.dtype = _DTYPES[k.dtype]
+        c.n_pages, c.page_size, c.hkv = k.shape[:3]
+        self.k, self.v, self.dtype, self.n_kv_heads = k, v, k.dtype, k.shape[2]
+        self._ref = ctypes.byref(c)
+
+
+def kda_kv_extend(pages: KvPages, new_lens, max_tokens: int, *, cu_seqlens=None, slot_map=None, step_lens=None,
+                  stream=None):
+    """Take the pages for ``new_lens`` [n_req] new tokens (int32, CUDA), at
+    most ``max_tokens`` in all.  Updates ``pages``; returns (cu_seqlens
+    [n_req + 1], slot_map [max_tokens], step_lens [n_req]), int32: the packed
+    layout, each token's slot (-1 where its request found no pages), and the
+    lengths that attention takes (0 where the request was not admitted)."""
+    n = pages.kv_lens.numel()
+    i32 = dict(dtype=torch.int32, device=pages.kv_lens.device)
+    cu_seqlens = torch.empty(n + 1, **i32) if cu_seqlens is None else cu_seqlens
+    slot_map = torch.empty(max_tokens, **i32) if slot_map is None else slot_map
+    step_lens = torch.empty(n, **i32) if step_lens is None else step_lens
+    _native.check(_native.lib().kda_kv_extend(
+        pages._ref, _int32(new_lens, "new_lens", n), _int32(cu_seqlens, "cu_seqlens", n + 1),
+        _int32(slot_map, "slot_map", max_tokens), max_tokens, _int32(step_lens, "step_lens", n), _stream(stream)))
+    return cu_seqlens, slot_map, step_lens
+
+
+def kda_kv_truncate(pages: KvPages, keep_lens, *, stream=None) -> None:
+    """Keep the first ``keep_lens`` [n_req] tokens of each request (int32,
+    CUDA) and hand the pages past them back."""
+    _native.check(_native.lib().kda_kv_truncate(
+        pages._ref, _int32(keep_lens, "keep_lens", pages.kv_lens.numel()), _stream(stream)))
+
+
+def kda_kv_append(cache: KvCache, k, v, slot_map, *, stream=None) -> None:
+    """Write k and v [T, Hkv, 128] to the slots ``slot_map`` [T] (int32, -1
+    skips the token)."""
+    kp, kt, kh = _rows(k, "k", cache.dtype, cache.n_kv_heads)
+    vp, vt, vh = _rows(v, "v", cache.dtype, cache.n_kv_heads)
+    t = k.shape[0]
+    if v.shape[0] != t:
+        raise ValueError("k and v must have the same number of tokens.")
+    _native.check(_native.lib().kda_kv_append(
+        cache._ref, kp, kt, kh, vp, vt, vh, _int32(slot_map, "slot_map", t), t, _stream(stream)))
+
+
+def paged_attention_workspace(device=None) -> torch.Tensor:
+    """A workspace for :func:`kda_paged_attention`.  One serves any sequence
+    of calls on one stream; calls that overlap need their own."""
+    n = int(_native.lib().kda_paged_attention_workspace_bytes())
+    return torch.zeros(n, dtype=torch.uint8, device="cuda" if device is None else device)
+
+
+def kda_paged_attention(cache: KvCache, q, cu_seqlens, kv_lens, block_table, *, scale: Optional[float] = None,
+                        window: int = 0, sinks: int = 0, out=None, lse=None, return_lse: bool = False,
+                        workspace=None, stream=None):
+    """Causal attention of packed tokens q [T, Hq, 128] over the paged cache,
+    which holds them already: request b owns tokens cu_seqlens[b] ..
+    cu_seqlens[b+1]-1, the last of its kv_lens[b] cached ones.  With
+    ``window`` > 0 a token sees the last ``window`` positions, its own among
+    them, and the first ``sinks``.  Returns (out [T, Hq, 128], lse fp32
+    [T, Hq] or None).  ``workspace``: :func:`paged_attention_workspace`, made
+    for the call when not given."""
+    qp, qt, qh = _rows(q, "q", cache.dtype)
+    t, hq, n = q.shape[0], q.shape[1], kv_lens.numel()
+    if out is None:
+        out = torch.empty((t, hq, D), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or not out.is_cuda:
+        raise ValueError("out must be a contiguous CUDA tensor of q's shape and dtype.")
+    if lse is None:
+        lse = torch.empty((t, hq), dtype=torch.float32, device=q.device) if return_lse else None
+    elif tuple(lse.shape) != (t, hq) or lse.dtype != torch.float32 or not lse.is_contiguous() or not lse.is_cuda:
+        raise ValueError("lse must be a contiguous float32 CUDA tensor [T, Hq].")
+    if workspace is None:
+        workspace = paged_attention_workspace(q.device)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or not workspace.is_cuda:
+        raise ValueError("workspace must be a contiguous uint8 CUDA tensor.")
+    _native.check(_native.lib().kda_paged_attention(
+        cache._ref, qp, qt, qh, hq, t, out.data_ptr(), None if lse is None else lse.data_ptr(),
+        _int32(cu_seqlens, "cu_seqlens", n + 1), _int32(kv_lens, "kv_lens"), _table(block_table, n),
+        block_table.stride(0), block_table.shape[1], n, D ** -0.5 if scale is None else scale, window, sinks,
+        workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    return out, lse

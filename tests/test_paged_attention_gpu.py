@@ -1,0 +1,344 @@
+"""Attention over the paged cache against the fp64 oracle.
+
+Tolerance, element by element, with u = eps / 2 of the 16-bit type (half a
+step, relative): the output is rounded to that type once (u |o|) and so is
+each weight before the product with the values (u W, W = sum_j p_j |v_j|, the
+normalised p).  In fp16 a weight may also fall below the normal range: at
+most 2^-25 of the largest, per key (n 2^-25 max|v|).  The 32-bit steps: a
+score is off by at most 128 additions at 2^-24 of sum |q_i k_i| scale, which
+is below 128 * 2^-24 * 16 = 2^-13 here, so p is off by as much, and the sum
+as well: 2^-12 W, and 2^-13 + 2^-22 |lse| for the lse.  Rows that see nothing
+are exactly 0 and -inf."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import linear_attention_serving_fwd_gb300 as kda
+from oracle import paged
+
+pytestmark = pytest.mark.gpu
+INDEX = 5
+BF16, FP16 = torch.bfloat16, torch.float16
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _np(x):
+    return x.double().cpu().numpy()
+
+
+class Case:
+    """new, kv: tokens of each request and its cached tokens, these included."""
+
+    def __init__(self, new, kv, hq, hkv, page, dtype=BF16, layout="tokens", seed=0, gain=1.0, extra_cols=1, cols=None):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dtype)  # noqa: E731
+        owned = [-(-n // page) for n in kv]
+        n_pages = sum(owned) + 2
+        shape = (n_pages, hkv, page, 128) if layout == "heads" else (n_pages, page, hkv, 128)
+        if layout == "pairs":
+            both = rnd(n_pages, 2, page, hkv, 128)
+            self.k, self.v = both[:, 0], both[:, 1]
+        else:
+            self.k, self.v = rnd(*shape), rnd(*shape)
+            if layout == "heads":
+                self.k, self.v = self.k.permute(0, 2, 1, 3), self.v.permute(0, 2, 1, 3)
+        ids = torch.randperm(n_pages, generator=g, device="cuda").tolist()
+        cols = cols or max(owned + [1]) + extra_cols
+        self.table = []
+        for n in owned:
+            self.table.append([ids.pop() for _ in range(n)] + [-1] * (cols - n))
+        t = sum(new)
+        self.q = (rnd(t, hq + 2, 128) * gain)[:, 1:hq + 1]  # a band of a wider projection
+        self.cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+        self.new, self.kv, self.page, self.dtype, self.scale = new, list(kv), page, dtype, 128 ** -0.5
+        self.owned = owned
+
+    def rows(self, b):
+        """(page, row) of request b's tokens in order."""
+        return [(self.table[b][j // self.page], j % self.page) for j in range(self.kv[b])]
+
+    def run(self, window=0, sinks=0, **kw):
+        out, lse = kda.kda_paged_attention(kda.KvCache(self.k, self.v), self.q, _i32(self.cu), _i32(self.kv),
+                                           _i32(self.table), scale=self.scale, window=window, sinks=sinks,
+                                           return_lse=True, **kw)
+        return out, lse
+
+    def check(self, window=0, sinks=0, result=None, rows=slice(None), q=None, k=None, v=None, kv=None):
+        out, lse = self.run(window, sinks) if result is None else result
+        want, want_lse, weight = paged.attention(
+            _np(self.q if q is None else q), _np(self.k if k is None else k), _np(self.v if v is None else v), self.cu,
+            self.kv if kv is None else kv, self.table, self.scale, window, sinks)
+        out, lse = _np(out)[rows], _np(lse)[rows]
+        want, want_lse, weight = want[rows], want_lse[rows], weight[rows]
+        u = torch.finfo(self.dtype).eps / 2
+        vmax = float(torch.nan_to_num(self.v.float(), 0, 0, 0).abs().max())
+        tol = u * np.abs(want) + (u + 2.0 ** -12) * weight * (1 + u)
+        tol += (max(self.kv + [0]) * 2.0 ** -25 * vmax if self.dtype == FP16 else 0) + 1e-30
+        empty = np.isneginf(want_lse)
+        assert np.array_equal(empty, np.isneginf(lse)) and not out[empty].any()
+        off = np.abs(out - want) - tol
+        assert np.isfinite(out).all() and off.max(initial=-1) <= 0, f"{np.argmax(off)}: {off.max()}"
+        lse_off = np.abs(lse[~empty] - want_lse[~empty]) - 2.0 ** -13 - 2.0 ** -22 * np.abs(want_lse[~empty])
+        assert lse_off.max(initial=-1) <= 0, lse_off.max()
+        assert kda.kda_device_status() == 0
+
+
+# --- lengths, heads, pages, windows ---------------------------------------------
+
+@pytest.mark.parametrize("kv", [1, 2, 15, 16, 17, 127, 128, 129, 255, 256, 257, 385, 1000])
+@pytest.mark.parametrize("dtype,layout,page", [(BF16, "tokens", 16), (FP16, "heads", 64), (BF16, "pairs", 256)])
+def test_single_tokens(kv, dtype, layout, page):
+    Case([1, 1], [kv, max(1, kv - 1)], 4, 2, page, dtype, layout, seed=kv).check()
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (2, 1), (3, 1), (10, 2), (6, 1), (7, 1), (8, 1), (24, 2), (16, 1), (33, 1),
+                                   (128, 1), (100, 1)])
+@pytest.mark.parametrize("new,kv", [([1, 3], [200, 130]), ([150], [150]), ([40], [300])])
+def test_head_groups(hq, hkv, new, kv):
+    Case(new, kv, hq, hkv, 32, seed=hq).check()
+
+
+@pytest.mark.parametrize("new,kv", [
+    ([128], [128]), ([129], [129]), ([127], [127]), ([256], [256]), ([257], [257]), ([300], [300]), ([513], [513]),
+    ([64], [1000]), ([200], [713]), ([5], [517]), ([1, 130, 2, 256, 1], [700, 130, 9, 600, 1]),
+    ([0, 3, 0, 140, 0], [5, 3, 0, 270, 900]),
+])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_chunks(new, kv, dtype):
+    Case(new, kv, 2, 1, 64, dtype, seed=sum(kv)).check()
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 0), (100, 5), (128, 128), (300, 130), (1, 0), (1, 1), (40, 1000)])
+def test_pages_and_windows(page, window, sinks):
+    Case([70, 1, 4], [480, 611, 260], 3, 1, page, FP16 if page == 32 else BF16, "heads" if page > 64 else "tokens",
+         seed=page).check(window, sinks)
+
+
+@pytest.mark.parametrize("window,sinks", [(128, 4), (64, 0), (513, 16), (1, 0), (5000, 4)])
+def test_windows_over_a_long_prompt(window, sinks):
+    Case([1100], [1100], 2, 2, 64, seed=3).check(window, sinks)
+
+
+@pytest.mark.parametrize("kv", [9000, 20000])
+def test_one_long_cache(kv):
+    Case([1], [kv], 4, 1, 64, seed=kv).check()
+    Case([2], [kv], 4, 2, 128, FP16, seed=kv).check(window=4096, sinks=4)
+    Case([3], [kv], 8, 1, 16, seed=kv).check()
+
+
+def test_many_requests():
+    r = np.random.default_rng(5)
+    kv = r.integers(1, 500, 300)
+    new = [int(min(n, r.choice([1, 1, 1, 2, 4]))) for n in kv]
+    Case(new, kv.tolist(), 4, 2, 32, seed=5).check()
+    Case(new, kv.tolist(), 4, 2, 32, seed=5).check(window=64, sinks=4)
+
+
+def test_more_requests_than_a_block_counts():
+    n = 3000
+    Case([1] * n, [1 + i % 37 for i in range(n)], 1, 1, 16, seed=6).check()
+
+
+@pytest.mark.parametrize("gain", [8.0, 40.0])
+def test_sharp_scores(gain):
+    """Rows whose maximum grows from tile to tile, and rows with one weight."""
+    c = Case([3, 140], [900, 400], 2, 1, 64, seed=9, gain=gain)
+    for b in range(2):
+        for j, (page, row) in enumerate(c.rows(b)):
+            c.k[page, row] *= 0.2 + j / 400
+    # scores reach a few hundred here: the 32-bit bound scales with them
+    out, lse = c.run()
+    want, want_lse, weight = paged.attention(_np(c.q), _np(c.k), _np(c.v), c.cu, c.kv, c.table, c.scale)
+    reach = float(np.abs(_np(c.q)).sum(-1).max() * np.abs(_np(c.k)).max() * c.scale)
+    eps = 128 * 2.0 ** -24 * reach
+    u = 2.0 ** -8
+    assert (np.abs(_np(out) - want) <= u * np.abs(want) + (u + 2 * eps) * weight * (1 + u) + 1e-30).all()
+    assert (np.abs(_np(lse) - want_lse) <= eps + 2.0 ** -22 * np.abs(want_lse)).all()
+
+
+# --- rows that see nothing, hidden places ------------------------------------------
+
+def test_rows_before_the_cache_begins():
+    """More tokens than cached ones: the first stand before position 0."""
+    Case([5, 200, 3], [2, 130, 0], 2, 1, 16, seed=11).check()
+    Case([300], [1], 4, 2, 64, FP16, seed=12).check(window=7, sinks=2)
+
+
+@pytest.mark.parametrize("poison", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (90, 3)])
+def test_hidden_places_have_no_influence(poison, page, window, sinks):
+    c = Case([3, 140, 1], [50, 300, 413], 2, 1, page, seed=13)
+    clean_k, clean_v = c.k.clone(), c.v.clone()
+    used = torch.zeros(c.k.shape[:2], dtype=torch.bool, device="cuda")
+    for b in range(3):
+        for j, (pg, row) in enumerate(c.rows(b)):
+            first = c.kv[b] - c.new[b]
+            lo = first + 1 - window if window else 0
+            used[pg, row] = j >= lo or j < sinks
+    c.k[~used], c.v[~used] = poison, poison
+    c.check(window, sinks, k=clean_k, v=clean_v)
+
+
+@pytest.mark.parametrize("poison", [float("nan"), float("inf")])
+def test_a_poisoned_token_reaches_the_rows_that_see_it_alone(poison):
+    """The chunk's own tokens: key and value of one of them are not finite."""
+    c = Case([200, 1], [260, 40], 2, 1, 32, seed=14)
+    at = 60 + 77  # position of token 77
+    pg, row = c.rows(0)[at]
+    clean = c.k.clone(), c.v.clone()
+    c.v[pg, row, 0, 5] = poison
+    out, lse = c.run()
+    c.check(result=(out, lse), rows=slice(0, 77), k=clean[0], v=clean[1])
+    c.check(result=(out, lse), rows=slice(200, 201), k=clean[0], v=clean[1])
+    assert not torch.isfinite(out[77:200, :, 5]).any() and torch.isfinite(lse[77:]).all()
+    assert torch.isfinite(out[77:200, :, :5]).all() and torch.isfinite(out[77:200, :, 6:]).all()
+    c.k[pg, row, 0, 9] = float("nan")
+    out, lse = c.run()
+    c.check(result=(out, lse), rows=slice(0, 77), k=clean[0], v=clean[1])
+    assert torch.isnan(out[77:200]).all() and torch.isnan(lse[77:200]).all()
+    c.k[pg, row, 0, 9] = clean[0][pg, row, 0, 9]
+    # out of a window that begins after it, but inside its tile
+    out, lse = c.run(window=30)
+    seen = list(range(77)) + list(range(107, 201))
+    c.check(window=30, result=(out, lse), rows=seen, k=clean[0], v=clean[1])
+
+
+@pytest.mark.parametrize("page", [16, 128])
+def test_pages_given_up_are_hidden(page):
+    """Negative entries: pages that left a window, or were never there."""
+    c = Case([2, 150], [700, 700], 2, 1, page, seed=15)
+    for col in (0, 2, 3):
+        c.table[0][col] = -1
+    c.table[1][1] = -5
+    c.check()
+    c.table[0] = [-1] * len(c.table[0])
+    c.check()
+    c.check(window=200, sinks=4)
+
+
+def test_pages_past_the_cache_are_hidden_and_reported():
+    c = Case([2, 1], [300, 40], 2, 1, 64, seed=16)
+    n = c.k.shape[0]
+    c.table[0][1], c.table[0][3] = n, 2**31 - 1
+    result = c.run()
+    assert kda.kda_device_status(clear=True) == INDEX
+    c.check(result=result)
+    # out of sight they are not met
+    c = Case([2, 1], [300, 40], 2, 1, 64, seed=16)
+    c.table[0][0] = c.table[0][1] = n
+    c.check(window=100)
+    c.table[0][5] = n  # past the request's tokens
+    c.check(window=100)
+
+
+def test_lengths_outside_the_table():
+    c = Case([2, 1, 1], [300, 40, 17], 2, 1, 64, seed=17, cols=5)
+    real = list(c.kv)
+    out, lse = kda.kda_paged_attention(kda.KvCache(c.k, c.v), c.q, _i32(c.cu), _i32([321, 40, -4]), _i32(c.table),
+                                       return_lse=True)
+    assert kda.kda_device_status(clear=True) == INDEX
+    c.check(result=(out, lse), rows=[2], kv=real)
+    assert not out[3].any() and torch.isneginf(lse[3]).all()
+    # clamped to the table's 5 pages
+    c.kv = [320, 40, 17]
+    c.check(result=(out, lse), rows=[0, 1, 2])
+
+
+@pytest.mark.parametrize("cu", [[0, 2, 1, 4], [0, 2, 3, 5], [-1, 2, 3, 4], [0, 9, 3, 4]])
+def test_bad_row_starts(cu):
+    c = Case([2, 1, 1], [300, 40, 17], 2, 1, 64, seed=18)
+    out = torch.full((6, 2, 128), 7.0, dtype=BF16, device="cuda")
+    kda.kda_paged_attention(kda.KvCache(c.k, c.v), c.q, _i32(cu), _i32(c.kv), _i32(c.table), out=out[:4])
+    assert kda.kda_device_status(clear=True) == INDEX
+    assert (out[4:] == 7).all() and torch.isfinite(out).all()
+
+
+def test_rows_of_no_request_and_guards():
+    c = Case([2, 130, 4], [300, 140, 17], 2, 1, 64, seed=19)
+    full = torch.full((136 + 9, 2, 128), 7.0, dtype=BF16, device="cuda")
+    lse = torch.full((136 + 9, 2), 7.0, device="cuda")
+    table = torch.full((3, 9), 10**6, dtype=torch.int32, device="cuda")
+    table[:, :len(c.table[0])] = _i32(c.table)
+    kda.kda_paged_attention(kda.KvCache(c.k, c.v), c.q, _i32(c.cu[:3]), _i32(c.kv[:2]), table[:2, :len(c.table[0])],
+                            out=full[:136], lse=lse[:136])
+    assert (full[132:] == 7).all() and (lse[132:] == 7).all() and not (full[:132] == 7).all(-1).any()
+    c.check(result=(full[:136], lse[:136]), rows=slice(0, 132))
+
+
+# --- how it is called ----------------------------------------------------------------
+
+def test_one_workspace_for_calls_of_all_shapes_and_the_same_bits_twice():
+    ws = kda.paged_attention_workspace()
+    cases = [Case([1], [9000], 4, 1, 64, seed=20), Case([1] * 40, list(range(3, 1203, 30)), 8, 2, 16, seed=21),
+             Case([700, 1, 300], [900, 2000, 300], 2, 2, 64, FP16, seed=22), Case([3], [3], 1, 1, 16, seed=23)]
+    first = [c.run(workspace=ws) for c in cases]
+    again = [c.run(workspace=ws) for c in reversed(cases)][::-1]
+    alone = [c.run() for c in cases]
+    for c, a, b, d in zip(cases, first, again, alone):
+        c.check(result=a)
+        for x, y in ((a, b), (a, d)):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    assert not ws[:4096].any()
+
+
+def test_other_stream_and_graph():
+    c = Case([1, 2, 150], [800, 700, 300], 4, 2, 64, seed=24)
+    want = c.run()
+    cache, ws = kda.KvCache(c.k, c.v), kda.paged_attention_workspace()
+    cu, kv, table = _i32(c.cu), _i32(c.kv), _i32(c.table)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got, lse = kda.kda_paged_attention(cache, c.q, cu, kv, table, workspace=ws, return_lse=True, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want[0]) and torch.equal(lse, want[1])
+    out, lse = torch.empty_like(got), torch.empty_like(lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kda.kda_paged_attention(cache, c.q, cu, kv, table, workspace=ws, out=out, lse=lse)
+    for lens in ([800, 700, 300], [5, 700, 222], [800, 1, 150]):
+        kv.copy_(_i32(lens))
+        graph.replay()
+        torch.cuda.synchronize()
+        c.kv = lens
+        c.check(result=(out, lse))
+
+
+def test_a_cache_past_32_bit_offsets():
+    page, hkv = 256, 64
+    n_pages = (1 << 31) // (page * hkv * 128) + 4
+    k = torch.empty(n_pages, page, hkv, 128, dtype=BF16, device="cuda")
+    v = torch.empty_like(k)
+    small = Case([2, 1], [500, 300], hkv, hkv, page, seed=25)
+    used = sorted(p for row in small.table for p in row if p >= 0)
+    high = {p: n_pages - 1 - i for i, p in enumerate(used)}
+    for p, to in high.items():
+        k[to], v[to] = small.k[p], small.v[p]
+    out, lse = kda.kda_paged_attention(kda.KvCache(k, v), small.q, _i32(small.cu), _i32(small.kv),
+                                       _i32([[high.get(p, -1) for p in row] for row in small.table]), return_lse=True)
+    small.check(result=(out, lse))
+
+
+def test_refusals():
+    c = Case([2], [30], 2, 1, 16)
+    cache = kda.KvCache(c.k, c.v)
+    a = dict(q=c.q, cu_seqlens=_i32(c.cu), kv_lens=_i32(c.kv), block_table=_i32(c.table))
+    for over, error in [(dict(q=c.q.half()), TypeError), (dict(q=c.q[..., :64]), ValueError),
+                        (dict(cu_seqlens=_i32([0])), ValueError), (dict(kv_lens=_i32(c.kv).long()), TypeError),
+                        (dict(block_table=_i32(c.table + c.table)), ValueError),
+                        (dict(out=torch.empty(2, 2, 128, device="cuda")), ValueError),
+                        (dict(lse=torch.empty(2, 3, device="cuda")), ValueError), (dict(scale=0.0), ValueError),
+                        (dict(window=-1), ValueError), (dict(workspace=torch.zeros(64, dtype=torch.uint8, device="cuda")),
+                                                        ValueError)]:
+        args = {**a, **over}
+        with pytest.raises(error):
+            kda.kda_paged_attention(cache, args.pop("q"), args.pop("cu_seqlens"), args.pop("kv_lens"),
+                                    args.pop("block_table"), **args)
+    with pytest.raises(ValueError):
+        kda.kda_kv_append(cache, c.q[:, :1], c.q[:1, :1], _i32([0, 1]))
