@@ -576,7 +576,8 @@ int kda_kv_append(const kda_kv_cache* cache, const void* k, int64_t k_stride_tok
  * What is hidden has no influence, whatever it holds (NaN and infinities
  * included).  One call serves single tokens, short windows and prompt chunks
  * in any mix.
- *   q           [t_total, Hq, 128], strides as kda_kv_append's k
+ *   q           [t_total, Hq, 128], 16-byte aligned, token and head strides
+ *               multiples of 8 elements and >= 128
  *   out         [t_total, Hq, 128] contiguous, 16-byte aligned, written;
  *               tokens past cu_seqlens[n_req] are left alone
  *   lse         fp32 [t_total, Hq] or NULL, written

@@ -4,20 +4,180 @@
 //
 // For the token at position p, query head h and the visible keys j:
 //   s_j = scale <q, k_j>,  out = sum_j e^{s_j} v_j / sum_j e^{s_j},
-// formed in one pass over the keys with the running maximum m of s, the sum
-// l = sum e^{s_j - m} and the accumulator o = sum e^{s_j - m} v_j, both
-// multiplied by e^{m_old - m_new} when the maximum grows.
+// formed in one pass over the keys with a running reference m of s, the sum
+// l = sum e^{s_j - m} and the accumulator o = sum e^{s_j - m} v_j.
+//
+// Tiles.  The query heads of one key head share every key, so a tile's 128
+// rows are (token, head of the group) pairs: 128 / G tokens by G heads.  A
+// block is two such tiles.  Keys come in tiles of 128, K and V 32 KB each.
+// Per key tile the tensor cores form S = Q K^T (128 x 128 x 128) and
+// O += P V (128 x 128 x 128); S, P and O live in tensor memory (S and P share
+// columns), Q, K and V in shared memory as the copies left them.
+//
+// Warps.  Two softmax warpgroups (one thread a row), each with an S/P and an O
+// of its own: while one of them works on its S, the tensor cores serve the
+// other.  One warp copies (TMA: a box per page and half row), one issues the
+// matrix products, one lays out the work.  A block of one tile (single tokens,
+// short windows) gives both warpgroups the same rows and every other key tile;
+// their two results are joined in shared memory.
+//
+// Work.  The (key head, block) pairs in a row, each as long as its key tiles,
+// form one line that is cut into equal pieces, one per CTA.  A pair that a cut
+// divides leaves partial results (o, m, l) in the workspace; the CTA that
+// finishes the pair last joins them in the order of the line, so results do not depend on timing.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <math_constants.h>
 
 #include "kda_kv.cuh"
+#include "kda_tc.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int ROW_THREADS = 256;
+constexpr int KT = 128;        // keys per tile
+constexpr int ROWS = 128;      // rows per query tile
+constexpr int STAGES = 5;      // K or V tiles in shared memory
+constexpr int TILE_BYTES = KT * D * 2;
+constexpr int HALF_BYTES = TILE_BYTES / 2;  // 64 of the 128 dimensions
+constexpr int RING = 4;        // items ahead
+constexpr int MASKS = 8;       // page masks of the K tiles in flight
+constexpr int THREADS = 384;
+constexpr int LOAD_WARP = 8, MMA_WARP = 9, PLAN_WARP = 10;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+// The running reference follows the row's maximum only when that has grown by
+// 2^GROWTH: until then weights up to 2^GROWTH stand in for ones, and the
+// accumulator is left alone.
+constexpr float GROWTH = 8.f;
+// fp16 weights are formed 2^7 larger: at most 2^15 with GROWTH, and the
+// smallest normal one (2^-14) is then 2^-21 of the reference.
+template <bool FP16>
+constexpr float WEIGHT_EXP = FP16 ? 7.f : 0.f;
 
-// One row (token, query head) by one warp, four of the 128 dimensions a lane.
-// first, kv: the request's position of its first token and its cached tokens.
+struct Item {
+  int b, kvh;
+  int tok, n_tok;      // first packed token, tokens of the block
+  int pos, kv;         // position of the first token, cached tokens
+  int i0, i1;          // this part's range of the key tile list
+  int n_sink, t_lo;    // list: tiles 0 .. n_sink - 1, then t_lo, t_lo + 1, ..
+  int lo, hi, sink_hi; // keys that some row sees: [lo, hi) and [0, sink_hi)
+  int first, parts;    // CTA of the first part, parts of the pair
+  int part;            // this part's number; < 0 in place of b ends the work
+};
+
+struct Smem {
+  uint64_t kv_full[STAGES], kv_empty[STAGES];
+  uint64_t ring_full[RING], ring_empty[RING];
+  uint64_t q_full, q_empty, merge_full;
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t drained;
+  Item ring[RING];
+  int page_mask[MASKS];
+  float2 merge_ml[ROWS];
+  long long sums[THREADS / 32];
+  long long total;
+  int start_b;
+  long long start_before;
+  uint32_t tmem;
+  int dead;
+  int last[2];
+};
+
+struct Params {
+  AttentionParams a;
+  int group, tile_tok;     // G, tokens per query tile
+  int n_cta;
+  int min_piece;           // least tiles per CTA
+  int boxes;               // pages per key tile (1 when a page holds more)
+  unsigned* counters;      // [n_cta][2], zero between calls
+  float2* part_ml;         // [n_cta][2 slots][2 tiles][ROWS]
+  float4* part_o;          // [n_cta][2 slots][2 tiles][ROWS][32]
+};
+
+// --- waits ---------------------------------------------------------------------
+// A wait that expires marks the CTA: from then on every wait of it returns at
+// once, and the roles run out.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* dead, unsigned* err) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0; i < WAIT_CAP; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*dead) return false;
+    const uint64_t t = globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    else if (t - t0 > WAIT_NS) break;
+  }
+  *dead = 1;
+  set_error(err, ERR_TIMEOUT);
+  return false;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Smem& sm, unsigned* err) {
+  if (mbar_test_wait(bar, parity)) return true;
+  return wait_slow(bar, parity, &sm.dead, err);
+}
+// by a whole warp, which runs warp-wide instructions next
+__device__ __forceinline__ void warp_wait(uint64_t* bar, uint32_t parity, Smem& sm, unsigned* err) {
+  wait(bar, parity, sm, err);
+  __syncwarp();
+}
+
+// --- PTX -----------------------------------------------------------------------
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)) : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem], B MN-major
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      "}\n" ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+// 128-byte-swizzled MN-major operand as the copies leave it: 64 dimensions (128
+// bytes) a row, 8-row groups 1024 bytes apart, the other 64 dimensions
+// HALF_BYTES further.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(HALF_BYTES >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// --- one row, by one warp ----------------------------------------------------------
+// The definition row by row, four of the 128 dimensions a lane.  The tiles'
+// products multiply the values of hidden keys by a weight of 0, which is not 0
+// where such a value is NaN or infinite: a row whose tiled result is not finite
+// is formed again here from the keys that it sees alone.
 template <bool FP16>
 __device__ __forceinline__ void attend_row(const AttentionParams& p, int b, int tok, int head, int pos, int kv) {
   const int lane = threadIdx.x & 31;
@@ -28,17 +188,18 @@ __device__ __forceinline__ void attend_row(const AttentionParams& p, int b, int 
   const int32_t* table = p.table + (int64_t)b * p.table_stride;
   const __nv_bfloat16* kc = p.kc + (int64_t)kvh * p.kc_sh + lane * 4;
   const __nv_bfloat16* vc = p.vc + (int64_t)kvh * p.vc_sh + lane * 4;
+#pragma unroll 1
   for (int part = 0; part < 2; ++part) {
-    const int end = part == 0 ? min(p.sinks, lo) : hi;
+    const int end = part == 0 ? min(min(p.sinks, lo), hi) : hi;
     int j = part == 0 ? 0 : lo;
     while (j < end) {
       const int stop = min(end, ((j >> p.page_shift) + 1) << p.page_shift);
       const int pg = table[j >> p.page_shift];
       if (pg < 0 || pg >= p.n_pages) {
-        if (pg >= 0) set_error(p.err, ERR_INDEX);
         j = stop;
         continue;
       }
+#pragma unroll 1
       for (; j < stop; ++j) {
         const int row = j & (page - 1);
         float k[4], v[4];
@@ -46,7 +207,7 @@ __device__ __forceinline__ void attend_row(const AttentionParams& p, int b, int 
         load_act4<FP16>(vc + pg * p.vc_sp + row * p.vc_st, v);
         const float s = p.scale * warp_sum(q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3]);
         const float top = fmaxf(m, s);
-        if (top == -CUDART_INF_F && !(s != s)) continue;  // e^s = 0, and no maximum yet
+        if (top == -CUDART_INF_F && s == s) continue;  // e^s = 0, and no maximum yet
         const float corr = m == -CUDART_INF_F ? 0.f : expf(m - top), w = expf(s - top);
         l = l * corr + w;
 #pragma unroll
@@ -61,55 +222,819 @@ __device__ __forceinline__ void attend_row(const AttentionParams& p, int b, int 
   if (p.lse && lane == 0) p.lse[(int64_t)tok * p.hq + head] = l == 0.f ? -CUDART_INF_F : m + logf(l);
 }
 
-// A request's tokens and lengths, checked; false: no tokens to run.
-__device__ __forceinline__ bool request(const AttentionParams& p, int b, int& t0, int& n, int& kv, bool report) {
+// --- the line of work ----------------------------------------------------------------
+// A request's tokens and lengths, checked; n = 0: no tokens to run.
+__device__ __forceinline__ void request(const AttentionParams& p, int b, int& t0, int& n, int& kv, bool report) {
   t0 = p.cu_seqlens[b];
   const int t1 = p.cu_seqlens[b + 1];
   const int most = p.table_cols << p.page_shift;
   kv = p.kv_lens[b];
+  n = t1 - t0;
   if (t0 < 0 || t1 < t0 || t1 > p.t_total) {
     if (report) set_error(p.err, ERR_INDEX);
-    return false;
+    n = 0;
   }
-  n = t1 - t0;
   if (kv < 0 || kv > most) {
     if (report) set_error(p.err, ERR_INDEX);
     kv = kv < 0 ? 0 : most;
   }
-  return n > 0;
+}
+
+// Key tiles of block k of a request of n tokens: fills the item's list.
+__device__ __forceinline__ int block_tiles(const Params& p, int n, int kv, int k, Item& it) {
+  const int tok = k * 2 * p.tile_tok;
+  it.n_tok = min(2 * p.tile_tok, n - tok);
+  it.pos = kv - n + tok;
+  it.hi = max(0, min(it.pos + it.n_tok, kv));
+  it.lo = p.a.window ? max(0, it.pos + 1 - p.a.window) : 0;
+  it.sink_hi = min(min(p.a.sinks, it.lo), it.hi);
+  it.t_lo = it.lo / KT;
+  it.n_sink = min((it.sink_hi + KT - 1) / KT, it.t_lo);
+  return it.n_sink + (it.hi > it.lo ? (it.hi + KT - 1) / KT - it.t_lo : 0);
+}
+__device__ __forceinline__ int block_cost(const Params& p, int n, int kv, int k) {
+  Item it;
+  return max(1, block_tiles(p, n, kv, k, it));
+}
+__device__ __forceinline__ int n_blocks(const Params& p, int n) { return (n + 2 * p.tile_tok - 1) / (2 * p.tile_tok); }
+
+// Sum of the costs of a request's blocks; the lanes of a warp share long ones.
+__device__ __forceinline__ long long request_cost(const Params& p, int b, bool valid, bool report) {
+  const int lane = threadIdx.x & 31;
+  int t0 = 0, n = 0, kv = 0;
+  if (valid) request(p.a, b, t0, n, kv, report);
+  const int blocks = n_blocks(p, n);
+  long long cost = 0;
+  if (blocks <= 4)
+    for (int k = 0; k < blocks; ++k) cost += block_cost(p, n, kv, k);
+  unsigned big = __ballot_sync(0xffffffffu, blocks > 4);
+  while (big) {
+    const int src = __ffs(big) - 1;
+    big &= big - 1;
+    const int n_s = __shfl_sync(0xffffffffu, n, src), kv_s = __shfl_sync(0xffffffffu, kv, src);
+    const int blocks_s = __shfl_sync(0xffffffffu, blocks, src);
+    long long sum = 0;
+    for (int k = lane; k < blocks_s; k += 32) sum += block_cost(p, n_s, kv_s, k);
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    if (lane == src) cost = sum;
+  }
+  return cost;
+}
+
+// --- the copying warp ------------------------------------------------------------------
+struct Maps {
+  CUtensorMap k, v, q, q1;  // q: a tile's tokens in a box, q1: one token
+};
+
+__device__ __forceinline__ int list_tile(const Item& it, int i) { return i < it.n_sink ? i : it.t_lo + i - it.n_sink; }
+
+// whether query tile s of a block in two tiles sees anything of key tile t
+__device__ __forceinline__ bool tile_active(const Params& p, const Item& it, int s, int t) {
+  const int first = it.pos + s * p.tile_tok, last = min(it.pos + it.n_tok, first + p.tile_tok);
+  const int hi = min(last, it.kv), lo = p.a.window ? first + 1 - p.a.window : 0;
+  return t * KT < hi && (t * KT + KT > lo || t * KT < p.a.sinks);
+}
+
+__device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Smem& sm, unsigned char* q_smem, unsigned char* kv_smem) {
+  const int lane = threadIdx.x & 31;
+  unsigned* err = p.a.err;
+  uint32_t fills = 0, tiles = 0, q_count = 0;
+  bool ok = true;
+  for (uint32_t items = 0; ok; ++items) {
+    const uint32_t slot = items % RING;
+    if (!wait(&sm.ring_full[slot], (items / RING) & 1, sm, err)) ok = false;
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    const Item it = sm.ring[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.ring_empty[slot]);
+    if (it.b < 0) break;
+    if (it.i1 == it.i0) continue;
+    const int32_t* table = p.a.table + (int64_t)it.b * p.a.table_stride;
+    const int page = 1 << p.a.page_shift, box = min(page, KT);
+    // Page of lane's box of key tile t; >= n_pages (the copy then fills with zeros) for a hidden one.
+    auto page_of = [&](int i) {
+      if (lane >= p.boxes || i >= it.i1) return -1;
+      const int key = list_tile(it, i) * KT + lane * box;
+      if (key >= it.kv) return -1;
+      const int pg = table[key >> p.a.page_shift];
+      if (pg >= p.a.n_pages) {
+        const int end = key + box;
+        if ((key < it.hi && end > it.lo) || key < it.sink_hi) set_error(err, ERR_INDEX);
+        return -1;
+      }
+      return pg < 0 ? -1 : pg;
+    };
+    int pg = page_of(it.i0);
+    // queries
+    const bool two = it.n_tok > p.tile_tok;
+    if (lane == 0 && !wait(&sm.q_empty, (q_count & 1) ^ 1, sm, err)) ok = false;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (!ok) break;
+    ++q_count;
+    const bool single = it.n_tok <= 8;
+    const uint32_t box_bytes = (uint32_t)p.group * 128u;
+    if (lane == 0)
+      mbar_arrive_expect_tx(&sm.q_full, single ? 2u * it.n_tok * box_bytes : (two ? 4u : 2u) * p.tile_tok * box_bytes);
+    __syncwarp();
+    if (single) {
+      // the swizzle goes by the shared-memory address, so a box may begin at any row of an 8-row group
+      if (lane < 2 * it.n_tok) {
+        const int i = lane >> 1, half = lane & 1, s = i / p.tile_tok, r = (i % p.tile_tok) * p.group;
+        tma_load4(q_smem + s * TILE_BYTES + half * HALF_BYTES + r * 128, &maps.q1, half * 64, 0, it.kvh, it.tok + i, &sm.q_full);
+      }
+    } else if (lane < (two ? 4 : 2)) {
+      const int s = lane >> 1, half = lane & 1;
+      tma_load4(q_smem + s * TILE_BYTES + half * HALF_BYTES, &maps.q, half * 64, 0, it.kvh, it.tok + s * p.tile_tok, &sm.q_full);
+    }
+    // keys and values
+    for (int i = it.i0; i < it.i1; ++i, ++tiles) {
+      const int row = (list_tile(it, i) * KT) & (page - 1) & ~(box - 1);
+      const int c_page = pg < 0 ? p.a.n_pages : pg;
+      const unsigned held = __ballot_sync(0xffffffffu, pg >= 0);
+      pg = page_of(i + 1);
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv, ++fills) {
+        const uint32_t st = fills % STAGES;
+        if (lane == 0 && !wait(&sm.kv_empty[st], ((fills / STAGES) & 1) ^ 1, sm, err)) ok = false;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (lane == 0) {
+          if (kv == 0) *(volatile int*)&sm.page_mask[tiles % MASKS] = (int)held;
+          mbar_arrive_expect_tx(&sm.kv_full[st], TILE_BYTES);
+        }
+        __syncwarp();
+        if (lane < p.boxes) {
+          unsigned char* dst = kv_smem + st * TILE_BYTES + lane * box * 128;
+          const CUtensorMap* map = kv == 0 ? &maps.k : &maps.v;
+          tma_load4(dst, map, 0, row, it.kvh, c_page, &sm.kv_full[st]);
+          tma_load4(dst + HALF_BYTES, map, 64, row, it.kvh, c_page, &sm.kv_full[st]);
+        }
+      }
+      if (!ok) break;
+    }
+  }
+  if (!ok && lane == 0) {
+    // copies in flight land before the CTA ends
+    for (uint32_t f = fills > STAGES ? fills - STAGES : 0; f < fills; ++f)
+      mbar_wait_bounded(&sm.kv_full[f % STAGES], (f / STAGES) & 1, err);
+    if (q_count > 0) mbar_wait_bounded(&sm.q_full, (q_count - 1) & 1, err);
+  }
+}
+
+// --- the issuing thread ------------------------------------------------------------------
+struct Step {
+  int s;            // stream
+  uint32_t v_stage, v_parity;
+  bool release_v, first, last;
+};
+
+__device__ __forceinline__ void mma_role(const Params& p, Smem& sm, uint32_t q_addr, uint32_t kv_addr, uint32_t tmem, uint32_t bf16) {
+  unsigned* err = p.a.err;
+  const uint32_t id_qk = tc::idesc_f16(ROWS, KT, bf16), id_pv = tc::idesc_f16(ROWS, D, bf16) | (1u << 16);
+  uint32_t fills = 0, q_count = 0;
+  uint32_t p_count[2] = {0, 0}, o_count[2] = {0, 0};
+  bool ok = true;
+  auto pv = [&](const Step& x) {
+    ok = ok && wait(&sm.kv_full[x.v_stage], x.v_parity, sm, err);
+    ok = ok && wait(&sm.p_full[x.s], p_count[x.s] & 1, sm, err);
+    ++p_count[x.s];
+    if (x.first) {
+      ok = ok && wait(&sm.o_free[x.s], (o_count[x.s] & 1) ^ 1, sm, err);
+      ++o_count[x.s];
+    }
+    if (!ok) return;
+    tc::fence_after_sync();
+    const uint32_t d = tmem + 256 + x.s * 128, a = tmem + x.s * 128;
+    const uint64_t vd = smem_desc_mn(kv_addr + x.v_stage * TILE_BYTES);
+#pragma unroll
+    for (int j = 0; j < KT / 16; ++j)  // 16 keys: two 8-row groups of V
+      mma_f16_ts(d, a + j * 8, vd + j * (2048 >> 4), id_pv, (j > 0 || !x.first) ? 1u : 0u);
+    if (x.release_v) tc::mma_commit(&sm.kv_empty[x.v_stage]);
+    if (x.last) tc::mma_commit(&sm.o_full[x.s]);
+  };
+  for (uint32_t items = 0; ok; ++items) {
+    const uint32_t slot = items % RING;
+    if (!wait(&sm.ring_full[slot], (items / RING) & 1, sm, err)) break;
+    const Item it = sm.ring[slot];
+    mbar_arrive(&sm.ring_empty[slot]);
+    if (it.b < 0) break;
+    if (it.i1 == it.i0) continue;
+    const bool two = it.n_tok > p.tile_tok;
+    int last_of[2] = {-1, -1};  // last list index of each stream
+    for (int s = 0; s < 2; ++s) {
+      if (!two) {
+        last_of[s] = it.i1 - 1 - ((it.i1 - 1 - it.i0 - s) & 1);
+        if (last_of[s] < it.i0) last_of[s] = -1;
+      } else {
+        for (int i = it.i1 - 1; i >= it.i0; --i)
+          if (tile_active(p, it, s, list_tile(it, i))) {
+            last_of[s] = i;
+            break;
+          }
+      }
+    }
+    ok = ok && wait(&sm.q_full, q_count & 1, sm, err);
+    ++q_count;
+    bool seen[2] = {false, false};
+    bool pending = false;
+    Step prev;
+    for (int i = it.i0; i < it.i1 && ok; ++i) {
+      const int t = list_tile(it, i);
+      const uint32_t ks = fills % STAGES, kp = (fills / STAGES) & 1;
+      const uint32_t vs = (fills + 1) % STAGES, vp = ((fills + 1) / STAGES) & 1;
+      fills += 2;
+      const bool act0 = two ? tile_active(p, it, 0, t) : ((i - it.i0) & 1) == 0;
+      const bool act1 = two ? tile_active(p, it, 1, t) : !act0;
+      ok = ok && wait(&sm.kv_full[ks], kp, sm, err);
+      tc::fence_after_sync();
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (!(s ? act1 : act0) || !ok) continue;
+        if (pending && prev.s == s) {  // S shares its columns with the weights of that step
+          pv(prev);
+          pending = false;
+        }
+        const uint32_t d = tmem + s * 128;
+        const uint64_t qd = tc::smem_desc_sw128(q_addr + (two ? s * TILE_BYTES : 0));
+        const uint64_t kd = tc::smem_desc_sw128(kv_addr + ks * TILE_BYTES);
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          const uint32_t off = ((j >> 2) * HALF_BYTES + (j & 3) * 32) >> 4;
+          tc::mma_f16(d, qd + off, kd + off, id_qk, j > 0 ? 1u : 0u);
+        }
+        tc::mma_commit(&sm.s_full[s]);
+        if (s == 1 || !act1) tc::mma_commit(&sm.kv_empty[ks]);
+        if (pending) pv(prev);
+        prev = {s, vs, vp, s == 1 || !act1, !seen[s], i == last_of[s]};
+        seen[s] = true;
+        pending = true;
+      }
+      if (!act0 && !act1) {  // no row of either tile sees it
+        ok = ok && wait(&sm.kv_full[vs], vp, sm, err);
+        mbar_arrive(&sm.kv_empty[ks]);
+        mbar_arrive(&sm.kv_empty[vs]);
+      }
+    }
+    // the queries' buffer: free once the products have read it, or, for a block
+    // of one tile, once the two results have been joined in it
+    if (two) tc::mma_commit(&sm.q_empty);
+    if (pending && ok) pv(prev);
+  }
+  // every product has ended before tensor memory is freed
+  tc::mma_commit(&sm.drained);
+  mbar_wait_bounded(&sm.drained, 0, err);
+}
+
+// --- the planning warp -----------------------------------------------------------------
+__device__ __forceinline__ void plan_role(const Params& p, Smem& sm, int cta, long long piece) {
+  const int lane = threadIdx.x & 31;
+  unsigned* err = p.a.err;
+  const long long total = sm.total, all = total * p.a.hkv;
+  const long long u0 = cta * piece, u1 = min(all, u0 + piece);
+  uint32_t items = 0;
+  bool ok = true;
+  auto post = [&](const Item& it) {
+    const uint32_t slot = items % RING;
+    if (lane == 0) {
+      ok = wait(&sm.ring_empty[slot], ((items / RING) & 1) ^ 1, sm, err);
+      if (ok) {
+        sm.ring[slot] = it;
+        mbar_arrive(&sm.ring_full[slot]);
+      }
+    }
+    ++items;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+  };
+  if (u0 < u1) {
+    int h = (int)(u0 / total), b = sm.start_b;
+    long long at = h * total + sm.start_before;  // of request b's first block
+    while (ok && at < u1) {
+      int t0, n, kv;
+      request(p.a, b, t0, n, kv, false);
+      const int blocks = n_blocks(p, n);
+      for (int k0 = 0; ok && k0 < blocks && at < u1; k0 += 32) {
+        long long upto = k0 + lane < blocks ? block_cost(p, n, kv, k0 + lane) : 0;
+        const long long mine = upto;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+          const long long x = __shfl_up_sync(0xffffffffu, upto, m);
+          if (lane >= m) upto += x;
+        }
+        const long long begin = at + upto - mine;
+        unsigned todo = __ballot_sync(0xffffffffu, mine > 0 && begin < u1 && begin + mine > u0);
+        while (ok && todo) {
+          const int src = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const long long s = __shfl_sync(0xffffffffu, begin, src);
+          Item it;
+          const int k = k0 + src, tiles = block_tiles(p, n, kv, k, it);
+          const long long e = s + max(1, tiles);
+          it.b = b;
+          it.kvh = h;
+          it.tok = t0 + k * 2 * p.tile_tok;
+          it.kv = kv;
+          it.i0 = (int)max(0LL, u0 - s);
+          it.i1 = (int)min((long long)tiles, u1 - s);
+          it.first = (int)(s / piece);
+          it.parts = (int)((e - 1) / piece) - it.first + 1;
+          it.part = cta - it.first;
+          post(it);
+        }
+        at += __shfl_sync(0xffffffffu, upto, 31);
+      }
+      if (++b == p.a.n_req) {
+        b = 0;
+        ++h;
+      }
+    }
+  }
+  Item end;
+  end.b = -1;
+  if (ok) post(end);
+}
+
+// Costs of all requests: the line's length, and the request in which this CTA's
+// piece begins.
+__device__ __forceinline__ long long measure_line(const Params& p, Smem& sm, int cta) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int each = (p.a.n_req + THREADS - 1) / THREADS;
+  long long cost = 0;
+  for (int j = 0; j < each; ++j) cost += request_cost(p, t * each + j, t * each + j < p.a.n_req, cta == 0);
+  long long upto = cost;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, upto, m);
+    if (lane >= m) upto += x;
+  }
+  if (lane == 31) sm.sums[warp] = upto;
+  __syncthreads();
+  long long total = 0;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) upto += sm.sums[w];
+    total += sm.sums[w];
+  }
+  const long long all = total * p.a.hkv;
+  const long long piece = max((all + p.n_cta - 1) / p.n_cta, (long long)p.min_piece);
+  const long long u0 = cta * piece;
+  if (u0 < all) {
+    const long long w0 = u0 % total;
+    long long before = upto - cost;
+    const bool mine = before <= w0 && w0 < upto;
+    if (__any_sync(0xffffffffu, mine)) {
+      bool found = false;
+      for (int j = 0; j < each; ++j) {
+        const long long c = request_cost(p, t * each + j, t * each + j < p.a.n_req, false);
+        if (mine && !found && w0 < before + c) {
+          found = true;
+          sm.start_b = t * each + j;
+          sm.start_before = before;
+        }
+        before += c;
+      }
+    }
+  }
+  if (t == 0) sm.total = total;
+  return piece;
+}
+
+// --- a softmax warpgroup -----------------------------------------------------------------
+__device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+template <bool FP16>
+__device__ __forceinline__ void join_parts(const Params& p, const Item& it, int tile, int n_rows) {
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  for (int row = warp; row < n_rows; row += 4) {
+    const int i = tile * p.tile_tok + row / p.group, head = it.kvh * p.group + row % p.group;
+    auto part_at = [&](int k) { return (((size_t)(it.first + k) * 2 + (k == 0 ? 1 : 0)) * 2 + tile) * ROWS + row; };
+    float top = -CUDART_INF_F;
+    for (int k = lane; k < it.parts; k += 32) top = fmaxf(top, __ldcg(&p.part_ml[part_at(k)]).x);
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < it.parts; ++k) {
+      const float2 ml = __ldcg(&p.part_ml[part_at(k)]);
+      const float4 x = __ldcg(&p.part_o[part_at(k) * 32 + lane]);
+      if (ml.x == -CUDART_INF_F) continue;  // nothing seen, nothing stored
+      const float w = ex2(ml.x - top);
+      l += w * ml.y;
+      o.x += w * x.x;
+      o.y += w * x.y;
+      o.z += w * x.z;
+      o.w += w * x.w;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    o.x *= inv;
+    o.y *= inv;
+    o.z *= inv;
+    o.w *= inv;
+    const int tok = it.tok + i;
+    const float zero = (o.x + o.y + o.z + o.w) * 0.f;  // NaN when one is not finite
+    if (__any_sync(0xffffffffu, zero != 0.f)) {
+      attend_row<FP16>(p.a, it.b, tok, head, it.pos + i, it.kv);
+      continue;
+    }
+    __nv_bfloat16* out = p.a.out + ((int64_t)tok * p.a.hq + head) * D + lane * 4;
+    *reinterpret_cast<uint2*>(out) = make_uint2(act_pack2<FP16>(o.x, o.y), act_pack2<FP16>(o.z, o.w));
+    if (p.a.lse && lane == 0)
+      p.a.lse[(int64_t)tok * p.a.hq + head] = l == 0.f ? -CUDART_INF_F : (top + log2f(l) - WEIGHT_EXP<FP16>) * LN2;
+  }
 }
 
 template <bool FP16>
-__global__ void __launch_bounds__(ROW_THREADS) attention_rows_kernel(AttentionParams p) {
-  const int b = blockIdx.y;
-  int t0, n, kv;
-  if (!request(p, b, t0, n, kv, blockIdx.x == 0 && threadIdx.x == 0)) return;
-  const int64_t rows = (int64_t)n * p.hq;
-  for (int64_t r = (int64_t)blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5); r < rows;
-       r += (int64_t)gridDim.x * (ROW_THREADS / 32)) {
-    const int i = (int)(r / p.hq), head = (int)(r % p.hq);
-    attend_row<FP16>(p, b, t0 + i, head, kv - n + i, kv);
+__device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, unsigned char* q_smem, unsigned char* kv_smem,
+                                             uint32_t tmem) {
+  unsigned* err = p.a.err;
+  const int r = threadIdx.x & 127, lane = r & 31, bar = 1 + s;
+  const uint32_t lane_base = tmem + ((uint32_t)(r & 96) << 16);
+  const uint32_t t_s = lane_base + s * 128, t_o = lane_base + 256 + s * 128;
+  const int row_tok = r / p.group, row_head = r % p.group;
+  const float sl = p.a.scale * LOG2E;
+  const int all_held = (1 << p.boxes) - 1;
+  const int box_shift = p.a.page_shift < 7 ? p.a.page_shift : 7;
+  uint32_t fills = 0, tiles = 0, s_count = 0, o_count = 0, merges = 0;
+  for (uint32_t items = 0;; ++items) {
+    const uint32_t slot = items % RING;
+    const bool got = wait(&sm.ring_full[slot], (items / RING) & 1, sm, err);
+    if (named_bar_or(bar, 128, !got)) break;
+    const Item& it = sm.ring[slot];
+    if (it.b < 0) break;
+    const bool two = it.n_tok > p.tile_tok;
+    const int tile = two ? s : 0, i0 = it.i0, i1 = it.i1, kv = it.kv;
+    const int tb = tile * p.tile_tok + row_tok;
+    const bool valid = row_tok < p.tile_tok && tb < it.n_tok;
+    const int pos = it.pos + tb;
+    const int hi = valid ? max(0, min(pos + 1, kv)) : 0, lo = p.a.window ? max(0, pos + 1 - p.a.window) : 0;
+    const int sink = min(p.a.sinks, hi);
+    const bool any_row = __any_sync(0xffffffffu, valid);
+    const int hi_min = __reduce_min_sync(0xffffffffu, valid ? hi : 0x7fffffff);
+    const int lo_max = __reduce_max_sync(0xffffffffu, valid ? lo : 0);
+    const int sink_min = __reduce_min_sync(0xffffffffu, valid ? sink : 0x7fffffff);
+    float m = -CUDART_INF_F, l = 0.f;
+    bool stepped = false;
+    for (int i = two ? i0 : i0 + s; i < i1; i += two ? 1 : 2) {
+      const int t = list_tile(it, i), key = t * KT;
+      if (two && !tile_active(p, it, s, t)) continue;
+      warp_wait(&sm.s_full[s], s_count & 1, sm, err);
+      ++s_count;
+      tc::fence_after_sync();
+      if (any_row) {
+        uint32_t x[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::tmem_ld32_async(t_s + c * 32, x[c]);
+        const int held = *(volatile int*)&sm.page_mask[(tiles + i - i0) % MASKS];
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::tmem_regs(x[c]);
+        const bool whole = held == all_held && key + KT <= hi_min && (key >= lo_max || key + KT <= sink_min);
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int k0 = key + c * 32;
+            uint32_t seen = bits_below(hi - k0) & (~bits_below(lo - k0) | bits_below(sink - k0));
+            if (box_shift == 4)
+              seen &= ((held >> (2 * c)) & 1 ? 0xffffu : 0u) | ((held >> (2 * c + 1)) & 1 ? 0xffff0000u : 0u);
+            else if (!((held >> ((c * 32) >> box_shift)) & 1))
+              seen = 0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[c][j] = (seen >> j) & 1 ? x[c][j] : 0xff800000u;
+          }
+        }
+        float top[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          top[c] = __uint_as_float(x[c][0]);
+#pragma unroll
+          for (int j = 1; j < 32; ++j) top[c] = fmaxf(top[c], __uint_as_float(x[c][j]));
+        }
+        const float m_new = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), m);
+        // m = -inf: nothing seen yet, any first maximum is taken (-inf - -inf
+        // compares false).  Rows past the block hold anything and have no say.
+        if (__any_sync(0xffffffffu, valid && (m_new - m) * sl > GROWTH)) {
+          const float corr = m_new == -CUDART_INF_F ? 1.f : ex2((m - m_new) * sl);
+          m = m_new;
+          l *= corr;
+          if (stepped) {
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t y[16];
+              tc::tmem_ld16_async(t_o + c * 16, y);
+              tc::tmem_wait_ld();
+              tc::tmem_regs(y);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * corr);
+              tmem_st16(t_o + c * 16, y);
+            }
+          }
+        }
+        // weights 2^(s sl - m sl + e): one fma and one ex2 each
+        const float ref = WEIGHT_EXP<FP16> - (m == -CUDART_INF_F ? 0.f : m * sl);
+        const float2 sl2 = make_float2(sl, sl), ref2 = make_float2(ref, ref);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t w[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const uint32_t* src = &x[half * 2 + (j >> 4)][(j & 15) * 2];
+            const float2 e = ffma2(make_float2(__uint_as_float(src[0]), __uint_as_float(src[1])), sl2, ref2);
+            const float2 y = make_float2(ex2(e.x), ex2(e.y));
+            sum[j & 1] = fadd2(sum[j & 1], y);
+            w[j] = act_pack2<FP16>(y.x, y.y);
+          }
+          tmem_st32(t_s + half * 32, w);
+        }
+        sum[0] = fadd2(sum[0], sum[1]);
+        l += sum[0].x + sum[0].y;
+        tmem_wait_st();
+      }
+      if (key + KT > kv) {
+        // the tile's rows past the cached tokens hold whatever was there: zeros
+        // there keep the products finite
+        const uint32_t f = fills + 2 * (i - i0) + 1;
+        wait(&sm.kv_full[f % STAGES], (f / STAGES) & 1, sm, err);
+        unsigned char* v = kv_smem + (f % STAGES) * TILE_BYTES + (kv - key) * 128;
+        for (int c = r; c < (KT - (kv - key)) * 16; c += 128)
+          *reinterpret_cast<int4*>(v + ((c >> 3) & 1) * HALF_BYTES + (c >> 4) * 128 + (c & 7) * 16) = make_int4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+      }
+      stepped = true;
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.p_full[s]);
+    }
+    fills += 2 * (i1 - i0);
+    tiles += i1 - i0;
+    if (stepped) {
+      warp_wait(&sm.o_full[s], o_count & 1, sm, err);
+      ++o_count;
+      tc::fence_after_sync();
+    }
+    // m2: the reference in powers of two, -inf where the row has seen nothing
+    float m2 = l == 0.f ? -CUDART_INF_F : m * sl;
+    const bool merged = !two && i1 - i0 > 1;
+    if (!two && s == 1) {
+      if (merged) {
+        // rows of 512 bytes, their 16-byte pieces rotated by the row: no bank conflicts
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          tc::tmem_ld32(t_o + c * 32, v);
+          if (valid) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float4*>(q_smem + r * 512 + (((c * 8 + j) ^ lane) << 4)) =
+                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          }
+          __syncwarp();
+        }
+        sm.merge_ml[r] = make_float2(m2, l);
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.o_free[1]);
+          mbar_arrive(&sm.merge_full);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.ring_empty[slot]);
+      continue;
+    }
+    float w0 = 1.f, w1 = 0.f;
+    if (merged) {
+      warp_wait(&sm.merge_full, merges & 1, sm, err);
+      ++merges;
+      const float2 other = sm.merge_ml[r];
+      const float top = fmaxf(m2, other.x);
+      if (top == -CUDART_INF_F) {
+        l = 0.f;
+      } else {
+        w0 = m2 == -CUDART_INF_F ? 0.f : ex2(m2 - top);
+        w1 = other.x == -CUDART_INF_F ? 0.f : ex2(other.x - top);
+        l = l * w0 + other.y * w1;
+        m2 = top;
+      }
+    }
+    const bool whole_pair = it.parts == 1;
+    const int tok = it.tok + tb, head = it.kvh * p.group + row_head;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const size_t part_row = (((size_t)blockIdx.x * 2 + (it.part == 0 ? 1 : 0)) * 2 + tile) * ROWS + r;
+    float poison = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      float v[32];
+      if (stepped) {
+        tc::tmem_ld32(t_o + c * 32, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+      }
+      if (merged && valid) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float4 y = *reinterpret_cast<const float4*>(q_smem + r * 512 + (((c * 8 + j) ^ lane) << 4));
+          v[4 * j] = v[4 * j] * w0 + y.x * w1;
+          v[4 * j + 1] = v[4 * j + 1] * w0 + y.y * w1;
+          v[4 * j + 2] = v[4 * j + 2] * w0 + y.z * w1;
+          v[4 * j + 3] = v[4 * j + 3] * w0 + y.w * w1;
+        }
+      }
+      if (valid && whole_pair) {
+        int4* out = reinterpret_cast<int4*>(p.a.out + ((int64_t)tok * p.a.hq + head) * D + c * 32);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          v[j] *= inv;
+          poison += v[j] * 0.f;  // NaN from then on when one is not finite
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          out[j] = make_int4(act_pack2<FP16>(v[8 * j], v[8 * j + 1]), act_pack2<FP16>(v[8 * j + 2], v[8 * j + 3]),
+                             act_pack2<FP16>(v[8 * j + 4], v[8 * j + 5]), act_pack2<FP16>(v[8 * j + 6], v[8 * j + 7]));
+      } else if (valid) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          __stcg(&p.part_o[part_row * 32 + c * 8 + j], make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+      }
+      __syncwarp();
+    }
+    if (stepped) {
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.o_free[s]);
+    }
+    if (!two && i1 > i0) {
+      // the next queries may land where the other half's result was
+      fence_proxy_async_smem();
+      named_bar_sync(bar, 128);
+      if (r == 0) mbar_arrive(&sm.q_empty);
+    }
+    if (whole_pair) {
+      if (valid && p.a.lse)
+        p.a.lse[(int64_t)tok * p.a.hq + head] = l == 0.f ? -CUDART_INF_F : (m2 + log2f(l) - WEIGHT_EXP<FP16>) * LN2;
+      unsigned bad = __ballot_sync(0xffffffffu, valid && poison != 0.f);
+      __syncwarp();  // the row's own stores come before those of attend_row
+      while (bad) {
+        const int src = __ffs(bad) - 1;
+        bad &= bad - 1;
+        attend_row<FP16>(p.a, it.b, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, head, src),
+                         __shfl_sync(0xffffffffu, pos, src), kv);
+      }
+    } else {
+      if (valid) __stcg(&p.part_ml[part_row], make_float2(m2, l));
+      __threadfence();
+      named_bar_sync(bar, 128);
+      if (r == 0) {
+        unsigned* counter = &p.counters[it.first * 2 + tile];
+        const bool last = atomicAdd(counter, 1u) + 1 == (unsigned)it.parts;
+        if (last) *counter = 0;
+        sm.last[s] = last;
+      }
+      named_bar_sync(bar, 128);
+      if (sm.last[s]) {
+        __threadfence();
+        join_parts<FP16>(p, it, tile, min(p.tile_tok, it.n_tok - tile * p.tile_tok) * p.group);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.ring_empty[slot]);
   }
+}
+
+template <bool FP16>
+__global__ void __launch_bounds__(THREADS, 1)
+    attention_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
+  extern __shared__ unsigned char raw[];
+  unsigned char* q_smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  unsigned char* kv_smem = q_smem + 2 * TILE_BYTES;
+  Smem& sm = *reinterpret_cast<Smem*>(kv_smem + STAGES * TILE_BYTES);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&sm.kv_full[i], 1);
+      mbar_init(&sm.kv_empty[i], 1);
+    }
+    for (int i = 0; i < RING; ++i) {
+      mbar_init(&sm.ring_full[i], 1);
+      mbar_init(&sm.ring_empty[i], 10);  // copying lane, issuing thread, eight softmax warps
+    }
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    mbar_init(&sm.merge_full, 4);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.s_full[s], 1);
+      mbar_init(&sm.p_full[s], 4);
+      mbar_init(&sm.o_full[s], 1);
+      mbar_init(&sm.o_free[s], 4);
+    }
+    mbar_init(&sm.drained, 1);
+    sm.dead = 0;
+    fence_mbar_init();
+  }
+  if (warp == MMA_WARP) {
+    tc::tmem_alloc(&sm.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  const long long piece = measure_line(p, sm, blockIdx.x);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = sm.tmem;
+  if (warp < 8) {
+    softmax_role<FP16>(p, sm, warp >> 2, q_smem, kv_smem, tmem);
+  } else if (warp == LOAD_WARP) {
+    load_role(p, maps, sm, q_smem, kv_smem);
+  } else if (warp == MMA_WARP) {
+    if ((threadIdx.x & 31) == 0) mma_role(p, sm, smem_u32(q_smem), smem_u32(kv_smem), tmem, FP16 ? 0u : 1u);
+  } else if (warp == PLAN_WARP) {
+    plan_role(p, sm, blockIdx.x, piece);
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == MMA_WARP) tc::tmem_dealloc(tmem, 512);
+}
+
+constexpr size_t SMEM_BYTES = (2 + STAGES) * TILE_BYTES + 1024 + sizeof(Smem);
+static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
+
+int sm_count() {
+  static int counts[64] = {0};
+  static uint64_t done = 0;
+  int dev = 0;
+  const bool have = once_per_device(done, [&](int d) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d) == cudaSuccess) counts[d] = n;
+    cudaFuncSetAttribute(attention_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    cudaFuncSetAttribute(attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+  });
+  if (!have || cudaGetDevice(&dev) != cudaSuccess || counts[dev] <= 0) {
+    cudaGetLastError();  // no device here: size for a full GB300
+    return 152;
+  }
+  return counts[dev] < 512 ? counts[dev] : 512;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  std::lock_guard<std::mutex> lk(host_mutex());
+  if (!fn) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }
+  return fn;
+}
+
+// [n3, n2, n1, 128] elements, strides s3, s2, s1 (elements); boxes of 64 x b1 x b2 x b3
+bool encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, bool fp16, const void* base, int64_t n1, int64_t s1,
+            int64_t n2, int64_t s2, int64_t n3, int64_t s3, uint32_t b1, uint32_t b2, uint32_t b3) {
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)n1, (cuuint64_t)n2, (cuuint64_t)n3};
+  // the stride of a dimension of size 1 is free, but not 0
+  const cuuint64_t strides[3] = {(cuuint64_t)(n1 > 1 ? s1 : D) * 2, (cuuint64_t)(n2 > 1 ? s2 : D) * 2,
+                                 (cuuint64_t)(n3 > 1 ? s3 : D) * 2};
+  const cuuint32_t box[4] = {64, b1, b2, b3}, step[4] = {1, 1, 1, 1};
+  return enc(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
+             dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
-size_t attention_workspace_bytes() { return KDA_ATTENTION_ZEROED_BYTES; }
+size_t attention_workspace_bytes() {
+  return KDA_ATTENTION_ZEROED_BYTES + (size_t)sm_count() * 4 * ROWS * (sizeof(float2) + 32 * sizeof(float4));
+}
 
-int launch_attention(const AttentionParams& p, bool fp16, void* workspace, cudaStream_t stream) {
-  const int64_t rows = (int64_t)p.t_total * p.hq;
-  const int64_t blocks = (rows + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32);
+int launch_attention(const AttentionParams& a, bool fp16, void* workspace, cudaStream_t stream) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = map_encoder();
+  if (!enc) return -1;
+  Params p;
+  p.a = a;
+  p.group = a.hq / a.hkv;
+  p.tile_tok = ROWS / p.group;
+  p.n_cta = sm_count();
+  const int page = 1 << a.page_shift;
+  p.boxes = page < KT ? KT / page : 1;
+  p.min_piece = 2;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  p.counters = reinterpret_cast<unsigned*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + KDA_ATTENTION_ZEROED_BYTES);
+  p.part_o = reinterpret_cast<float4*>(p.part_ml + (size_t)p.n_cta * 4 * ROWS);
+  Maps maps;
+  const int box = page < KT ? page : KT;
+  if (!encode(enc, &maps.k, fp16, a.kc, page, a.kc_st, a.hkv, a.kc_sh, a.n_pages, a.kc_sp, box, 1, 1) ||
+      !encode(enc, &maps.v, fp16, a.vc, page, a.vc_st, a.hkv, a.vc_sh, a.n_pages, a.vc_sp, box, 1, 1) ||
+      !encode(enc, &maps.q, fp16, a.q, p.group, a.q_sh, a.hkv, a.q_sh * p.group, a.t_total, a.q_st, p.group, 1, p.tile_tok) ||
+      !encode(enc, &maps.q1, fp16, a.q, p.group, a.q_sh, a.hkv, a.q_sh * p.group, a.t_total, a.q_st, p.group, 1, 1))
+    return -1;
   trace_begin("attention", stream);
-  for (int b0 = 0; b0 < p.n_req; b0 += 65535) {
-    AttentionParams part = p;
-    part.cu_seqlens += b0;
-    part.kv_lens += b0;
-    part.table += b0 * p.table_stride;
-    const int n = p.n_req - b0 < 65535 ? p.n_req - b0 : 65535;
-    const dim3 grid((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8), n);
-    if (fp16) attention_rows_kernel<true><<<grid, ROW_THREADS, 0, stream>>>(part);
-    else attention_rows_kernel<false><<<grid, ROW_THREADS, 0, stream>>>(part);
-  }
+  if (fp16) attention_kernel<true><<<p.n_cta, THREADS, SMEM_BYTES, stream>>>(p, maps);
+  else attention_kernel<false><<<p.n_cta, THREADS, SMEM_BYTES, stream>>>(p, maps);
   trace_end(stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

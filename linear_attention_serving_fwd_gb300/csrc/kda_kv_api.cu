@@ -195,6 +195,8 @@ int kda_paged_attention(const kda_kv_cache* cache, const void* q, int64_t q_stri
   if (window < 0 || sinks < 0) return fail(KDA_ERR_INVALID_ARGUMENT, "window and sinks must be >= 0.");
   if (t_total == 0 || n_req == 0) return ok();
   if ((rc = check_rows(q, q_stride_tok, q_stride_head, "q"))) return rc;
+  if ((t_total > 1 && q_stride_tok < kda::D) || (hq > 1 && q_stride_head < kda::D))
+    return fail(KDA_ERR_INVALID_ARGUMENT, "q rows must not overlap: strides >= 128 elements.");
   if (!out) return fail(KDA_ERR_INVALID_ARGUMENT, "out must not be NULL.");
   if (!aligned16(out)) return fail(KDA_ERR_INVALID_ARGUMENT, "out must be 16-byte aligned.");
   if (!cu_seqlens || !kv_lens) return fail(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens and kv_lens must not be NULL.");
