@@ -383,12 +383,26 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
   }
 }
 
-// --- the issuing thread ------------------------------------------------------------------
+// --- the issuing warp --------------------------------------------------------------------
+// Every lane runs the role, so that its values are uniform and live in the
+// registers that the tensor instructions read; one elected lane issues.
 struct Step {
   int s;            // stream
   uint32_t v_stage, v_parity;
   bool release_v, first, last;
 };
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "elect.sync _|p, 0xffffffff;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, uint32_t q_addr, uint32_t kv_addr, uint32_t tmem, uint32_t bf16) {
   unsigned* err = p.a.err;
@@ -396,29 +410,46 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, uint32_t q_a
   uint32_t fills = 0, q_count = 0;
   uint32_t p_count[2] = {0, 0}, o_count[2] = {0, 0};
   bool ok = true;
+  auto await = [&](uint64_t* bar, uint32_t parity) {
+    if (ok) ok = __all_sync(0xffffffffu, wait(bar, parity, sm, err));
+  };
   auto pv = [&](const Step& x) {
-    ok = ok && wait(&sm.kv_full[x.v_stage], x.v_parity, sm, err);
-    ok = ok && wait(&sm.p_full[x.s], p_count[x.s] & 1, sm, err);
-    ++p_count[x.s];
+    await(&sm.kv_full[x.v_stage], x.v_parity);
     if (x.first) {
-      ok = ok && wait(&sm.o_free[x.s], (o_count[x.s] & 1) ^ 1, sm, err);
+      await(&sm.o_free[x.s], (o_count[x.s] & 1) ^ 1);
       ++o_count[x.s];
     }
+    await(&sm.p_full[x.s], p_count[x.s] & 1);
+    ++p_count[x.s];
     if (!ok) return;
     tc::fence_after_sync();
     const uint32_t d = tmem + 256 + x.s * 128, a = tmem + x.s * 128;
     const uint64_t vd = smem_desc_mn(kv_addr + x.v_stage * TILE_BYTES);
+    if (elect_one()) {
 #pragma unroll
-    for (int j = 0; j < KT / 16; ++j)  // 16 keys: two 8-row groups of V
-      mma_f16_ts(d, a + j * 8, vd + j * (2048 >> 4), id_pv, (j > 0 || !x.first) ? 1u : 0u);
-    if (x.release_v) tc::mma_commit(&sm.kv_empty[x.v_stage]);
-    if (x.last) tc::mma_commit(&sm.o_full[x.s]);
+      for (int j = 0; j < KT / 16; ++j)  // 16 keys: two 8-row groups of V
+        mma_f16_ts(d, a + j * 8, vd + j * (2048 >> 4), id_pv, (j > 0 || !x.first) ? 1u : 0u);
+      if (x.release_v) tc::mma_commit(&sm.kv_empty[x.v_stage]);
+      if (x.last) tc::mma_commit(&sm.o_full[x.s]);
+    }
+    __syncwarp();
   };
   for (uint32_t items = 0; ok; ++items) {
     const uint32_t slot = items % RING;
-    if (!wait(&sm.ring_full[slot], (items / RING) & 1, sm, err)) break;
-    const Item it = sm.ring[slot];
-    mbar_arrive(&sm.ring_empty[slot]);
+    await(&sm.ring_full[slot], (items / RING) & 1);
+    if (!ok) break;
+    const Item& from = sm.ring[slot];
+    Item it;
+    it.b = uniform(from.b);
+    it.n_tok = uniform(from.n_tok);
+    it.pos = uniform(from.pos);
+    it.kv = uniform(from.kv);
+    it.i0 = uniform(from.i0);
+    it.i1 = uniform(from.i1);
+    it.n_sink = uniform(from.n_sink);
+    it.t_lo = uniform(from.t_lo);
+    if (elect_one()) mbar_arrive(&sm.ring_empty[slot]);
+    __syncwarp();
     if (it.b < 0) break;
     if (it.i1 == it.i0) continue;
     const bool two = it.n_tok > p.tile_tok;
@@ -435,7 +466,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, uint32_t q_a
           }
       }
     }
-    ok = ok && wait(&sm.q_full, q_count & 1, sm, err);
+    await(&sm.q_full, q_count & 1);
     ++q_count;
     bool seen[2] = {false, false};
     bool pending = false;
@@ -447,7 +478,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, uint32_t q_a
       fills += 2;
       const bool act0 = two ? tile_active(p, it, 0, t) : ((i - it.i0) & 1) == 0;
       const bool act1 = two ? tile_active(p, it, 1, t) : !act0;
-      ok = ok && wait(&sm.kv_full[ks], kp, sm, err);
+      await(&sm.kv_full[ks], kp);
       tc::fence_after_sync();
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -459,31 +490,39 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, uint32_t q_a
         const uint32_t d = tmem + s * 128;
         const uint64_t qd = tc::smem_desc_sw128(q_addr + (two ? s * TILE_BYTES : 0));
         const uint64_t kd = tc::smem_desc_sw128(kv_addr + ks * TILE_BYTES);
+        if (elect_one()) {
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          const uint32_t off = ((j >> 2) * HALF_BYTES + (j & 3) * 32) >> 4;
-          tc::mma_f16(d, qd + off, kd + off, id_qk, j > 0 ? 1u : 0u);
+          for (int j = 0; j < D / 16; ++j) {
+            const uint32_t off = ((j >> 2) * HALF_BYTES + (j & 3) * 32) >> 4;
+            tc::mma_f16(d, qd + off, kd + off, id_qk, j > 0 ? 1u : 0u);
+          }
+          tc::mma_commit(&sm.s_full[s]);
+          if (s == 1 || !act1) tc::mma_commit(&sm.kv_empty[ks]);
         }
-        tc::mma_commit(&sm.s_full[s]);
-        if (s == 1 || !act1) tc::mma_commit(&sm.kv_empty[ks]);
+        __syncwarp();
         if (pending) pv(prev);
         prev = {s, vs, vp, s == 1 || !act1, !seen[s], i == last_of[s]};
         seen[s] = true;
         pending = true;
       }
       if (!act0 && !act1) {  // no row of either tile sees it
-        ok = ok && wait(&sm.kv_full[vs], vp, sm, err);
-        mbar_arrive(&sm.kv_empty[ks]);
-        mbar_arrive(&sm.kv_empty[vs]);
+        await(&sm.kv_full[vs], vp);
+        if (elect_one()) {
+          mbar_arrive(&sm.kv_empty[ks]);
+          mbar_arrive(&sm.kv_empty[vs]);
+        }
+        __syncwarp();
       }
     }
     // the queries' buffer: free once the products have read it, or, for a block
     // of one tile, once the two results have been joined in it
-    if (two) tc::mma_commit(&sm.q_empty);
+    if (two && elect_one()) tc::mma_commit(&sm.q_empty);
+    __syncwarp();
     if (pending && ok) pv(prev);
   }
   // every product has ended before tensor memory is freed
-  tc::mma_commit(&sm.drained);
+  if (elect_one()) tc::mma_commit(&sm.drained);
+  __syncwarp();
   mbar_wait_bounded(&sm.drained, 0, err);
 }
 
@@ -682,35 +721,44 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
       ++s_count;
       tc::fence_after_sync();
       if (any_row) {
-        uint32_t x[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc::tmem_ld32_async(t_s + c * 32, x[c]);
         const int held = *(volatile int*)&sm.page_mask[(tiles + i - i0) % MASKS];
-        tc::tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc::tmem_regs(x[c]);
         const bool whole = held == all_held && key + KT <= hi_min && (key >= lo_max || key + KT <= sink_min);
-        if (!whole) {
+        // S is read twice, 64 columns at a time: for the maximum and for the
+        // weights.  All 128 at once would not leave the row's state in registers.
+        auto load = [&](int half, uint32_t (&x)[2][32]) {
+          tc::tmem_ld32_async(t_s + half * 64, x[0]);
+          tc::tmem_ld32_async(t_s + half * 64 + 32, x[1]);
+          tc::tmem_wait_ld();
+          tc::tmem_regs(x[0]);
+          tc::tmem_regs(x[1]);
+          if (!whole) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int k0 = key + half * 64 + c * 32, box = half * 2 + c;
+              uint32_t seen = bits_below(hi - k0) & (~bits_below(lo - k0) | bits_below(sink - k0));
+              if (box_shift == 4)
+                seen &= ((held >> (2 * box)) & 1 ? 0xffffu : 0u) | ((held >> (2 * box + 1)) & 1 ? 0xffff0000u : 0u);
+              else if (!((held >> ((box * 32) >> box_shift)) & 1))
+                seen = 0;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[c][j] = (seen >> j) & 1 ? x[c][j] : 0xff800000u;
+            }
+          }
+        };
+        float m_new = m;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t x[2][32];
+          load(half, x);
+          float top[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int k0 = key + c * 32;
-            uint32_t seen = bits_below(hi - k0) & (~bits_below(lo - k0) | bits_below(sink - k0));
-            if (box_shift == 4)
-              seen &= ((held >> (2 * c)) & 1 ? 0xffffu : 0u) | ((held >> (2 * c + 1)) & 1 ? 0xffff0000u : 0u);
-            else if (!((held >> ((c * 32) >> box_shift)) & 1))
-              seen = 0;
+            top[c] = __uint_as_float(x[c >> 1][(c & 1) * 16]);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[c][j] = (seen >> j) & 1 ? x[c][j] : 0xff800000u;
+            for (int j = 1; j < 16; ++j) top[c] = fmaxf(top[c], __uint_as_float(x[c >> 1][(c & 1) * 16 + j]));
           }
+          m_new = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), m_new);
         }
-        float top[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          top[c] = __uint_as_float(x[c][0]);
-#pragma unroll
-          for (int j = 1; j < 32; ++j) top[c] = fmaxf(top[c], __uint_as_float(x[c][j]));
-        }
-        const float m_new = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), m);
         // m = -inf: nothing seen yet, any first maximum is taken (-inf - -inf
         // compares false).  Rows past the block hold anything and have no say.
         if (__any_sync(0xffffffffu, valid && (m_new - m) * sl > GROWTH)) {
@@ -736,10 +784,11 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          uint32_t w[32];
+          uint32_t x[2][32], w[32];
+          load(half, x);
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            const uint32_t* src = &x[half * 2 + (j >> 4)][(j & 15) * 2];
+            const uint32_t* src = &x[j >> 4][(j & 15) * 2];
             const float2 e = ffma2(make_float2(__uint_as_float(src[0]), __uint_as_float(src[1])), sl2, ref2);
             const float2 y = make_float2(ex2(e.x), ex2(e.y));
             sum[j & 1] = fadd2(sum[j & 1], y);
@@ -910,7 +959,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   unsigned char* q_smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* kv_smem = q_smem + 2 * TILE_BYTES;
   Smem& sm = *reinterpret_cast<Smem*>(kv_smem + STAGES * TILE_BYTES);
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&sm.kv_full[i], 1);
@@ -918,7 +967,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int i = 0; i < RING; ++i) {
       mbar_init(&sm.ring_full[i], 1);
-      mbar_init(&sm.ring_empty[i], 10);  // copying lane, issuing thread, eight softmax warps
+      mbar_init(&sm.ring_empty[i], 10);  // copying lane, issuing lane, eight softmax warps
     }
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
@@ -947,7 +996,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp == LOAD_WARP) {
     load_role(p, maps, sm, q_smem, kv_smem);
   } else if (warp == MMA_WARP) {
-    if ((threadIdx.x & 31) == 0) mma_role(p, sm, smem_u32(q_smem), smem_u32(kv_smem), tmem, FP16 ? 0u : 1u);
+    mma_role(p, sm, smem_u32(q_smem), smem_u32(kv_smem), tmem, FP16 ? 0u : 1u);
   } else if (warp == PLAN_WARP) {
     plan_role(p, sm, blockIdx.x, piece);
   }
