@@ -16,7 +16,7 @@
 //
 // Warps.  Two softmax warpgroups (one thread a row), each with an S/P and an O
 // of its own: while one of them works on its S, the tensor cores serve the
-// other.  One warp copies (TMA: a box per page and half row), one issues the
+// other.  One warp copies (TMA: a box per page and half row), two issue the
 // matrix products, one lays out the work.  A block of one tile (single tokens,
 // short windows) gives both warpgroups the same rows and every other key tile;
 // their two results are joined in shared memory.
@@ -43,7 +43,7 @@ constexpr int HALF_BYTES = TILE_BYTES / 2;  // 64 of the 128 dimensions
 constexpr int RING = 4;        // items ahead
 constexpr int MASKS = 8;       // page masks of the K tiles in flight
 constexpr int THREADS = 384;
-constexpr int LOAD_WARP = 8, MMA_WARP = 9, PLAN_WARP = 10;
+constexpr int LOAD_WARP = 8, PLAN_WARP = 9, MMA_WARP = 10;  // MMA_WARP + 1: the second stream's
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // The running reference follows the row's maximum only when that has grown by
 // 2^GROWTH: until then weights up to 2^GROWTH stand in for ones, and the
@@ -68,9 +68,9 @@ struct Item {
 struct Smem {
   uint64_t kv_full[STAGES], kv_empty[STAGES];
   uint64_t ring_full[RING], ring_empty[RING];
-  uint64_t q_full, q_empty, merge_full;
-  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
-  uint64_t drained;
+  uint64_t q_full, q_empty, q_read, merge_full;
+  uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];
+  uint64_t drained[2];
   Item ring[RING];
   int page_mask[MASKS];
   float2 merge_ml[ROWS];
@@ -81,6 +81,7 @@ struct Smem {
   uint32_t tmem;
   int dead;
   int last[2];
+  unsigned poisoned[2][4];  // rows of a joined tile
 };
 
 struct Params {
@@ -91,7 +92,7 @@ struct Params {
   int boxes;               // pages per key tile (1 when a page holds more)
   unsigned* counters;      // [n_cta][2], zero between calls
   float2* part_ml;         // [n_cta][2 slots][2 tiles][ROWS]
-  float4* part_o;          // [n_cta][2 slots][2 tiles][ROWS][32]
+  float4* part_o;          // [n_cta][2 slots][2 tiles][ROWS / 8][32][8]: 16-byte pieces of 8 rows side by side
 };
 
 // --- waits ---------------------------------------------------------------------
@@ -111,7 +112,9 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile 
   return false;
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Smem& sm, unsigned* err) {
-  if (mbar_test_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)  // most waits are short: parking and waking costs more
+    if (mbar_test_wait(bar, parity)) return true;
   return wait_slow(bar, parity, &sm.dead, err);
 }
 // by a whole warp, which runs warp-wide instructions next
@@ -383,15 +386,11 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
   }
 }
 
-// --- the issuing warp --------------------------------------------------------------------
-// Every lane runs the role, so that its values are uniform and live in the
-// registers that the tensor instructions read; one elected lane issues.
-struct Step {
-  int s;            // stream
-  uint32_t v_stage, v_parity;
-  bool release_v, first, last;
-};
-
+// --- the issuing warps -------------------------------------------------------------------
+// One warp a stream, so that neither waits for the other's softmax; the tensor
+// cores take the products of both as they come.  Every lane runs the role, so
+// that its values are uniform and live in the registers that the tensor
+// instructions read; one elected lane issues.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile(
@@ -404,35 +403,28 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-__device__ __forceinline__ void mma_role(const Params& p, Smem& sm, uint32_t q_addr, uint32_t kv_addr, uint32_t tmem, uint32_t bf16) {
+// A place in the ring of K and V tiles and the parity of its fill.
+struct Stage {
+  uint32_t at = 0, parity = 0;
+  __device__ __forceinline__ void skip(uint32_t n) {
+    at += n;
+    if (at >= STAGES) {
+      at -= STAGES;
+      parity ^= 1;
+    }
+  }
+};
+
+__device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint32_t q_addr, uint32_t kv_addr, uint32_t tmem,
+                                         uint32_t bf16) {
   unsigned* err = p.a.err;
   const uint32_t id_qk = tc::idesc_f16(ROWS, KT, bf16), id_pv = tc::idesc_f16(ROWS, D, bf16) | (1u << 16);
-  uint32_t fills = 0, q_count = 0;
-  uint32_t p_count[2] = {0, 0}, o_count[2] = {0, 0};
+  const uint32_t t_s = tmem + s * 128, t_p = t_s + 64, t_o = tmem + 256 + s * 128;
+  Stage next;  // of list index i0 of the next item
+  uint32_t q_parity = 0, p_parity = 0, o_parity = 1;
   bool ok = true;
   auto await = [&](uint64_t* bar, uint32_t parity) {
     if (ok) ok = __all_sync(0xffffffffu, wait(bar, parity, sm, err));
-  };
-  auto pv = [&](const Step& x) {
-    await(&sm.kv_full[x.v_stage], x.v_parity);
-    if (x.first) {
-      await(&sm.o_free[x.s], (o_count[x.s] & 1) ^ 1);
-      ++o_count[x.s];
-    }
-    await(&sm.p_full[x.s], p_count[x.s] & 1);
-    ++p_count[x.s];
-    if (!ok) return;
-    tc::fence_after_sync();
-    const uint32_t d = tmem + 256 + x.s * 128, a = tmem + x.s * 128;
-    const uint64_t vd = smem_desc_mn(kv_addr + x.v_stage * TILE_BYTES);
-    if (elect_one()) {
-#pragma unroll
-      for (int j = 0; j < KT / 16; ++j)  // 16 keys: two 8-row groups of V
-        mma_f16_ts(d, a + j * 8, vd + j * (2048 >> 4), id_pv, (j > 0 || !x.first) ? 1u : 0u);
-      if (x.release_v) tc::mma_commit(&sm.kv_empty[x.v_stage]);
-      if (x.last) tc::mma_commit(&sm.o_full[x.s]);
-    }
-    __syncwarp();
   };
   for (uint32_t items = 0; ok; ++items) {
     const uint32_t slot = items % RING;
@@ -453,77 +445,85 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, uint32_t q_a
     if (it.b < 0) break;
     if (it.i1 == it.i0) continue;
     const bool two = it.n_tok > p.tile_tok;
-    int last_of[2] = {-1, -1};  // last list index of each stream
-    for (int s = 0; s < 2; ++s) {
-      if (!two) {
-        last_of[s] = it.i1 - 1 - ((it.i1 - 1 - it.i0 - s) & 1);
-        if (last_of[s] < it.i0) last_of[s] = -1;
-      } else {
-        for (int i = it.i1 - 1; i >= it.i0; --i)
-          if (tile_active(p, it, s, list_tile(it, i))) {
-            last_of[s] = i;
-            break;
-          }
+    await(&sm.q_full, q_parity);
+    q_parity ^= 1;
+    const uint64_t qd = tc::smem_desc_sw128(q_addr + (two ? s * TILE_BYTES : 0));
+    bool first = true;
+    Stage st = next;
+    for (int i = it.i0; i < it.i1; ++i, st.skip(2)) {
+      Stage sv = st;
+      sv.skip(1);
+      if (two ? !tile_active(p, it, s, list_tile(it, i)) : ((i - it.i0) & 1) != s) {
+        // hidden from every row, or the other stream's: both streams see every
+        // fill, so that none is two fills behind (a wait tells odd from even)
+        await(&sm.kv_full[st.at], st.parity);
+        await(&sm.kv_full[sv.at], sv.parity);
+        if (elect_one()) {
+          mbar_arrive(&sm.kv_empty[st.at]);
+          mbar_arrive(&sm.kv_empty[sv.at]);
+        }
+        __syncwarp();
+        continue;
       }
-    }
-    await(&sm.q_full, q_count & 1);
-    ++q_count;
-    bool seen[2] = {false, false};
-    bool pending = false;
-    Step prev;
-    for (int i = it.i0; i < it.i1 && ok; ++i) {
-      const int t = list_tile(it, i);
-      const uint32_t ks = fills % STAGES, kp = (fills / STAGES) & 1;
-      const uint32_t vs = (fills + 1) % STAGES, vp = ((fills + 1) / STAGES) & 1;
-      fills += 2;
-      const bool act0 = two ? tile_active(p, it, 0, t) : ((i - it.i0) & 1) == 0;
-      const bool act1 = two ? tile_active(p, it, 1, t) : !act0;
-      await(&sm.kv_full[ks], kp);
+      await(&sm.kv_full[st.at], st.parity);
+      if (!ok) break;
       tc::fence_after_sync();
+      const uint64_t kd = tc::smem_desc_sw128(kv_addr + st.at * TILE_BYTES);
+      if (elect_one()) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (!(s ? act1 : act0) || !ok) continue;
-        if (pending && prev.s == s) {  // S shares its columns with the weights of that step
-          pv(prev);
-          pending = false;
+        for (int j = 0; j < D / 16; ++j) {
+          const uint32_t off = ((j >> 2) * HALF_BYTES + (j & 3) * 32) >> 4;
+          tc::mma_f16(t_s, qd + off, kd + off, id_qk, j > 0 ? 1u : 0u);
         }
-        const uint32_t d = tmem + s * 128;
-        const uint64_t qd = tc::smem_desc_sw128(q_addr + (two ? s * TILE_BYTES : 0));
-        const uint64_t kd = tc::smem_desc_sw128(kv_addr + ks * TILE_BYTES);
-        if (elect_one()) {
+        tc::mma_commit(&sm.s_full[s]);
+        // the first stream's last scores of a block of one tile: from here on the
+        // other stream's result may take the queries' place
+        if (!two && s == 0 && it.i1 - it.i0 > 1 && i + 2 >= it.i1) tc::mma_commit(&sm.q_read);
+        tc::mma_commit(&sm.kv_empty[st.at]);
+      }
+      __syncwarp();
+      await(&sm.kv_full[sv.at], sv.parity);
+      if (first) {
+        await(&sm.o_free[s], o_parity);
+        o_parity ^= 1;
+      }
+      // the weights come in halves, of the last 64 keys first
+      const uint64_t vd = smem_desc_mn(kv_addr + sv.at * TILE_BYTES);
+      await(&sm.p_half[s], p_parity);
+      if (!ok) break;
+      tc::fence_after_sync();
+      if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            const uint32_t off = ((j >> 2) * HALF_BYTES + (j & 3) * 32) >> 4;
-            tc::mma_f16(d, qd + off, kd + off, id_qk, j > 0 ? 1u : 0u);
-          }
-          tc::mma_commit(&sm.s_full[s]);
-          if (s == 1 || !act1) tc::mma_commit(&sm.kv_empty[ks]);
-        }
-        __syncwarp();
-        if (pending) pv(prev);
-        prev = {s, vs, vp, s == 1 || !act1, !seen[s], i == last_of[s]};
-        seen[s] = true;
-        pending = true;
+        for (int j = KT / 32; j < KT / 16; ++j)  // 16 keys: two 8-row groups of V
+          mma_f16_ts(t_o, t_p + j * 8, vd + j * (2048 >> 4), id_pv, (j > KT / 32 || !first) ? 1u : 0u);
       }
-      if (!act0 && !act1) {  // no row of either tile sees it
-        await(&sm.kv_full[vs], vp);
-        if (elect_one()) {
-          mbar_arrive(&sm.kv_empty[ks]);
-          mbar_arrive(&sm.kv_empty[vs]);
-        }
-        __syncwarp();
+      __syncwarp();
+      await(&sm.p_full[s], p_parity);
+      p_parity ^= 1;
+      if (!ok) break;
+      tc::fence_after_sync();
+      if (elect_one()) {
+#pragma unroll
+        for (int j = 0; j < KT / 32; ++j) mma_f16_ts(t_o, t_p + j * 8, vd + j * (2048 >> 4), id_pv, 1u);
+        tc::mma_commit(&sm.kv_empty[sv.at]);
       }
+      __syncwarp();
+      first = false;
     }
-    // the queries' buffer: free once the products have read it, or, for a block
-    // of one tile, once the two results have been joined in it
-    if (two && elect_one()) tc::mma_commit(&sm.q_empty);
+    next = st;
+    if (elect_one()) {
+      if (!first) tc::mma_commit(&sm.o_full[s]);
+      // the queries' buffer: free once both streams' products have read it; for a
+      // block of one tile the first warpgroup answers for its stream, once the
+      // two results have been joined in the buffer
+      if (two || s == 1) tc::mma_commit(&sm.q_empty);
+    }
     __syncwarp();
-    if (pending && ok) pv(prev);
   }
   // every product has ended before tensor memory is freed
-  if (elect_one()) tc::mma_commit(&sm.drained);
+  if (elect_one()) tc::mma_commit(&sm.drained[s]);
   __syncwarp();
-  mbar_wait_bounded(&sm.drained, 0, err);
+  mbar_wait_bounded(&sm.drained[s], 0, err);
 }
 
 // --- the planning warp -----------------------------------------------------------------
@@ -641,45 +641,65 @@ __device__ __forceinline__ long long measure_line(const Params& p, Smem& sm, int
 // --- a softmax warpgroup -----------------------------------------------------------------
 __device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
+// Where 16-byte piece c of a partial row lies: pieces of 8 rows fill a line, so
+// that threads of neighbouring rows write, and lanes of 8 rows and 4 pieces
+// read, whole lines.
+__device__ __forceinline__ size_t part_piece(size_t row, int c) { return ((row >> 3) * 32 + c) * 8 + (row & 7); }
+
+// Joins a tile's parts, by the warpgroup that finished the last of them.
 template <bool FP16>
-__device__ __forceinline__ void join_parts(const Params& p, const Item& it, int tile, int n_rows) {
+__device__ __forceinline__ void join_parts(const Params& p, Smem& sm, int s, const Item& it, int tile, int n_rows) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
-  for (int row = warp; row < n_rows; row += 4) {
-    const int i = tile * p.tile_tok + row / p.group, head = it.kvh * p.group + row % p.group;
-    auto part_at = [&](int k) { return (((size_t)(it.first + k) * 2 + (k == 0 ? 1 : 0)) * 2 + tile) * ROWS + row; };
+  const int parts = it.parts, first = it.first;
+  auto part_row = [&](int k, int row) { return (((size_t)(first + k) * 2 + (k == 0 ? 1 : 0)) * 2 + tile) * ROWS + row; };
+  if ((threadIdx.x & 127) < 4) sm.poisoned[s][threadIdx.x & 3] = 0;
+  named_bar_sync(1 + s, 128);
+  // a unit: 8 rows by 8 pieces; a lane: one row, two pieces
+  for (int u = warp; u < (n_rows + 7) / 8 * 4; u += 4) {
+    const int row = (u >> 2) * 8 + (lane & 7), c = (u & 3) * 8 + (lane >> 3);
+    if (row >= n_rows) continue;
     float top = -CUDART_INF_F;
-    for (int k = lane; k < it.parts; k += 32) top = fmaxf(top, __ldcg(&p.part_ml[part_at(k)]).x);
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int k = 0; k < it.parts; ++k) {
-      const float2 ml = __ldcg(&p.part_ml[part_at(k)]);
-      const float4 x = __ldcg(&p.part_o[part_at(k) * 32 + lane]);
-      if (ml.x == -CUDART_INF_F) continue;  // nothing seen, nothing stored
-      const float w = ex2(ml.x - top);
-      l += w * ml.y;
-      o.x += w * x.x;
-      o.y += w * x.y;
-      o.z += w * x.z;
-      o.w += w * x.w;
+    for (int k = 0; k < parts; ++k) top = fmaxf(top, __ldcg(&p.part_ml[part_row(k, row)]).x);
+    float l = 0.f, o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      const size_t at = part_row(k, row);
+      const float2 ml = __ldcg(&p.part_ml[at]);
+      const float4 x = __ldcg(&p.part_o[part_piece(at, c)]), y = __ldcg(&p.part_o[part_piece(at, c + 4)]);
+      // a part that has seen nothing stored nothing
+      const bool some = ml.x != -CUDART_INF_F;
+      const float w = some ? ex2(ml.x - top) : 0.f;
+      l += some ? w * ml.y : 0.f;
+      const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] += some ? w * z[j] : 0.f;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    o.x *= inv;
-    o.y *= inv;
-    o.z *= inv;
-    o.w *= inv;
-    const int tok = it.tok + i;
-    const float zero = (o.x + o.y + o.z + o.w) * 0.f;  // NaN when one is not finite
-    if (__any_sync(0xffffffffu, zero != 0.f)) {
-      attend_row<FP16>(p.a, it.b, tok, head, it.pos + i, it.kv);
-      continue;
+    float poison = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      o[j] *= inv;
+      poison += o[j] * 0.f;  // NaN from then on when one is not finite
     }
-    __nv_bfloat16* out = p.a.out + ((int64_t)tok * p.a.hq + head) * D + lane * 4;
-    *reinterpret_cast<uint2*>(out) = make_uint2(act_pack2<FP16>(o.x, o.y), act_pack2<FP16>(o.z, o.w));
-    if (p.a.lse && lane == 0)
+    if (poison != 0.f) atomicOr(&sm.poisoned[s][row >> 5], 1u << (row & 31));
+    const int tok = it.tok + tile * p.tile_tok + row / p.group, head = it.kvh * p.group + row % p.group;
+    __nv_bfloat16* out = p.a.out + ((int64_t)tok * p.a.hq + head) * D;
+    *reinterpret_cast<uint2*>(out + c * 4) = make_uint2(act_pack2<FP16>(o[0], o[1]), act_pack2<FP16>(o[2], o[3]));
+    *reinterpret_cast<uint2*>(out + c * 4 + 16) = make_uint2(act_pack2<FP16>(o[4], o[5]), act_pack2<FP16>(o[6], o[7]));
+    if (p.a.lse && c == 0)
       p.a.lse[(int64_t)tok * p.a.hq + head] = l == 0.f ? -CUDART_INF_F : (top + log2f(l) - WEIGHT_EXP<FP16>) * LN2;
+  }
+  __syncwarp();
+  named_bar_sync(1 + s, 128);
+  unsigned bad = sm.poisoned[s][warp];
+  while (bad) {
+    const int row = warp * 32 + __ffs(bad) - 1;
+    bad &= bad - 1;
+    const int i = tile * p.tile_tok + row / p.group;
+    attend_row<FP16>(p.a, it.b, it.tok + i, it.kvh * p.group + row % p.group, it.pos + i, it.kv);
   }
 }
 
@@ -720,6 +740,16 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
       warp_wait(&sm.s_full[s], s_count & 1, sm, err);
       ++s_count;
       tc::fence_after_sync();
+      if (key + KT > kv) {
+        // the tile's rows past the cached tokens hold whatever was there: zeros
+        // there keep the products finite
+        const uint32_t f = fills + 2 * (i - i0) + 1;
+        wait(&sm.kv_full[f % STAGES], (f / STAGES) & 1, sm, err);
+        unsigned char* v = kv_smem + (f % STAGES) * TILE_BYTES + (kv - key) * 128;
+        for (int c = r; c < (KT - (kv - key)) * 16; c += 128)
+          *reinterpret_cast<int4*>(v + ((c >> 3) & 1) * HALF_BYTES + (c >> 4) * 128 + (c & 7) * 16) = make_int4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+      }
       if (any_row) {
         const int held = *(volatile int*)&sm.page_mask[(tiles + i - i0) % MASKS];
         const bool whole = held == all_held && key + KT <= hi_min && (key >= lo_max || key + KT <= sink_min);
@@ -745,11 +775,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
             }
           }
         };
-        float m_new = m;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t x[2][32];
-          load(half, x);
+        auto maximum = [&](const uint32_t (&x)[2][32], float top0) {
           float top[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -757,8 +783,13 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
 #pragma unroll
             for (int j = 1; j < 16; ++j) top[c] = fmaxf(top[c], __uint_as_float(x[c >> 1][(c & 1) * 16 + j]));
           }
-          m_new = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), m_new);
-        }
+          return fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), top0);
+        };
+        uint32_t x[2][32];
+        load(0, x);
+        float m_new = maximum(x, m);
+        load(1, x);
+        m_new = maximum(x, m_new);
         // m = -inf: nothing seen yet, any first maximum is taken (-inf - -inf
         // compares false).  Rows past the block hold anything and have no say.
         if (__any_sync(0xffffffffu, valid && (m_new - m) * sl > GROWTH)) {
@@ -782,10 +813,9 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
         const float ref = WEIGHT_EXP<FP16> - (m == -CUDART_INF_F ? 0.f : m * sl);
         const float2 sl2 = make_float2(sl, sl), ref2 = make_float2(ref, ref);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t x[2][32], w[32];
-          load(half, x);
+        // the weights take the last 64 columns of S, whose scores are in registers
+        auto weights = [&](int half) {
+          uint32_t w[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const uint32_t* src = &x[j >> 4][(j & 15) * 2];
@@ -794,21 +824,20 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
             sum[j & 1] = fadd2(sum[j & 1], y);
             w[j] = act_pack2<FP16>(y.x, y.y);
           }
-          tmem_st32(t_s + half * 32, w);
-        }
+          tmem_st32(t_s + 64 + half * 32, w);
+        };
+        weights(1);
+        tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_half[s]);
+        load(0, x);
+        weights(0);
         sum[0] = fadd2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
         tmem_wait_st();
-      }
-      if (key + KT > kv) {
-        // the tile's rows past the cached tokens hold whatever was there: zeros
-        // there keep the products finite
-        const uint32_t f = fills + 2 * (i - i0) + 1;
-        wait(&sm.kv_full[f % STAGES], (f / STAGES) & 1, sm, err);
-        unsigned char* v = kv_smem + (f % STAGES) * TILE_BYTES + (kv - key) * 128;
-        for (int c = r; c < (KT - (kv - key)) * 16; c += 128)
-          *reinterpret_cast<int4*>(v + ((c >> 3) & 1) * HALF_BYTES + (c >> 4) * 128 + (c & 7) * 16) = make_int4(0, 0, 0, 0);
-        fence_proxy_async_smem();
+      } else if (lane == 0) {
+        mbar_arrive(&sm.p_half[s]);
       }
       stepped = true;
       tc::fence_before_sync();
@@ -827,6 +856,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
     const bool merged = !two && i1 - i0 > 1;
     if (!two && s == 1) {
       if (merged) {
+        warp_wait(&sm.q_read, merges & 1, sm, err);
+        ++merges;
         // rows of 512 bytes, their 16-byte pieces rotated by the row: no bank conflicts
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -905,7 +936,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
       } else if (valid) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          __stcg(&p.part_o[part_row * 32 + c * 8 + j], make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+          __stcg(&p.part_o[part_piece(part_row, c * 8 + j)], make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
       }
       __syncwarp();
     }
@@ -944,7 +975,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
       named_bar_sync(bar, 128);
       if (sm.last[s]) {
         __threadfence();
-        join_parts<FP16>(p, it, tile, min(p.tile_tok, it.n_tok - tile * p.tile_tok) * p.group);
+        join_parts<FP16>(p, sm, s, it, tile, min(p.tile_tok, it.n_tok - tile * p.tile_tok) * p.group);
       }
     }
     __syncwarp();
@@ -963,22 +994,24 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&sm.kv_full[i], 1);
-      mbar_init(&sm.kv_empty[i], 1);
+      mbar_init(&sm.kv_empty[i], 2);  // both streams
     }
     for (int i = 0; i < RING; ++i) {
       mbar_init(&sm.ring_full[i], 1);
-      mbar_init(&sm.ring_empty[i], 10);  // copying lane, issuing lane, eight softmax warps
+      mbar_init(&sm.ring_empty[i], 11);  // copying lane, two issuing lanes, eight softmax warps
     }
     mbar_init(&sm.q_full, 1);
-    mbar_init(&sm.q_empty, 1);
+    mbar_init(&sm.q_empty, 2);
+    mbar_init(&sm.q_read, 1);
     mbar_init(&sm.merge_full, 4);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.s_full[s], 1);
+      mbar_init(&sm.p_half[s], 4);
       mbar_init(&sm.p_full[s], 4);
+      mbar_init(&sm.drained[s], 1);
       mbar_init(&sm.o_full[s], 1);
       mbar_init(&sm.o_free[s], 4);
     }
-    mbar_init(&sm.drained, 1);
     sm.dead = 0;
     fence_mbar_init();
   }
@@ -995,8 +1028,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     softmax_role<FP16>(p, sm, warp >> 2, q_smem, kv_smem, tmem);
   } else if (warp == LOAD_WARP) {
     load_role(p, maps, sm, q_smem, kv_smem);
-  } else if (warp == MMA_WARP) {
-    mma_role(p, sm, smem_u32(q_smem), smem_u32(kv_smem), tmem, FP16 ? 0u : 1u);
+  } else if (warp >= MMA_WARP) {
+    mma_role(p, sm, warp - MMA_WARP, smem_u32(q_smem), smem_u32(kv_smem), tmem, FP16 ? 0u : 1u);
   } else if (warp == PLAN_WARP) {
     plan_role(p, sm, blockIdx.x, piece);
   }
