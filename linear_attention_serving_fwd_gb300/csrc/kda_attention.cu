@@ -70,7 +70,7 @@ struct Smem {
   uint64_t ring_full[RING], ring_empty[RING];
   uint64_t q_full, q_empty, q_read, merge_full;
   uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];
-  uint64_t drained[2];
+  uint64_t turn[2], drained[2];
   Item ring[RING];
   int page_mask[MASKS];
   float2 merge_ml[ROWS];
@@ -426,6 +426,16 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
   auto await = [&](uint64_t* bar, uint32_t parity) {
     if (ok) ok = __all_sync(0xffffffffu, wait(bar, parity, sm, err));
   };
+  // In blocks of two tiles the streams take turns at the tensor cores, key tile
+  // by key tile: a product of one and its next scores go in a row.  Left to mix,
+  // both streams' products finish late together, and both softmaxes run while
+  // the tensor cores idle.  (The turn passes through barriers: a lock in shared
+  // memory, spun on or slept on, halved the rate of the products themselves.)
+  uint32_t turn = s == 0 ? 1 : 0;  // parity: the first stream's first turn needs no pass
+  auto pass = [&]() {
+    if (elect_one()) mbar_arrive(&sm.turn[s ^ 1]);
+    __syncwarp();
+  };
   for (uint32_t items = 0; ok; ++items) {
     const uint32_t slot = items % RING;
     await(&sm.ring_full[slot], (items / RING) & 1);
@@ -450,6 +460,23 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
     const uint64_t qd = tc::smem_desc_sw128(q_addr + (two ? s * TILE_BYTES : 0));
     bool first = true;
     Stage st = next;
+    bool scored = false;  // this tile's scores have been issued behind the last tile's product
+    auto scores = [&](int i, const Stage& at) {
+      const uint64_t kd = tc::smem_desc_sw128(kv_addr + at.at * TILE_BYTES);
+      if (elect_one()) {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          const uint32_t off = ((j >> 2) * HALF_BYTES + (j & 3) * 32) >> 4;
+          tc::mma_f16(t_s, qd + off, kd + off, id_qk, j > 0 ? 1u : 0u);
+        }
+        tc::mma_commit(&sm.s_full[s]);
+        // the first stream's last scores of a block of one tile: from here on the
+        // other stream's result may take the queries' place
+        if (!two && s == 0 && it.i1 - it.i0 > 1 && i + 2 >= it.i1) tc::mma_commit(&sm.q_read);
+        tc::mma_commit(&sm.kv_empty[at.at]);
+      }
+      __syncwarp();
+    };
     for (int i = it.i0; i < it.i1; ++i, st.skip(2)) {
       Stage sv = st;
       sv.skip(1);
@@ -463,25 +490,20 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
           mbar_arrive(&sm.kv_empty[sv.at]);
         }
         __syncwarp();
+        if (two) {
+          await(&sm.turn[s], turn);
+          turn ^= 1;
+          pass();
+        }
         continue;
       }
-      await(&sm.kv_full[st.at], st.parity);
-      if (!ok) break;
-      tc::fence_after_sync();
-      const uint64_t kd = tc::smem_desc_sw128(kv_addr + st.at * TILE_BYTES);
-      if (elect_one()) {
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          const uint32_t off = ((j >> 2) * HALF_BYTES + (j & 3) * 32) >> 4;
-          tc::mma_f16(t_s, qd + off, kd + off, id_qk, j > 0 ? 1u : 0u);
-        }
-        tc::mma_commit(&sm.s_full[s]);
-        // the first stream's last scores of a block of one tile: from here on the
-        // other stream's result may take the queries' place
-        if (!two && s == 0 && it.i1 - it.i0 > 1 && i + 2 >= it.i1) tc::mma_commit(&sm.q_read);
-        tc::mma_commit(&sm.kv_empty[st.at]);
+      if (!scored) {
+        await(&sm.kv_full[st.at], st.parity);
+        if (!ok) break;
+        tc::fence_after_sync();
+        scores(i, st);
       }
-      __syncwarp();
+      scored = false;
       await(&sm.kv_full[sv.at], sv.parity);
       if (first) {
         await(&sm.o_free[s], o_parity);
@@ -502,12 +524,26 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
       p_parity ^= 1;
       if (!ok) break;
       tc::fence_after_sync();
+      if (two) {
+        await(&sm.turn[s], turn);
+        turn ^= 1;
+      }
       if (elect_one()) {
 #pragma unroll
         for (int j = 0; j < KT / 32; ++j) mma_f16_ts(t_o, t_p + j * 8, vd + j * (2048 >> 4), id_pv, 1u);
         tc::mma_commit(&sm.kv_empty[sv.at]);
       }
       __syncwarp();
+      if (two && i + 1 < it.i1 && tile_active(p, it, s, list_tile(it, i + 1))) {
+        Stage sk = sv;
+        sk.skip(1);
+        scored = __all_sync(0xffffffffu, mbar_test_wait(&sm.kv_full[sk.at], sk.parity));
+        if (scored) {
+          tc::fence_after_sync();
+          scores(i + 1, sk);
+        }
+      }
+      if (two) pass();
       first = false;
     }
     next = st;
@@ -1008,6 +1044,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&sm.s_full[s], 1);
       mbar_init(&sm.p_half[s], 4);
       mbar_init(&sm.p_full[s], 4);
+      mbar_init(&sm.turn[s], 1);
       mbar_init(&sm.drained[s], 1);
       mbar_init(&sm.o_full[s], 1);
       mbar_init(&sm.o_free[s], 4);
