@@ -61,6 +61,7 @@ struct Item {
   int i0, i1;          // this part's range of the key tile list
   int n_sink, t_lo;    // list: tiles 0 .. n_sink - 1, then t_lo, t_lo + 1, ..
   int lo, hi, sink_hi; // keys that some row sees: [lo, hi) and [0, sink_hi)
+  int act[2][3];       // a query tile sees list entries below [0] and in [[1], [2])
   int first, parts;    // CTA of the first part, parts of the pair
   int part;            // this part's number; < 0 in place of b ends the work
 };
@@ -127,6 +128,11 @@ __device__ __forceinline__ void warp_wait(uint64_t* bar, uint32_t parity, Smem& 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 __device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
@@ -292,12 +298,15 @@ struct Maps {
 
 __device__ __forceinline__ int list_tile(const Item& it, int i) { return i < it.n_sink ? i : it.t_lo + i - it.n_sink; }
 
-// whether query tile s of a block in two tiles sees anything of key tile t
-__device__ __forceinline__ bool tile_active(const Params& p, const Item& it, int s, int t) {
+// The list entries that query tile s of a block sees: sink tiles, then a range.
+__device__ __forceinline__ void tile_range(const Params& p, Item& it, int s) {
   const int first = it.pos + s * p.tile_tok, last = min(it.pos + it.n_tok, first + p.tile_tok);
-  const int hi = min(last, it.kv), lo = p.a.window ? first + 1 - p.a.window : 0;
-  return t * KT < hi && (t * KT + KT > lo || t * KT < p.a.sinks);
+  const int hi = max(0, min(last, it.kv)), lo = p.a.window ? max(0, first + 1 - p.a.window) : 0;
+  it.act[s][0] = (min(p.a.sinks, hi) + KT - 1) / KT;  // past n_sink the list runs on without a gap
+  it.act[s][1] = it.n_sink + max(0, lo / KT - it.t_lo);
+  it.act[s][2] = hi > lo ? it.n_sink + (hi + KT - 1) / KT - it.t_lo : 0;
 }
+__device__ __forceinline__ bool active(const int (&act)[3], int i) { return i < act[0] || (i >= act[1] && i < act[2]); }
 
 __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Smem& sm, unsigned char* q_smem, unsigned char* kv_smem) {
   const int lane = threadIdx.x & 31;
@@ -444,12 +453,9 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
     Item it;
     it.b = uniform(from.b);
     it.n_tok = uniform(from.n_tok);
-    it.pos = uniform(from.pos);
-    it.kv = uniform(from.kv);
     it.i0 = uniform(from.i0);
     it.i1 = uniform(from.i1);
-    it.n_sink = uniform(from.n_sink);
-    it.t_lo = uniform(from.t_lo);
+    const int act[3] = {uniform(from.act[s][0]), uniform(from.act[s][1]), uniform(from.act[s][2])};
     if (elect_one()) mbar_arrive(&sm.ring_empty[slot]);
     __syncwarp();
     if (it.b < 0) break;
@@ -480,7 +486,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
     for (int i = it.i0; i < it.i1; ++i, st.skip(2)) {
       Stage sv = st;
       sv.skip(1);
-      if (two ? !tile_active(p, it, s, list_tile(it, i)) : ((i - it.i0) & 1) != s) {
+      if (two ? !active(act, i) : ((i - it.i0) & 1) != s) {
         // hidden from every row, or the other stream's: both streams see every
         // fill, so that none is two fills behind (a wait tells odd from even)
         await(&sm.kv_full[st.at], st.parity);
@@ -504,6 +510,10 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
         scores(i, st);
       }
       scored = false;
+      // off the path from the weights to the next scores
+      const bool more = two && i + 1 < it.i1 && active(act, i + 1);
+      Stage sk = sv;
+      sk.skip(1);
       await(&sm.kv_full[sv.at], sv.parity);
       if (first) {
         await(&sm.o_free[s], o_parity);
@@ -534,9 +544,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
         tc::mma_commit(&sm.kv_empty[sv.at]);
       }
       __syncwarp();
-      if (two && i + 1 < it.i1 && tile_active(p, it, s, list_tile(it, i + 1))) {
-        Stage sk = sv;
-        sk.skip(1);
+      if (more) {
         scored = __all_sync(0xffffffffu, mbar_test_wait(&sm.kv_full[sk.at], sk.parity));
         if (scored) {
           tc::fence_after_sync();
@@ -615,6 +623,8 @@ __device__ __forceinline__ void plan_role(const Params& p, Smem& sm, int cta, lo
           it.first = (int)(s / piece);
           it.parts = (int)((e - 1) / piece) - it.first + 1;
           it.part = cta - it.first;
+          tile_range(p, it, 0);
+          tile_range(p, it, 1);
           post(it);
         }
         at += __shfl_sync(0xffffffffu, upto, 31);
@@ -772,7 +782,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
     bool stepped = false;
     for (int i = two ? i0 : i0 + s; i < i1; i += two ? 1 : 2) {
       const int t = list_tile(it, i), key = t * KT;
-      if (two && !tile_active(p, it, s, t)) continue;
+      if (two && !active(it.act[s], i)) continue;
       warp_wait(&sm.s_full[s], s_count & 1, sm, err);
       ++s_count;
       tc::fence_after_sync();
@@ -789,43 +799,43 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
       if (any_row) {
         const int held = *(volatile int*)&sm.page_mask[(tiles + i - i0) % MASKS];
         const bool whole = held == all_held && key + KT <= hi_min && (key >= lo_max || key + KT <= sink_min);
-        // S is read twice, 64 columns at a time: for the maximum and for the
-        // weights.  All 128 at once would not leave the row's state in registers.
-        auto load = [&](int half, uint32_t (&x)[2][32]) {
-          tc::tmem_ld32_async(t_s + half * 64, x[0]);
-          tc::tmem_ld32_async(t_s + half * 64 + 32, x[1]);
-          tc::tmem_wait_ld();
-          tc::tmem_regs(x[0]);
-          tc::tmem_regs(x[1]);
-          if (!whole) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int k0 = key + half * 64 + c * 32, box = half * 2 + c;
-              uint32_t seen = bits_below(hi - k0) & (~bits_below(lo - k0) | bits_below(sink - k0));
-              if (box_shift == 4)
-                seen &= ((held >> (2 * box)) & 1 ? 0xffffu : 0u) | ((held >> (2 * box + 1)) & 1 ? 0xffff0000u : 0u);
-              else if (!((held >> ((box * 32) >> box_shift)) & 1))
-                seen = 0;
-#pragma unroll
-              for (int j = 0; j < 32; ++j) x[c][j] = (seen >> j) & 1 ? x[c][j] : 0xff800000u;
-            }
-          }
-        };
-        auto maximum = [&](const uint32_t (&x)[2][32], float top0) {
-          float top[4];
-#pragma unroll
+        if (!whole) {
+          // hidden scores become -inf where they are
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            top[c] = __uint_as_float(x[c >> 1][(c & 1) * 16]);
+            uint32_t x[32];
+            tc::tmem_ld32_async(t_s + c * 32, x);
+            const int k0 = key + c * 32;
+            uint32_t seen = bits_below(hi - k0) & (~bits_below(lo - k0) | bits_below(sink - k0));
+            if (box_shift == 4)
+              seen &= ((held >> (2 * c)) & 1 ? 0xffffu : 0u) | ((held >> (2 * c + 1)) & 1 ? 0xffff0000u : 0u);
+            else if (!((held >> ((c * 32) >> box_shift)) & 1))
+              seen = 0;
+            tc::tmem_wait_ld();
+            tc::tmem_regs(x);
 #pragma unroll
-            for (int j = 1; j < 16; ++j) top[c] = fmaxf(top[c], __uint_as_float(x[c >> 1][(c & 1) * 16 + j]));
+            for (int j = 0; j < 32; ++j) x[j] = (seen >> j) & 1 ? x[j] : 0xff800000u;
+            tmem_st32(t_s + c * 32, x);
           }
-          return fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), top0);
-        };
-        uint32_t x[2][32];
-        load(0, x);
-        float m_new = maximum(x, m);
-        load(1, x);
-        m_new = maximum(x, m_new);
+          tmem_wait_st();
+        }
+        // S is read twice: for the maximum all 128 columns at once; the last 64
+        // stay for their weights, the first 64 come again, 32 at a time and
+        // ahead of their use, so that what is live fits the registers
+        uint32_t x[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::tmem_ld32_async(t_s + c * 32, x[c]);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::tmem_regs(x[c]);
+        float top[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          top[c] = max3(m, __uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
+#pragma unroll
+          for (int j = 2; j < 32; j += 2) top[c] = max3(top[c], __uint_as_float(x[c][j]), __uint_as_float(x[c][j + 1]));
+        }
+        const float m_new = fmaxf(max3(top[0], top[1], top[2]), top[3]);
         // m = -inf: nothing seen yet, any first maximum is taken (-inf - -inf
         // compares false).  Rows past the block hold anything and have no say.
         if (__any_sync(0xffffffffu, valid && (m_new - m) * sl > GROWTH)) {
@@ -849,29 +859,35 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
         const float ref = WEIGHT_EXP<FP16> - (m == -CUDART_INF_F ? 0.f : m * sl);
         const float2 sl2 = make_float2(sl, sl), ref2 = make_float2(ref, ref);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // the weights take the last 64 columns of S, whose scores are in registers
-        auto weights = [&](int half) {
-          uint32_t w[32];
+        auto weights = [&](const uint32_t (&x)[32], int c) {
+          uint32_t w[16];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const uint32_t* src = &x[j >> 4][(j & 15) * 2];
-            const float2 e = ffma2(make_float2(__uint_as_float(src[0]), __uint_as_float(src[1])), sl2, ref2);
+          for (int j = 0; j < 16; ++j) {
+            const float2 e = ffma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), sl2, ref2);
             const float2 y = make_float2(ex2(e.x), ex2(e.y));
             sum[j & 1] = fadd2(sum[j & 1], y);
             w[j] = act_pack2<FP16>(y.x, y.y);
           }
-          tmem_st32(t_s + 64 + half * 32, w);
+          tmem_st16(t_s + 64 + c * 16, w);
         };
-        weights(1);
+        // the weights take the place of the last 64 columns of S, which go first
+        weights(x[3], 3);
+        tc::tmem_ld32_async(t_s, x[0]);
+        weights(x[2], 2);
         tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_half[s]);
-        load(0, x);
-        weights(0);
+        tc::tmem_wait_ld();
+        tc::tmem_regs(x[0]);
+        tc::tmem_ld32_async(t_s + 32, x[1]);
+        weights(x[0], 0);
+        tc::tmem_wait_ld();
+        tc::tmem_regs(x[1]);
+        weights(x[1], 1);
+        tmem_wait_st();
         sum[0] = fadd2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
-        tmem_wait_st();
       } else if (lane == 0) {
         mbar_arrive(&sm.p_half[s]);
       }
