@@ -169,6 +169,8 @@ def select_variant(name) -> None:
 def lib():
     """The loaded library (built in-tree on first use if needed)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build(variant=_variant)

@@ -6,6 +6,7 @@ namespace kda {
 namespace {
 
 constexpr int PT = 1024;  // threads: one request each per round
+constexpr int EXTEND_CTAS = 8, EXTEND_ONE = 4096;
 
 // Inclusive sums of two values over the block, and both totals.
 struct Scan2 {
@@ -60,6 +61,14 @@ __device__ __forceinline__ int owner(const int* off, int n, int x) {
   return lo;
 }
 
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return (int)r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 __device__ __forceinline__ int clamped_count(const KvPagesParams& p, bool report) {
   const int c = *p.free_count;
   if (c < 0 || c > p.n_pages) {
@@ -71,14 +80,16 @@ __device__ __forceinline__ int clamped_count(const KvPagesParams& p, bool report
 
 // One thread per request and round: page counts and token counts are summed
 // over the block, then the round's tokens and pages are spread over all
-// threads, each finding its request in the sums.
+// threads, each finding its request in the sums.  The CTAs of the cluster
+// each form the same sums, share out tokens and pages, and only the first
+// updates the lengths and the free count, once all have read them.
 __global__ void __launch_bounds__(PT) kv_extend_kernel(KvPagesParams p) {
   __shared__ long long sums[32][2];
   __shared__ int tok_off[PT], page_off[PT], r_len[PT], r_have[PT];  // r_have < 0: not admitted
   const int t = threadIdx.x, page = 1 << p.page_shift;
-  const int count = clamped_count(p, t == 0);
+  const int rank = cluster_rank(), stride = PT * (int)gridDim.x, first = rank * PT + t;
+  const int count = clamped_count(p, first == 0);
   long long tok_base = 0, page_base = 0, taken = 0;
-  if (t == 0) p.cu_seqlens[0] = 0;
   for (int r0 = 0; r0 < p.n_req; r0 += PT) {
     const int b = r0 + t, n_round = min(PT, p.n_req - r0);
     long long n_new = 0, add = 0;
@@ -95,40 +106,46 @@ __global__ void __launch_bounds__(PT) kv_extend_kernel(KvPagesParams p) {
         valid = need <= p.table_cols;
         add = valid ? need - have : 0;
       }
-      if (!valid) set_error(p.err, ERR_INDEX);
+      if (!valid && rank == 0) set_error(p.err, ERR_INDEX);
     }
+    if (gridDim.x > 1) cluster_arrive();  // lengths (and the count) have been read
     const Scan2 s = block_scan2(n_new, add, sums);
     const bool fits = valid && (add == 0 || page_base + s.b <= count);
-    const long long my_tok = tok_base + s.a - n_new;
-    if (b < p.n_req) {
-      // sums past int32 are out of max_tokens' range as well
-      p.cu_seqlens[b + 1] = (int)min(tok_base + s.a, 0x7fffffffLL);
-      p.step_lens[b] = fits ? (int)(len + n_new) : 0;
-      if (fits) p.kv_lens[b] = (int)(len + n_new);
-      if (tok_base + s.a > p.max_tokens && n_new > 0) set_error(p.err, ERR_INDEX);
-    }
-    tok_off[t] = (int)min(my_tok, 0x7fffffffLL);
+    tok_off[t] = (int)min(tok_base + s.a - n_new, 0x7fffffffLL);
     page_off[t] = (int)(s.b - add);
     r_len[t] = len;
     r_have[t] = fits ? have : -1;
     // admitted pages are a prefix of the sums: the first refusal ends it
-    const long long mine = fits && add > 0 ? page_base + s.b : 0;
+    long long top = fits && add > 0 ? page_base + s.b : 0;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
     __syncthreads();
+    if ((t & 31) == 0) sums[t >> 5][0] = top;
+    if (gridDim.x > 1) cluster_wait();
+    if (rank == 0 && b < p.n_req) {
+      // sums past int32 are out of max_tokens' range as well
+      p.cu_seqlens[b + 1] = (int)min(tok_base + s.a, 0x7fffffffLL);
+      p.step_lens[b] = fits ? (int)(len + n_new) : 0;
+      if (fits && n_new > 0) p.kv_lens[b] = (int)(len + n_new);
+      if (tok_base + s.a > p.max_tokens && n_new > 0) set_error(p.err, ERR_INDEX);
+    }
     const long long tok_end = min(tok_base + s.total_a, (long long)p.max_tokens);
     const int pages_end = (int)min(s.total_b, max(0LL, count - page_base));
-    for (int i = t; i < pages_end; i += PT) {
+    for (int i = first; i < pages_end; i += stride) {
       const int r = owner(page_off, n_round, i);
       if (r_have[r] < 0) continue;
       const int col = r_have[r] + i - page_off[r];
       p.table[(int64_t)(r0 + r) * p.table_stride + col] = p.free_pages[count - 1 - (page_base + i)];
     }
-    for (long long i = tok_base + t; i < tok_end; i += PT) {
+#pragma unroll 4
+    for (long long i = tok_base + first; i < tok_end; i += stride) {
       const int r = owner(tok_off, n_round, (int)i);
       int slot = -1;
       if (r_have[r] >= 0) {
         const int pos = r_len[r] + (int)i - tok_off[r], col = pos >> p.page_shift;
-        const long long at = page_base + page_off[r] + col - r_have[r];
-        const int pg = col < r_have[r] ? p.table[(int64_t)(r0 + r) * p.table_stride + col] : p.free_pages[count - 1 - at];
+        const int32_t* from = col < r_have[r] ? p.table + (int64_t)(r0 + r) * p.table_stride + col
+                                              : p.free_pages + (count - 1 - (page_base + page_off[r] + col - r_have[r]));
+        const int pg = *from;
         slot = (pg << p.page_shift) + (pos & (page - 1));
         if (pg < 0 || pg >= p.n_pages) {
           set_error(p.err, ERR_INDEX);
@@ -137,18 +154,16 @@ __global__ void __launch_bounds__(PT) kv_extend_kernel(KvPagesParams p) {
       }
       p.slot_map[i] = slot;
     }
-    long long top = mine;
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
-    __syncthreads();
-    if ((t & 31) == 0) sums[t >> 5][0] = top;
     __syncthreads();
     for (int i = 0; i < 32; ++i) taken = max(taken, sums[i][0]);
     tok_base += s.total_a;
     page_base += s.total_b;
   }
-  for (long long i = tok_base + t; i < p.max_tokens; i += PT) p.slot_map[i] = -1;
-  if (t == 0) *p.free_count = count - (int)taken;
+  for (long long i = tok_base + first; i < p.max_tokens; i += stride) p.slot_map[i] = -1;
+  if (first == 0) {
+    p.cu_seqlens[0] = 0;
+    *p.free_count = count - (int)taken;
+  }
 }
 
 // Requests from the last to the first, one per thread and round.
@@ -220,7 +235,20 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendParams p) {
 
 int launch_kv_extend(const KvPagesParams& p, cudaStream_t stream) {
   trace_begin("kv_extend", stream);
-  kv_extend_kernel<<<1, PT, 0, stream>>>(p);
+  // One cluster: the lengths are updated in place, so the CTAs that share the
+  // tokens out have to agree on when they have been read.
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  const unsigned ctas = p.max_tokens > EXTEND_ONE ? EXTEND_CTAS : 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(PT);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kv_extend_kernel, p);
   trace_end(stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

@@ -19,12 +19,18 @@ D = 128
 _DTYPES = {torch.bfloat16: _native.KDA_DTYPE_BF16, torch.float16: _native.KDA_DTYPE_FP16}
 
 
-def _stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+# The current stream's handle without the object around it: a decode step makes
+# a few of these calls per layer, and the object costs more than a launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _stream(stream, device):
+    return _raw_stream(device) if stream is None else stream.cuda_stream
 
 
 def _int32(t, name, numel=None):
-    if t.dtype != torch.int32 or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 CUDA tensor.")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} must have {numel} entries (got {t.numel()}).")
@@ -32,21 +38,26 @@ def _int32(t, name, numel=None):
 
 
 def _table(t, n_req):
+    """(pointer, row stride, columns)"""
     if t.dtype != torch.int32 or not t.is_cuda:
         raise TypeError("block_table must be an int32 CUDA tensor.")
-    if t.dim() != 2 or t.shape[0] != n_req or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"block_table must be [{n_req}, columns] with contiguous rows (got {tuple(t.shape)}).")
-    return t.data_ptr()
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != n_req or (shape[1] > 1 and stride[1] != 1):
+        raise ValueError(f"block_table must be [{n_req}, columns] with contiguous rows (got {tuple(shape)}).")
+    return t.data_ptr(), stride[0], shape[1]
 
 
 def _rows(t, name, dtype, heads=None):
-    """[T, H, 128] of the cache's type; a size-1 dimension's stride is free."""
+    """(tokens, heads, pointer, token stride, head stride) of [T, H, 128] in the
+    cache's type; a size-1 dimension's stride is free."""
     if t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor of the cache's dtype {dtype} (got {t.dtype} on {t.device}).")
-    if t.dim() != 3 or t.shape[2] != D or t.stride(2) != 1 or (heads is not None and t.shape[1] != heads):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != D or stride[2] != 1 or (heads is not None and shape[1] != heads):
         want = "H" if heads is None else heads
-        raise ValueError(f"{name} must be [T, {want}, 128] with a contiguous last dimension (got {tuple(t.shape)}).")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+        raise ValueError(f"{name} must be [T, {want}, 128] with a contiguous last dimension (got {tuple(shape)}).")
+    n, h, _ = shape
+    return n, h, t.data_ptr(), stride[0] if n > 1 else 0, stride[1] if h > 1 else 0
 
 
 class KvPages:
@@ -60,9 +71,11 @@ class KvPages:
         n = kv_lens.numel()
         g = self._struct = _native.KdaKvPages()
         g.kv_lens = _int32(kv_lens, "kv_lens")
-        g.block_table, g.table_stride = _table(block_table, n), block_table.stride(0)
+        g.block_table, g.table_stride, g.table_cols = _table(block_table, n)
         g.free_pages, g.free_count = _int32(free_pages, "free_pages"), _int32(free_count, "free_count", 1)
-        g.n_req, g.table_cols, g.n_pages, g.page_size = n, block_table.shape[1], free_pages.numel(), page_size
+        g.n_req, g.n_pages, g.page_size = n, free_pages.numel(), page_size
+        self.n_req, self.device = n, kv_lens.device
+        self._index = kv_lens.get_device()
         self.kv_lens, self.block_table = kv_lens, block_table
         self.free_pages, self.free_count, self.page_size = free_pages, free_count, page_size
         self._ref = ctypes.byref(g)
@@ -96,6 +109,7 @@ class KvCache:
         c.dtype = _DTYPES[k.dtype]
         c.n_pages, c.page_size, c.hkv = k.shape[:3]
         self.k, self.v, self.dtype, self.n_kv_heads = k, v, k.dtype, k.shape[2]
+        self._index = k.get_device()
         self._ref = ctypes.byref(c)
 
 
@@ -106,34 +120,42 @@ def kda_kv_extend(pages: KvPages, new_lens, max_tokens: int, *, cu_seqlens=None,
     [n_req + 1], slot_map [max_tokens], step_lens [n_req]), int32: the packed
     layout, each token's slot (-1 where its request found no pages), and the
     lengths that attention takes (0 where the request was not admitted)."""
-    n = pages.kv_lens.numel()
-    i32 = dict(dtype=torch.int32, device=pages.kv_lens.device)
-    cu_seqlens = torch.empty(n + 1, **i32) if cu_seqlens is None else cu_seqlens
-    slot_map = torch.empty(max_tokens, **i32) if slot_map is None else slot_map
-    step_lens = torch.empty(n, **i32) if step_lens is None else step_lens
-    _native.check(_native.lib().kda_kv_extend(
-        pages._ref, _int32(new_lens, "new_lens", n), _int32(cu_seqlens, "cu_seqlens", n + 1),
-        _int32(slot_map, "slot_map", max_tokens), max_tokens, _int32(step_lens, "step_lens", n), _stream(stream)))
+    n = pages.n_req
+    new = _int32(new_lens, "new_lens", n)
+    if cu_seqlens is None:
+        cu_seqlens = torch.empty(n + 1, dtype=torch.int32, device=pages.device)
+    if slot_map is None:
+        slot_map = torch.empty(max_tokens, dtype=torch.int32, device=pages.device)
+    if step_lens is None:
+        step_lens = torch.empty(n, dtype=torch.int32, device=pages.device)
+    rc = _native.lib().kda_kv_extend(
+        pages._ref, new, _int32(cu_seqlens, "cu_seqlens", n + 1), _int32(slot_map, "slot_map", max_tokens), max_tokens,
+        _int32(step_lens, "step_lens", n), _stream(stream, pages._index))
+    if rc:
+        _native.check(rc)
     return cu_seqlens, slot_map, step_lens
 
 
 def kda_kv_truncate(pages: KvPages, keep_lens, *, stream=None) -> None:
     """Keep the first ``keep_lens`` [n_req] tokens of each request (int32,
     CUDA) and hand the pages past them back."""
-    _native.check(_native.lib().kda_kv_truncate(
-        pages._ref, _int32(keep_lens, "keep_lens", pages.kv_lens.numel()), _stream(stream)))
+    rc = _native.lib().kda_kv_truncate(pages._ref, _int32(keep_lens, "keep_lens", pages.n_req),
+                                       _stream(stream, pages._index))
+    if rc:
+        _native.check(rc)
 
 
 def kda_kv_append(cache: KvCache, k, v, slot_map, *, stream=None) -> None:
     """Write k and v [T, Hkv, 128] to the slots ``slot_map`` [T] (int32, -1
     skips the token)."""
-    kp, kt, kh = _rows(k, "k", cache.dtype, cache.n_kv_heads)
-    vp, vt, vh = _rows(v, "v", cache.dtype, cache.n_kv_heads)
-    t = k.shape[0]
-    if v.shape[0] != t:
+    t, _, kp, kt, kh = _rows(k, "k", cache.dtype, cache.n_kv_heads)
+    tv, _, vp, vt, vh = _rows(v, "v", cache.dtype, cache.n_kv_heads)
+    if tv != t:
         raise ValueError("k and v must have the same number of tokens.")
-    _native.check(_native.lib().kda_kv_append(
-        cache._ref, kp, kt, kh, vp, vt, vh, _int32(slot_map, "slot_map", t), t, _stream(stream)))
+    rc = _native.lib().kda_kv_append(cache._ref, kp, kt, kh, vp, vt, vh, _int32(slot_map, "slot_map", t), t,
+                                     _stream(stream, cache._index))
+    if rc:
+        _native.check(rc)
 
 
 def paged_attention_workspace(device=None) -> torch.Tensor:
@@ -153,8 +175,8 @@ def kda_paged_attention(cache: KvCache, q, cu_seqlens, kv_lens, block_table, *, 
     them, and the first ``sinks``.  Returns (out [T, Hq, 128], lse fp32
     [T, Hq] or None).  ``workspace``: :func:`paged_attention_workspace`, made
     for the call when not given."""
-    qp, qt, qh = _rows(q, "q", cache.dtype)
-    t, hq, n = q.shape[0], q.shape[1], kv_lens.numel()
+    t, hq, qp, qt, qh = _rows(q, "q", cache.dtype)
+    n = kv_lens.numel()
     if out is None:
         out = torch.empty((t, hq, D), dtype=q.dtype, device=q.device)
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or not out.is_cuda:
@@ -167,9 +189,12 @@ def kda_paged_attention(cache: KvCache, q, cu_seqlens, kv_lens, block_table, *, 
         workspace = paged_attention_workspace(q.device)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or not workspace.is_cuda:
         raise ValueError("workspace must be a contiguous uint8 CUDA tensor.")
-    _native.check(_native.lib().kda_paged_attention(
+    table, table_stride, cols = _table(block_table, n)
+    rc = _native.lib().kda_paged_attention(
         cache._ref, qp, qt, qh, hq, t, out.data_ptr(), None if lse is None else lse.data_ptr(),
-        _int32(cu_seqlens, "cu_seqlens", n + 1), _int32(kv_lens, "kv_lens"), _table(block_table, n),
-        block_table.stride(0), block_table.shape[1], n, D ** -0.5 if scale is None else scale, window, sinks,
-        workspace.data_ptr(), workspace.numel(), _stream(stream)))
+        _int32(cu_seqlens, "cu_seqlens", n + 1), _int32(kv_lens, "kv_lens"), table, table_stride, cols, n,
+        D ** -0.5 if scale is None else scale, window, sinks, workspace.data_ptr(), workspace.numel(),
+        _stream(stream, cache._index))
+    if rc:
+        _native.check(rc)
     return out, lse
