@@ -232,6 +232,12 @@ __device__ __forceinline__ void attend_row(const AttentionParams& p, int b, int 
 }
 
 // --- the line of work ----------------------------------------------------------------
+// The line's places are 64 bits, but seldom need them: a 64-bit division costs
+// several times a 32-bit one, and a single token's call waits for a few.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
 // A request's tokens and lengths, checked; n = 0: no tokens to run.
 __device__ __forceinline__ void request(const AttentionParams& p, int b, int& t0, int& n, int& kv, bool report) {
   t0 = p.cu_seqlens[b];
@@ -363,7 +369,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
     // keys and values
     for (int i = it.i0; i < it.i1; ++i, ++tiles) {
       const int row = (list_tile(it, i) * KT) & (page - 1) & ~(box - 1);
-      const int c_page = pg < 0 ? p.a.n_pages : pg;
+      const int c_page = __shfl_sync(0xffffffffu, pg < 0 ? p.a.n_pages : pg, lane >> 1);
       const unsigned held = __ballot_sync(0xffffffffu, pg >= 0);
       pg = page_of(i + 1);
 #pragma unroll 1
@@ -377,12 +383,9 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
           mbar_arrive_expect_tx(&sm.kv_full[st], TILE_BYTES);
         }
         __syncwarp();
-        if (lane < p.boxes) {
-          unsigned char* dst = kv_smem + st * TILE_BYTES + lane * box * 128;
-          const CUtensorMap* map = kv == 0 ? &maps.k : &maps.v;
-          tma_load4(dst, map, 0, row, it.kvh, c_page, &sm.kv_full[st]);
-          tma_load4(dst + HALF_BYTES, map, 64, row, it.kvh, c_page, &sm.kv_full[st]);
-        }
+        if (lane < 2 * p.boxes)  // a lane a box: page, half
+          tma_load4(kv_smem + st * TILE_BYTES + (lane & 1) * HALF_BYTES + (lane >> 1) * box * 128, kv == 0 ? &maps.k : &maps.v,
+                    (lane & 1) * 64, row, it.kvh, c_page, &sm.kv_full[st]);
       }
       if (!ok) break;
     }
@@ -591,43 +594,49 @@ __device__ __forceinline__ void plan_role(const Params& p, Smem& sm, int cta, lo
     ok = __shfl_sync(0xffffffffu, ok, 0);
   };
   if (u0 < u1) {
-    int h = (int)(u0 / total), b = sm.start_b;
+    int h = (int)quotient(u0, total), b = sm.start_b;
     long long at = h * total + sm.start_before;  // of request b's first block
     while (ok && at < u1) {
       int t0, n, kv;
       request(p.a, b, t0, n, kv, false);
       const int blocks = n_blocks(p, n);
+      // block k, whose place on the line is [s, s + its cost)
+      auto emit = [&](int k, long long s) {
+        Item it;
+        const int tiles = block_tiles(p, n, kv, k, it);
+        const long long e = s + max(1, tiles);
+        it.b = b;
+        it.kvh = h;
+        it.tok = t0 + k * 2 * p.tile_tok;
+        it.kv = kv;
+        it.i0 = (int)max(0LL, u0 - s);
+        it.i1 = (int)min((long long)tiles, u1 - s);
+        it.first = (int)quotient(s, piece);
+        it.parts = (int)quotient(e - 1, piece) - it.first + 1;
+        it.part = cta - it.first;
+        tile_range(p, it, 0);
+        tile_range(p, it, 1);
+        post(it);
+      };
       for (int k0 = 0; ok && k0 < blocks && at < u1; k0 += 32) {
+        // 32 blocks at once, unless the request has but one
         long long upto = k0 + lane < blocks ? block_cost(p, n, kv, k0 + lane) : 0;
         const long long mine = upto;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-          const long long x = __shfl_up_sync(0xffffffffu, upto, m);
-          if (lane >= m) upto += x;
+        if (blocks > 1) {
+#pragma unroll 1
+          for (int m = 1; m < 32; m <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, upto, m);
+            if (lane >= m) upto += x;
+          }
         }
         const long long begin = at + upto - mine;
         unsigned todo = __ballot_sync(0xffffffffu, mine > 0 && begin < u1 && begin + mine > u0);
         while (ok && todo) {
           const int src = __ffs(todo) - 1;
           todo &= todo - 1;
-          const long long s = __shfl_sync(0xffffffffu, begin, src);
-          Item it;
-          const int k = k0 + src, tiles = block_tiles(p, n, kv, k, it);
-          const long long e = s + max(1, tiles);
-          it.b = b;
-          it.kvh = h;
-          it.tok = t0 + k * 2 * p.tile_tok;
-          it.kv = kv;
-          it.i0 = (int)max(0LL, u0 - s);
-          it.i1 = (int)min((long long)tiles, u1 - s);
-          it.first = (int)(s / piece);
-          it.parts = (int)((e - 1) / piece) - it.first + 1;
-          it.part = cta - it.first;
-          tile_range(p, it, 0);
-          tile_range(p, it, 1);
-          post(it);
+          emit(k0 + src, __shfl_sync(0xffffffffu, begin, src));
         }
-        at += __shfl_sync(0xffffffffu, upto, 31);
+        at += __shfl_sync(0xffffffffu, upto, min(31, blocks - 1 - k0));
       }
       if (++b == p.a.n_req) {
         b = 0;
@@ -661,13 +670,18 @@ __device__ __forceinline__ long long measure_line(const Params& p, Smem& sm, int
     total += sm.sums[w];
   }
   const long long all = total * p.a.hkv;
-  const long long piece = max((all + p.n_cta - 1) / p.n_cta, (long long)p.min_piece);
+  const long long piece = max(quotient(all + p.n_cta - 1, p.n_cta), (long long)p.min_piece);
   const long long u0 = cta * piece;
   if (u0 < all) {
-    const long long w0 = u0 % total;
+    const long long w0 = u0 - quotient(u0, total) * total;
     long long before = upto - cost;
     const bool mine = before <= w0 && w0 < upto;
-    if (__any_sync(0xffffffffu, mine)) {
+    if (each == 1) {
+      if (mine) {
+        sm.start_b = t;
+        sm.start_before = before;
+      }
+    } else if (__any_sync(0xffffffffu, mine)) {
       bool found = false;
       for (int j = 0; j < each; ++j) {
         const long long c = request_cost(p, t * each + j, t * each + j < p.a.n_req, false);
@@ -702,15 +716,18 @@ __device__ __forceinline__ void join_parts(const Params& p, Smem& sm, int s, con
   named_bar_sync(1 + s, 128);
   // a unit: 8 rows by 8 pieces; a lane: one row, two pieces
   for (int u = warp; u < (n_rows + 7) / 8 * 4; u += 4) {
-    const int row = (u >> 2) * 8 + (lane & 7), c = (u & 3) * 8 + (lane >> 3);
-    if (row >= n_rows) continue;
+    const bool real = (u >> 2) * 8 + (lane & 7) < n_rows;
+    const int row = min((u >> 2) * 8 + (lane & 7), n_rows - 1), c = (u & 3) * 8 + (lane >> 3);
+    // the four lanes of a row look through the references together
     float top = -CUDART_INF_F;
 #pragma unroll 4
-    for (int k = 0; k < parts; ++k) top = fmaxf(top, __ldcg(&p.part_ml[part_row(k, row)]).x);
+    for (int k = lane >> 3; k < parts; k += 4) top = fmaxf(top, __ldcg(&p.part_ml[part_row(k, row)]).x);
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
     float l = 0.f, o[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < parts; ++k) {
       const size_t at = part_row(k, row);
       const float2 ml = __ldcg(&p.part_ml[at]);
@@ -723,6 +740,7 @@ __device__ __forceinline__ void join_parts(const Params& p, Smem& sm, int s, con
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] += some ? w * z[j] : 0.f;
     }
+    if (!real) continue;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     float poison = 0.f;
 #pragma unroll
@@ -912,7 +930,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
         ++merges;
         // rows of 512 bytes, their 16-byte pieces rotated by the row: no bank conflicts
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 4 && any_row; ++c) {
           float v[32];
           tc::tmem_ld32(t_o + c * 32, v);
           if (valid) {
@@ -956,7 +974,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
     const size_t part_row = (((size_t)blockIdx.x * 2 + (it.part == 0 ? 1 : 0)) * 2 + tile) * ROWS + r;
     float poison = 0.f;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < 4 && any_row; ++c) {
       float v[32];
       if (stepped) {
         tc::tmem_ld32(t_o + c * 32, v);
@@ -987,8 +1005,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
                              act_pack2<FP16>(v[8 * j + 4], v[8 * j + 5]), act_pack2<FP16>(v[8 * j + 6], v[8 * j + 7]));
       } else if (valid) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          __stcg(&p.part_o[part_piece(part_row, c * 8 + j)], make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+        for (int j = 0; j < 8; ++j)  // pieces are 8 apart
+          __stcg(p.part_o + part_piece(part_row, 0) + (c * 8 + j) * 8, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
       }
       __syncwarp();
     }
@@ -1016,17 +1034,19 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
       }
     } else {
       if (valid) __stcg(&p.part_ml[part_row], make_float2(m2, l));
-      __threadfence();
       named_bar_sync(bar, 128);
       if (r == 0) {
+        __threadfence();  // for the whole warpgroup's stores, which the barrier put before it
         unsigned* counter = &p.counters[it.first * 2 + tile];
         const bool last = atomicAdd(counter, 1u) + 1 == (unsigned)it.parts;
-        if (last) *counter = 0;
+        if (last) {
+          *counter = 0;
+          __threadfence();
+        }
         sm.last[s] = last;
       }
       named_bar_sync(bar, 128);
       if (sm.last[s]) {
-        __threadfence();
         join_parts<FP16>(p, sm, s, it, tile, min(p.tile_tok, it.n_tok - tile * p.tile_tok) * p.group);
       }
     }
@@ -1072,6 +1092,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc::tmem_alloc(&sm.tmem, 512);
     tc::tmem_relinquish();
   }
+  // the set-up above overlaps the end of the kernel before; what it wrote is read below
+  griddep_launch_dependents();
+  griddep_wait();
   const long long piece = measure_line(p, sm, blockIdx.x);
   tc::fence_before_sync();
   __syncthreads();
@@ -1167,9 +1190,19 @@ int launch_attention(const AttentionParams& a, bool fp16, void* workspace, cudaS
       !encode(enc, &maps.q, fp16, a.q, p.group, a.q_sh, a.hkv, a.q_sh * p.group, a.t_total, a.q_st, p.group, 1, p.tile_tok) ||
       !encode(enc, &maps.q1, fp16, a.q, p.group, a.q_sh, a.hkv, a.q_sh * p.group, a.t_total, a.q_st, p.group, 1, 1))
     return -1;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(p.n_cta);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   trace_begin("attention", stream);
-  if (fp16) attention_kernel<true><<<p.n_cta, THREADS, SMEM_BYTES, stream>>>(p, maps);
-  else attention_kernel<false><<<p.n_cta, THREADS, SMEM_BYTES, stream>>>(p, maps);
+  if (fp16) cudaLaunchKernelEx(&cfg, attention_kernel<true>, p, maps);
+  else cudaLaunchKernelEx(&cfg, attention_kernel<false>, p, maps);
   trace_end(stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
