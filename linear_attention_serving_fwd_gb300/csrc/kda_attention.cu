@@ -42,8 +42,9 @@ constexpr int TILE_BYTES = KT * D * 2;
 constexpr int HALF_BYTES = TILE_BYTES / 2;  // 64 of the 128 dimensions
 constexpr int RING = 4;        // items ahead
 constexpr int MASKS = 8;       // page masks of the K tiles in flight
-constexpr int THREADS = 384;
-constexpr int LOAD_WARP = 8, PLAN_WARP = 9, MMA_WARP = 10;  // MMA_WARP + 1: the second stream's
+constexpr int THREADS = 640;
+constexpr int SOFTMAX_WARPS = 16;  // two warpgroups a stream
+constexpr int LOAD_WARP = 16, PLAN_WARP = 17, MMA_WARP = 18;  // MMA_WARP + 1: the second stream's
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // The running reference follows the row's maximum only when that has grown by
 // 2^GROWTH: until then weights up to 2^GROWTH stand in for ones, and the
@@ -70,11 +71,10 @@ struct Smem {
   uint64_t kv_full[STAGES], kv_empty[STAGES];
   uint64_t ring_full[RING], ring_empty[RING];
   uint64_t q_full, q_empty, q_read, merge_full;
-  uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t turn[2], drained[2];
   Item ring[RING];
   int page_mask[MASKS];
-  float2 merge_ml[ROWS];
   long long sums[THREADS / 32];
   long long total;
   int start_b;
@@ -82,7 +82,8 @@ struct Smem {
   uint32_t tmem;
   int dead;
   int last[2];
-  unsigned poisoned[2][4];  // rows of a joined tile
+  unsigned poisoned[2][2][4];  // rows of a tile with a result that is not finite, by stream and half
+  float share[2][2][ROWS];     // what the halves of a row tell each other
 };
 
 struct Params {
@@ -96,28 +97,28 @@ struct Params {
   float4* part_o;          // [n_cta][2 slots][2 tiles][ROWS / 8][32][8]: 16-byte pieces of 8 rows side by side
 };
 
+// hardware barriers: a pair of warps that share rows (stream, quarter), a stream's eight warps
+constexpr int PAIR_BAR = 1, STREAM_BAR = 9;
+
 // --- waits ---------------------------------------------------------------------
-// A wait that expires marks the CTA: from then on every wait of it returns at
-// once, and the roles run out.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* dead, unsigned* err) {
+// A wait that expires (bounded as all waits are) marks the CTA: its other waits
+// then return at once, and the roles run out.  What they still do stays inside
+// the CTA's own memory; only the ring of items is not read on.
+__device__ __noinline__ void wait_slow(uint64_t* bar, uint32_t parity, volatile int* dead, unsigned* err) {
   uint64_t t0 = 0;
-  for (uint32_t i = 0; i < WAIT_CAP; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*dead) return false;
+  for (uint32_t i = 0; i < WAIT_CAP && !*dead; ++i) {
+    if (mbar_try_wait(bar, parity)) return;
     const uint64_t t = globaltimer_ns();
     if (t0 == 0) t0 = t;
     else if (t - t0 > WAIT_NS) break;
   }
   *dead = 1;
   set_error(err, ERR_TIMEOUT);
-  return false;
 }
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Smem& sm, unsigned* err) {
-#pragma unroll 1
-  for (int i = 0; i < 16; ++i)  // most waits are short: parking and waking costs more
-    if (mbar_test_wait(bar, parity)) return true;
-  return wait_slow(bar, parity, &sm.dead, err);
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, Smem& sm, unsigned* err) {
+  if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, &sm.dead, err);
 }
+__device__ __forceinline__ bool is_dead(const Smem& sm) { return *(const volatile int*)&sm.dead != 0; }
 // by a whole warp, which runs warp-wide instructions next
 __device__ __forceinline__ void warp_wait(uint64_t* bar, uint32_t parity, Smem& sm, unsigned* err) {
   wait(bar, parity, sm, err);
@@ -318,12 +319,10 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
   const int lane = threadIdx.x & 31;
   unsigned* err = p.a.err;
   uint32_t fills = 0, tiles = 0, q_count = 0;
-  bool ok = true;
-  for (uint32_t items = 0; ok; ++items) {
+  for (uint32_t items = 0;; ++items) {
     const uint32_t slot = items % RING;
-    if (!wait(&sm.ring_full[slot], (items / RING) & 1, sm, err)) ok = false;
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
+    wait(&sm.ring_full[slot], (items / RING) & 1, sm, err);
+    if (__any_sync(0xffffffffu, is_dead(sm))) break;
     const Item it = sm.ring[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.ring_empty[slot]);
@@ -347,9 +346,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
     int pg = page_of(it.i0);
     // queries
     const bool two = it.n_tok > p.tile_tok;
-    if (lane == 0 && !wait(&sm.q_empty, (q_count & 1) ^ 1, sm, err)) ok = false;
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (!ok) break;
+    warp_wait(&sm.q_empty, (q_count & 1) ^ 1, sm, err);
     ++q_count;
     const bool single = it.n_tok <= 8;
     const uint32_t box_bytes = (uint32_t)p.group * 128u;
@@ -375,9 +372,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++fills) {
         const uint32_t st = fills % STAGES;
-        if (lane == 0 && !wait(&sm.kv_empty[st], ((fills / STAGES) & 1) ^ 1, sm, err)) ok = false;
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
+        warp_wait(&sm.kv_empty[st], ((fills / STAGES) & 1) ^ 1, sm, err);
         if (lane == 0) {
           if (kv == 0) *(volatile int*)&sm.page_mask[tiles % MASKS] = (int)held;
           mbar_arrive_expect_tx(&sm.kv_full[st], TILE_BYTES);
@@ -387,10 +382,9 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
           tma_load4(kv_smem + st * TILE_BYTES + (lane & 1) * HALF_BYTES + (lane >> 1) * box * 128, kv == 0 ? &maps.k : &maps.v,
                     (lane & 1) * 64, row, it.kvh, c_page, &sm.kv_full[st]);
       }
-      if (!ok) break;
     }
   }
-  if (!ok && lane == 0) {
+  if (is_dead(sm) && lane == 0) {
     // copies in flight land before the CTA ends
     for (uint32_t f = fills > STAGES ? fills - STAGES : 0; f < fills; ++f)
       mbar_wait_bounded(&sm.kv_full[f % STAGES], (f / STAGES) & 1, err);
@@ -431,13 +425,10 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
                                          uint32_t bf16) {
   unsigned* err = p.a.err;
   const uint32_t id_qk = tc::idesc_f16(ROWS, KT, bf16), id_pv = tc::idesc_f16(ROWS, D, bf16) | (1u << 16);
-  const uint32_t t_s = tmem + s * 128, t_p = t_s + 64, t_o = tmem + 256 + s * 128;
+  const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * 128;
   Stage next;  // of list index i0 of the next item
   uint32_t q_parity = 0, p_parity = 0, o_parity = 1;
-  bool ok = true;
-  auto await = [&](uint64_t* bar, uint32_t parity) {
-    if (ok) ok = __all_sync(0xffffffffu, wait(bar, parity, sm, err));
-  };
+  auto await = [&](uint64_t* bar, uint32_t parity) { warp_wait(bar, parity, sm, err); };
   // In blocks of two tiles the streams take turns at the tensor cores, key tile
   // by key tile: a product of one and its next scores go in a row.  Left to mix,
   // both streams' products finish late together, and both softmaxes run while
@@ -448,10 +439,10 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
     if (elect_one()) mbar_arrive(&sm.turn[s ^ 1]);
     __syncwarp();
   };
-  for (uint32_t items = 0; ok; ++items) {
+  for (uint32_t items = 0;; ++items) {
     const uint32_t slot = items % RING;
     await(&sm.ring_full[slot], (items / RING) & 1);
-    if (!ok) break;
+    if (__any_sync(0xffffffffu, is_dead(sm))) break;
     const Item& from = sm.ring[slot];
     Item it;
     it.b = uniform(from.b);
@@ -508,7 +499,6 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
       }
       if (!scored) {
         await(&sm.kv_full[st.at], st.parity);
-        if (!ok) break;
         tc::fence_after_sync();
         scores(i, st);
       }
@@ -522,20 +512,9 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
         await(&sm.o_free[s], o_parity);
         o_parity ^= 1;
       }
-      // the weights come in halves, of the last 64 keys first
       const uint64_t vd = smem_desc_mn(kv_addr + sv.at * TILE_BYTES);
-      await(&sm.p_half[s], p_parity);
-      if (!ok) break;
-      tc::fence_after_sync();
-      if (elect_one()) {
-#pragma unroll
-        for (int j = KT / 32; j < KT / 16; ++j)  // 16 keys: two 8-row groups of V
-          mma_f16_ts(t_o, t_p + j * 8, vd + j * (2048 >> 4), id_pv, (j > KT / 32 || !first) ? 1u : 0u);
-      }
-      __syncwarp();
       await(&sm.p_full[s], p_parity);
       p_parity ^= 1;
-      if (!ok) break;
       tc::fence_after_sync();
       if (two) {
         await(&sm.turn[s], turn);
@@ -543,7 +522,8 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
       }
       if (elect_one()) {
 #pragma unroll
-        for (int j = 0; j < KT / 32; ++j) mma_f16_ts(t_o, t_p + j * 8, vd + j * (2048 >> 4), id_pv, 1u);
+        for (int j = 0; j < KT / 16; ++j)  // 16 keys: two 8-row groups of V
+          mma_f16_ts(t_o, t_s + (j >> 2) * 64 + (j & 3) * 8, vd + j * (2048 >> 4), id_pv, (j > 0 || !first) ? 1u : 0u);
         tc::mma_commit(&sm.kv_empty[sv.at]);
       }
       __syncwarp();
@@ -584,7 +564,8 @@ __device__ __forceinline__ void plan_role(const Params& p, Smem& sm, int cta, lo
   auto post = [&](const Item& it) {
     const uint32_t slot = items % RING;
     if (lane == 0) {
-      ok = wait(&sm.ring_empty[slot], ((items / RING) & 1) ^ 1, sm, err);
+      wait(&sm.ring_empty[slot], ((items / RING) & 1) ^ 1, sm, err);
+      ok = !is_dead(sm);
       if (ok) {
         sm.ring[slot] = it;
         mbar_arrive(&sm.ring_full[slot]);
@@ -706,16 +687,16 @@ __device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xfffff
 // read, whole lines.
 __device__ __forceinline__ size_t part_piece(size_t row, int c) { return ((row >> 3) * 32 + c) * 8 + (row & 7); }
 
-// Joins a tile's parts, by the warpgroup that finished the last of them.
+// Joins a tile's parts, by the stream's warpgroups that finished the last of them.
 template <bool FP16>
 __device__ __forceinline__ void join_parts(const Params& p, Smem& sm, int s, const Item& it, int tile, int n_rows) {
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 7, bar = STREAM_BAR + s;
   const int parts = it.parts, first = it.first;
   auto part_row = [&](int k, int row) { return (((size_t)(first + k) * 2 + (k == 0 ? 1 : 0)) * 2 + tile) * ROWS + row; };
-  if ((threadIdx.x & 127) < 4) sm.poisoned[s][threadIdx.x & 3] = 0;
-  named_bar_sync(1 + s, 128);
+  if ((threadIdx.x & 255) < 4) sm.poisoned[s][0][threadIdx.x & 3] = 0;
+  named_bar_sync(bar, 256);
   // a unit: 8 rows by 8 pieces; a lane: one row, two pieces
-  for (int u = warp; u < (n_rows + 7) / 8 * 4; u += 4) {
+  for (int u = warp; u < (n_rows + 7) / 8 * 4; u += 8) {
     const bool real = (u >> 2) * 8 + (lane & 7) < n_rows;
     const int row = min((u >> 2) * 8 + (lane & 7), n_rows - 1), c = (u & 3) * 8 + (lane >> 3);
     // the four lanes of a row look through the references together
@@ -748,7 +729,7 @@ __device__ __forceinline__ void join_parts(const Params& p, Smem& sm, int s, con
       o[j] *= inv;
       poison += o[j] * 0.f;  // NaN from then on when one is not finite
     }
-    if (poison != 0.f) atomicOr(&sm.poisoned[s][row >> 5], 1u << (row & 31));
+    if (poison != 0.f) atomicOr(&sm.poisoned[s][0][row >> 5], 1u << (row & 31));
     const int tok = it.tok + tile * p.tile_tok + row / p.group, head = it.kvh * p.group + row % p.group;
     __nv_bfloat16* out = p.a.out + ((int64_t)tok * p.a.hq + head) * D;
     *reinterpret_cast<uint2*>(out + c * 4) = make_uint2(act_pack2<FP16>(o[0], o[1]), act_pack2<FP16>(o[2], o[3]));
@@ -757,8 +738,8 @@ __device__ __forceinline__ void join_parts(const Params& p, Smem& sm, int s, con
       p.a.lse[(int64_t)tok * p.a.hq + head] = l == 0.f ? -CUDART_INF_F : (top + log2f(l) - WEIGHT_EXP<FP16>) * LN2;
   }
   __syncwarp();
-  named_bar_sync(1 + s, 128);
-  unsigned bad = sm.poisoned[s][warp];
+  named_bar_sync(bar, 256);
+  unsigned bad = warp < 4 ? sm.poisoned[s][0][warp] : 0;
   while (bad) {
     const int row = warp * 32 + __ffs(bad) - 1;
     bad &= bad - 1;
@@ -768,12 +749,14 @@ __device__ __forceinline__ void join_parts(const Params& p, Smem& sm, int s, con
 }
 
 template <bool FP16>
-__device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, unsigned char* q_smem, unsigned char* kv_smem,
+__device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned char* q_smem, unsigned char* kv_smem,
                                              uint32_t tmem) {
   unsigned* err = p.a.err;
-  const int r = threadIdx.x & 127, lane = r & 31, bar = 1 + s;
+  const int s = threadIdx.x >> 8, half = (threadIdx.x >> 7) & 1;  // stream; half of the tile's keys, and of the dimensions
+  const int r = threadIdx.x & 127, lane = r & 31, quarter = r >> 5;
+  const int bar = STREAM_BAR + s, pair = PAIR_BAR + s * 4 + quarter;
   const uint32_t lane_base = tmem + ((uint32_t)(r & 96) << 16);
-  const uint32_t t_s = lane_base + s * 128, t_o = lane_base + 256 + s * 128;
+  const uint32_t t_s = lane_base + s * 128 + half * 64, t_o = lane_base + 256 + s * 128 + half * 64;
   const int row_tok = r / p.group, row_head = r % p.group;
   const float sl = p.a.scale * LOG2E;
   const int all_held = (1 << p.boxes) - 1;
@@ -781,8 +764,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
   uint32_t fills = 0, tiles = 0, s_count = 0, o_count = 0, merges = 0;
   for (uint32_t items = 0;; ++items) {
     const uint32_t slot = items % RING;
-    const bool got = wait(&sm.ring_full[slot], (items / RING) & 1, sm, err);
-    if (named_bar_or(bar, 128, !got)) break;
+    wait(&sm.ring_full[slot], (items / RING) & 1, sm, err);
+    if (named_bar_or(bar, 256, is_dead(sm))) break;
     const Item& it = sm.ring[slot];
     if (it.b < 0) break;
     const bool two = it.n_tok > p.tile_tok;
@@ -796,38 +779,40 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
     const int hi_min = __reduce_min_sync(0xffffffffu, valid ? hi : 0x7fffffff);
     const int lo_max = __reduce_max_sync(0xffffffffu, valid ? lo : 0);
     const int sink_min = __reduce_min_sync(0xffffffffu, valid ? sink : 0x7fffffff);
-    float m = -CUDART_INF_F, l = 0.f;
+    float m = -CUDART_INF_F, l = 0.f;  // m is the row's, l this half's
     bool stepped = false;
     for (int i = two ? i0 : i0 + s; i < i1; i += two ? 1 : 2) {
-      const int t = list_tile(it, i), key = t * KT;
       if (two && !active(it.act[s], i)) continue;
+      const int key = list_tile(it, i) * KT + half * 64;
       warp_wait(&sm.s_full[s], s_count & 1, sm, err);
       ++s_count;
       tc::fence_after_sync();
-      if (key + KT > kv) {
-        // the tile's rows past the cached tokens hold whatever was there: zeros
-        // there keep the products finite
+      if (key + 64 > kv) {
+        // the rows past the cached tokens hold whatever was there: zeros there
+        // keep the products finite
         const uint32_t f = fills + 2 * (i - i0) + 1;
         wait(&sm.kv_full[f % STAGES], (f / STAGES) & 1, sm, err);
-        unsigned char* v = kv_smem + (f % STAGES) * TILE_BYTES + (kv - key) * 128;
-        for (int c = r; c < (KT - (kv - key)) * 16; c += 128)
+        const int from = max(0, kv - key);
+        unsigned char* v = kv_smem + (f % STAGES) * TILE_BYTES + (half * 64 + from) * 128;
+        for (int c = r; c < (64 - from) * 16; c += 128)
           *reinterpret_cast<int4*>(v + ((c >> 3) & 1) * HALF_BYTES + (c >> 4) * 128 + (c & 7) * 16) = make_int4(0, 0, 0, 0);
         fence_proxy_async_smem();
+        __syncwarp();
       }
       if (any_row) {
         const int held = *(volatile int*)&sm.page_mask[(tiles + i - i0) % MASKS];
-        const bool whole = held == all_held && key + KT <= hi_min && (key >= lo_max || key + KT <= sink_min);
+        const bool whole = held == all_held && key + 64 <= hi_min && (key >= lo_max || key + 64 <= sink_min);
         if (!whole) {
           // hidden scores become -inf where they are
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) {
             uint32_t x[32];
             tc::tmem_ld32_async(t_s + c * 32, x);
-            const int k0 = key + c * 32;
+            const int k0 = key + c * 32, box = half * 2 + c;
             uint32_t seen = bits_below(hi - k0) & (~bits_below(lo - k0) | bits_below(sink - k0));
             if (box_shift == 4)
-              seen &= ((held >> (2 * c)) & 1 ? 0xffffu : 0u) | ((held >> (2 * c + 1)) & 1 ? 0xffff0000u : 0u);
-            else if (!((held >> ((c * 32) >> box_shift)) & 1))
+              seen &= ((held >> (2 * box)) & 1 ? 0xffffu : 0u) | ((held >> (2 * box + 1)) & 1 ? 0xffff0000u : 0u);
+            else if (!((held >> ((box * 32) >> box_shift)) & 1))
               seen = 0;
             tc::tmem_wait_ld();
             tc::tmem_regs(x);
@@ -837,32 +822,35 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
           }
           tmem_wait_st();
         }
-        // S is read twice: for the maximum all 128 columns at once; the last 64
-        // stay for their weights, the first 64 come again, 32 at a time and
-        // ahead of their use, so that what is live fits the registers
-        uint32_t x[4][32];
+        uint32_t x[32];
+        float top[2] = {m, m};
+        auto load = [&](int c) {
+          tc::tmem_ld32_async(t_s + c * 32, x);
+          tc::tmem_wait_ld();
+          tc::tmem_regs(x);
+        };
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tc::tmem_ld32_async(t_s + c * 32, x[c]);
-        tc::tmem_wait_ld();
+        for (int c = 0; c < 2; ++c) {
+          load(c);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tc::tmem_regs(x[c]);
-        float top[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          top[c] = max3(m, __uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
-#pragma unroll
-          for (int j = 2; j < 32; j += 2) top[c] = max3(top[c], __uint_as_float(x[c][j]), __uint_as_float(x[c][j + 1]));
+          for (int j = 0; j < 32; j += 4) {
+            top[0] = max3(top[0], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+            top[1] = max3(top[1], __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+          }
         }
-        const float m_new = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+        float m_new = fmaxf(top[0], top[1]);
         // m = -inf: nothing seen yet, any first maximum is taken (-inf - -inf
         // compares false).  Rows past the block hold anything and have no say.
-        if (__any_sync(0xffffffffu, valid && (m_new - m) * sl > GROWTH)) {
+        if (named_bar_or(pair, 64, valid && (m_new - m) * sl > GROWTH)) {
+          sm.share[s][half][r] = m_new;
+          named_bar_sync(pair, 64);
+          m_new = fmaxf(m_new, sm.share[s][half ^ 1][r]);
           const float corr = m_new == -CUDART_INF_F ? 1.f : ex2((m - m_new) * sl);
           m = m_new;
           l *= corr;
           if (stepped) {
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < 4; ++c) {
               uint32_t y[16];
               tc::tmem_ld16_async(t_o + c * 16, y);
               tc::tmem_wait_ld();
@@ -873,41 +861,29 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
             }
           }
         }
-        // weights 2^(s sl - m sl + e): one fma and one ex2 each
+        // weights 2^(s sl - m sl + e): one fma and one ex2 each.  They take the
+        // place of the first 32 of this half's columns of S: the last 32, still
+        // in registers, go first, to the upper 16.
         const float ref = WEIGHT_EXP<FP16> - (m == -CUDART_INF_F ? 0.f : m * sl);
         const float2 sl2 = make_float2(sl, sl), ref2 = make_float2(ref, ref);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        auto weights = [&](const uint32_t (&x)[32], int c) {
-          uint32_t w[16];
+        uint32_t w[2][16];
+#pragma unroll
+        for (int c = 1; c >= 0; --c) {
+          if (c == 0) load(0);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const float2 e = ffma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), sl2, ref2);
             const float2 y = make_float2(ex2(e.x), ex2(e.y));
             sum[j & 1] = fadd2(sum[j & 1], y);
-            w[j] = act_pack2<FP16>(y.x, y.y);
+            w[c][j] = act_pack2<FP16>(y.x, y.y);
           }
-          tmem_st16(t_s + 64 + c * 16, w);
-        };
-        // the weights take the place of the last 64 columns of S, which go first
-        weights(x[3], 3);
-        tc::tmem_ld32_async(t_s, x[0]);
-        weights(x[2], 2);
-        tmem_wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_half[s]);
-        tc::tmem_wait_ld();
-        tc::tmem_regs(x[0]);
-        tc::tmem_ld32_async(t_s + 32, x[1]);
-        weights(x[0], 0);
-        tc::tmem_wait_ld();
-        tc::tmem_regs(x[1]);
-        weights(x[1], 1);
-        tmem_wait_st();
+        }
+        tmem_st16(t_s, w[0]);
+        tmem_st16(t_s + 16, w[1]);
         sum[0] = fadd2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
-      } else if (lane == 0) {
-        mbar_arrive(&sm.p_half[s]);
+        tmem_wait_st();
       }
       stepped = true;
       tc::fence_before_sync();
@@ -917,6 +893,11 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
     fills += 2 * (i1 - i0);
     tiles += i1 - i0;
     if (stepped) {
+      // the row's sum.  (Without a step the other stream may still be reading
+      // the last item's results here.)
+      sm.share[s][half][r] = l;
+      named_bar_sync(pair, 64);
+      l += sm.share[s][half ^ 1][r];
       warp_wait(&sm.o_full[s], o_count & 1, sm, err);
       ++o_count;
       tc::fence_after_sync();
@@ -931,17 +912,21 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
         // rows of 512 bytes, their 16-byte pieces rotated by the row: no bank conflicts
 #pragma unroll 1
         for (int c = 0; c < 4 && any_row; ++c) {
-          float v[32];
-          tc::tmem_ld32(t_o + c * 32, v);
+          float v[16];
+          tc::tmem_ld16(t_o + c * 16, v);
           if (valid) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<float4*>(q_smem + r * 512 + (((c * 8 + j) ^ lane) << 4)) =
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<float4*>(q_smem + r * 512 + (((half * 16 + c * 4 + j) ^ lane) << 4)) =
                   make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
           }
           __syncwarp();
         }
-        sm.merge_ml[r] = make_float2(m2, l);
+        named_bar_sync(pair, 64);  // both halves have read their sums
+        if (half == 0) {
+          sm.share[1][0][r] = m2;
+          sm.share[1][1][r] = l;
+        }
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) {
@@ -957,7 +942,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
     if (merged) {
       warp_wait(&sm.merge_full, merges & 1, sm, err);
       ++merges;
-      const float2 other = sm.merge_ml[r];
+      const float2 other = make_float2(sm.share[1][0][r], sm.share[1][1][r]);
       const float top = fmaxf(m2, other.x);
       if (top == -CUDART_INF_F) {
         l = 0.f;
@@ -975,17 +960,17 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
     float poison = 0.f;
 #pragma unroll 1
     for (int c = 0; c < 4 && any_row; ++c) {
-      float v[32];
+      float v[16];
       if (stepped) {
-        tc::tmem_ld32(t_o + c * 32, v);
+        tc::tmem_ld16(t_o + c * 16, v);
       } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        for (int j = 0; j < 16; ++j) v[j] = 0.f;
       }
       if (merged && valid) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float4 y = *reinterpret_cast<const float4*>(q_smem + r * 512 + (((c * 8 + j) ^ lane) << 4));
+        for (int j = 0; j < 4; ++j) {
+          const float4 y = *reinterpret_cast<const float4*>(q_smem + r * 512 + (((half * 16 + c * 4 + j) ^ lane) << 4));
           v[4 * j] = v[4 * j] * w0 + y.x * w1;
           v[4 * j + 1] = v[4 * j + 1] * w0 + y.y * w1;
           v[4 * j + 2] = v[4 * j + 2] * w0 + y.z * w1;
@@ -993,20 +978,21 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
         }
       }
       if (valid && whole_pair) {
-        int4* out = reinterpret_cast<int4*>(p.a.out + ((int64_t)tok * p.a.hq + head) * D + c * 32);
+        int4* out = reinterpret_cast<int4*>(p.a.out + ((int64_t)tok * p.a.hq + head) * D + half * 64 + c * 16);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < 16; ++j) {
           v[j] *= inv;
           poison += v[j] * 0.f;  // NaN from then on when one is not finite
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 2; ++j)
           out[j] = make_int4(act_pack2<FP16>(v[8 * j], v[8 * j + 1]), act_pack2<FP16>(v[8 * j + 2], v[8 * j + 3]),
                              act_pack2<FP16>(v[8 * j + 4], v[8 * j + 5]), act_pack2<FP16>(v[8 * j + 6], v[8 * j + 7]));
       } else if (valid) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)  // pieces are 8 apart
-          __stcg(p.part_o + part_piece(part_row, 0) + (c * 8 + j) * 8, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+        for (int j = 0; j < 4; ++j)  // pieces are 8 apart
+          __stcg(p.part_o + part_piece(part_row, 0) + (half * 16 + c * 4 + j) * 8,
+                 make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
       }
       __syncwarp();
     }
@@ -1016,16 +1002,18 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
       if (lane == 0) mbar_arrive(&sm.o_free[s]);
     }
     if (!two && i1 > i0) {
-      // the next queries may land where the other half's result was
+      // the next queries may land where the other stream's result was
       fence_proxy_async_smem();
-      named_bar_sync(bar, 128);
-      if (r == 0) mbar_arrive(&sm.q_empty);
+      named_bar_sync(bar, 256);
+      if ((threadIdx.x & 255) == 0) mbar_arrive(&sm.q_empty);
     }
     if (whole_pair) {
-      if (valid && p.a.lse)
+      if (half == 0 && valid && p.a.lse)
         p.a.lse[(int64_t)tok * p.a.hq + head] = l == 0.f ? -CUDART_INF_F : (m2 + log2f(l) - WEIGHT_EXP<FP16>) * LN2;
-      unsigned bad = __ballot_sync(0xffffffffu, valid && poison != 0.f);
-      __syncwarp();  // the row's own stores come before those of attend_row
+      const unsigned mine = __ballot_sync(0xffffffffu, valid && poison != 0.f);
+      if (lane == 0) sm.poisoned[s][half][quarter] = mine;
+      named_bar_sync(pair, 64);  // the row's own stores come before those of attend_row
+      unsigned bad = half == 0 ? mine | sm.poisoned[s][1][quarter] : 0;
       while (bad) {
         const int src = __ffs(bad) - 1;
         bad &= bad - 1;
@@ -1033,10 +1021,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
                          __shfl_sync(0xffffffffu, pos, src), kv);
       }
     } else {
-      if (valid) __stcg(&p.part_ml[part_row], make_float2(m2, l));
-      named_bar_sync(bar, 128);
-      if (r == 0) {
-        __threadfence();  // for the whole warpgroup's stores, which the barrier put before it
+      if (half == 0 && valid) __stcg(&p.part_ml[part_row], make_float2(m2, l));
+      named_bar_sync(bar, 256);
+      if ((threadIdx.x & 255) == 0) {
+        __threadfence();  // for all of the stream's stores, which the barrier put before it
         unsigned* counter = &p.counters[it.first * 2 + tile];
         const bool last = atomicAdd(counter, 1u) + 1 == (unsigned)it.parts;
         if (last) {
@@ -1045,7 +1033,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
         }
         sm.last[s] = last;
       }
-      named_bar_sync(bar, 128);
+      named_bar_sync(bar, 256);
       if (sm.last[s]) {
         join_parts<FP16>(p, sm, s, it, tile, min(p.tile_tok, it.n_tok - tile * p.tile_tok) * p.group);
       }
@@ -1058,8 +1046,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, int s, u
 template <bool FP16>
 __global__ void __launch_bounds__(THREADS, 1)
     attention_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
-  extern __shared__ unsigned char raw[];
-  unsigned char* q_smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) unsigned char q_smem[];  // the swizzle repeats every 1024 bytes
   unsigned char* kv_smem = q_smem + 2 * TILE_BYTES;
   Smem& sm = *reinterpret_cast<Smem*>(kv_smem + STAGES * TILE_BYTES);
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
@@ -1070,20 +1057,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int i = 0; i < RING; ++i) {
       mbar_init(&sm.ring_full[i], 1);
-      mbar_init(&sm.ring_empty[i], 11);  // copying lane, two issuing lanes, eight softmax warps
+      mbar_init(&sm.ring_empty[i], 3 + SOFTMAX_WARPS);  // copying lane, two issuing lanes, softmax warps
     }
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 2);
     mbar_init(&sm.q_read, 1);
-    mbar_init(&sm.merge_full, 4);
+    mbar_init(&sm.merge_full, 8);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.s_full[s], 1);
-      mbar_init(&sm.p_half[s], 4);
-      mbar_init(&sm.p_full[s], 4);
+      mbar_init(&sm.p_full[s], 8);
       mbar_init(&sm.turn[s], 1);
       mbar_init(&sm.drained[s], 1);
       mbar_init(&sm.o_full[s], 1);
-      mbar_init(&sm.o_free[s], 4);
+      mbar_init(&sm.o_free[s], 8);
     }
     sm.dead = 0;
     fence_mbar_init();
@@ -1100,8 +1086,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem;
-  if (warp < 8) {
-    softmax_role<FP16>(p, sm, warp >> 2, q_smem, kv_smem, tmem);
+  if (warp < SOFTMAX_WARPS) {
+    softmax_role<FP16>(p, sm, q_smem, kv_smem, tmem);
   } else if (warp == LOAD_WARP) {
     load_role(p, maps, sm, q_smem, kv_smem);
   } else if (warp >= MMA_WARP) {
@@ -1116,7 +1102,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == MMA_WARP) tc::tmem_dealloc(tmem, 512);
 }
 
-constexpr size_t SMEM_BYTES = (2 + STAGES) * TILE_BYTES + 1024 + sizeof(Smem);
+constexpr size_t SMEM_BYTES = (2 + STAGES) * TILE_BYTES + sizeof(Smem);
 static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 
 int sm_count() {
