@@ -46,12 +46,13 @@ constexpr int THREADS = 640;
 constexpr int SOFTMAX_WARPS = 16;  // two warpgroups a stream
 constexpr int LOAD_WARP = 16, PLAN_WARP = 17, MMA_WARP = 18;  // MMA_WARP + 1: the second stream's
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-// The running reference follows the row's maximum only when that has grown by
-// 2^GROWTH: until then weights up to 2^GROWTH stand in for ones, and the
-// accumulator is left alone.
-constexpr float GROWTH = 8.f;
-// fp16 weights are formed 2^7 larger: at most 2^15 with GROWTH, and the
-// smallest normal one (2^-14) is then 2^-21 of the reference.
+// The running reference follows the row's maximum only when 64 weights have
+// come to sum to more: until then weights above one stand, and the accumulator
+// is left alone.  A weight rounds to 16 bits with the same relative error
+// whatever its size.
+constexpr float LIMIT = 32768.f;
+// fp16 weights are formed 2^7 larger: none passes LIMIT (65504 is the largest
+// number), and the smallest normal one (2^-14) is then 2^-21 of the reference.
 template <bool FP16>
 constexpr float WEIGHT_EXP = FP16 ? 7.f : 0.f;
 
@@ -513,13 +514,13 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
         o_parity ^= 1;
       }
       const uint64_t vd = smem_desc_mn(kv_addr + sv.at * TILE_BYTES);
-      await(&sm.p_full[s], p_parity);
-      p_parity ^= 1;
-      tc::fence_after_sync();
       if (two) {
         await(&sm.turn[s], turn);
         turn ^= 1;
       }
+      await(&sm.p_full[s], p_parity);
+      p_parity ^= 1;
+      tc::fence_after_sync();
       if (elect_one()) {
 #pragma unroll
         for (int j = 0; j < KT / 16; ++j)  // 16 keys: two 8-row groups of V
@@ -779,11 +780,15 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
     const int hi_min = __reduce_min_sync(0xffffffffu, valid ? hi : 0x7fffffff);
     const int lo_max = __reduce_max_sync(0xffffffffu, valid ? lo : 0);
     const int sink_min = __reduce_min_sync(0xffffffffu, valid ? sink : 0x7fffffff);
+    // key tiles that every row of the warp sees whole: up to clear_hi, from
+    // clear_lo on or below clear_sink
+    const int clear_hi = hi_min - 64 - half * 64, clear_lo = lo_max - half * 64, clear_sink = sink_min - 64 - half * 64;
     float m = -CUDART_INF_F, l = 0.f;  // m is the row's, l this half's
     bool stepped = false;
     for (int i = two ? i0 : i0 + s; i < i1; i += two ? 1 : 2) {
       if (two && !active(it.act[s], i)) continue;
-      const int key = list_tile(it, i) * KT + half * 64;
+      const int first_key = list_tile(it, i) * KT, key = first_key + half * 64;
+      const bool clear = first_key <= clear_hi && (first_key >= clear_lo || first_key <= clear_sink);
       warp_wait(&sm.s_full[s], s_count & 1, sm, err);
       ++s_count;
       tc::fence_after_sync();
@@ -801,8 +806,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
       }
       if (any_row) {
         const int held = *(volatile int*)&sm.page_mask[(tiles + i - i0) % MASKS];
-        const bool whole = held == all_held && key + 64 <= hi_min && (key >= lo_max || key + 64 <= sink_min);
-        if (!whole) {
+        if (!clear || held != all_held) {
           // hidden scores become -inf where they are
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
@@ -822,26 +826,52 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
           }
           tmem_wait_st();
         }
-        uint32_t x[32];
-        float top[2] = {m, m};
+        // Weights 2^(s sl - m sl + e), one fma and one ex2 each, against the
+        // reference as it stands: no maximum is looked for while their sum
+        // stays below LIMIT.  Where it does not (or the row has no reference
+        // yet), the reference moves to the row's maximum so far, and the weights
+        // are formed once more.
+        uint32_t x[32], w[2][16];
         auto load = [&](int c) {
           tc::tmem_ld32_async(t_s + c * 32, x);
           tc::tmem_wait_ld();
           tc::tmem_regs(x);
         };
+        float2 sum[2];
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
+          if (stepped || pass > 0) {
+            const float ref = WEIGHT_EXP<FP16> - (m == -CUDART_INF_F ? 0.f : m * sl);
+            const float2 sl2 = make_float2(sl, sl), ref2 = make_float2(ref, ref);
+            sum[0] = sum[1] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          load(c);
+            for (int c = 0; c < 2; ++c) {
+              load(c);
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            top[0] = max3(top[0], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-            top[1] = max3(top[1], __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+              for (int j = 0; j < 16; ++j) {
+                const float2 e = ffma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), sl2, ref2);
+                const float2 y = make_float2(ex2(e.x), ex2(e.y));
+                sum[j & 1] = fadd2(sum[j & 1], y);
+                w[c][j] = act_pack2<FP16>(y.x, y.y);
+              }
+            }
+            sum[0] = fadd2(sum[0], sum[1]);
+            sum[0].x += sum[0].y;
+            // rows past the block hold anything and have no say
+            if (pass > 0 || !named_bar_or(pair, 64, valid && (m == -CUDART_INF_F || !(sum[0].x <= LIMIT)))) break;
           }
-        }
-        float m_new = fmaxf(top[0], top[1]);
-        // m = -inf: nothing seen yet, any first maximum is taken (-inf - -inf
-        // compares false).  Rows past the block hold anything and have no say.
-        if (named_bar_or(pair, 64, valid && (m_new - m) * sl > GROWTH)) {
+          float m_new = m;
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            load(c);
+            float top[2] = {m_new, m_new};
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              top[0] = max3(top[0], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+              top[1] = max3(top[1], __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+            }
+            m_new = fmaxf(top[0], top[1]);
+          }
           sm.share[s][half][r] = m_new;
           named_bar_sync(pair, 64);
           m_new = fmaxf(m_new, sm.share[s][half ^ 1][r]);
@@ -861,28 +891,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
             }
           }
         }
-        // weights 2^(s sl - m sl + e): one fma and one ex2 each.  They take the
-        // place of the first 32 of this half's columns of S: the last 32, still
-        // in registers, go first, to the upper 16.
-        const float ref = WEIGHT_EXP<FP16> - (m == -CUDART_INF_F ? 0.f : m * sl);
-        const float2 sl2 = make_float2(sl, sl), ref2 = make_float2(ref, ref);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        uint32_t w[2][16];
-#pragma unroll
-        for (int c = 1; c >= 0; --c) {
-          if (c == 0) load(0);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float2 e = ffma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), sl2, ref2);
-            const float2 y = make_float2(ex2(e.x), ex2(e.y));
-            sum[j & 1] = fadd2(sum[j & 1], y);
-            w[c][j] = act_pack2<FP16>(y.x, y.y);
-          }
-        }
+        l += sum[0].x;
+        // they take the place of the first 32 of this half's columns of S
         tmem_st16(t_s, w[0]);
         tmem_st16(t_s + 16, w[1]);
-        sum[0] = fadd2(sum[0], sum[1]);
-        l += sum[0].x + sum[0].y;
         tmem_wait_st();
       }
       stepped = true;
