@@ -578,7 +578,7 @@ int kda_kv_append(const kda_kv_cache* cache, const void* k, int64_t k_stride_tok
  * in any mix.
  *   q           [t_total, Hq, 128], 16-byte aligned, token and head strides
  *               multiples of 8 elements and >= 128
- *   out         [t_total, Hq, 128] contiguous, 16-byte aligned, written;
+ *   out         [t_total, Hq, 128] contiguous, 32-byte aligned, written;
  *               tokens past cu_seqlens[n_req] are left alone
  *   lse         fp32 [t_total, Hq] or NULL, written
  *   cu_seqlens  device int32 [n_req + 1], kv_lens device int32 [n_req]

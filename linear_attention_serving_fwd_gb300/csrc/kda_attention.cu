@@ -45,6 +45,7 @@ constexpr int MASKS = 8;       // page masks of the K tiles in flight
 constexpr int THREADS = 640;
 constexpr int SOFTMAX_WARPS = 16;  // two warpgroups a stream
 constexpr int LOAD_WARP = 16, PLAN_WARP = 17, MMA_WARP = 18;  // MMA_WARP + 1: the second stream's
+constexpr int LEAD_TWO = 4, LEAD_ONE = 2;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // The running reference follows the row's maximum only when 64 weights have
 // come to sum to more: until then weights above one stand, and the accumulator
@@ -136,6 +137,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
+}
+// 32 bytes, a whole sector: rows lie far apart, so a warp's store takes the
+// memory pipe a cycle a row, whatever its width
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 __device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
   asm volatile(
@@ -269,9 +277,13 @@ __device__ __forceinline__ int block_tiles(const Params& p, int n, int kv, int k
   it.n_sink = min((it.sink_hi + KT - 1) / KT, it.t_lo);
   return it.n_sink + (it.hi > it.lo ? (it.hi + KT - 1) / KT - it.t_lo : 0);
 }
+// Its length on the line: the key tiles, and before them what a block costs by
+// itself (queries, pipeline fill, results), in key tiles.
+__device__ __forceinline__ int block_lead(const Params& p, const Item& it) { return it.n_tok > p.tile_tok ? LEAD_TWO : LEAD_ONE; }
 __device__ __forceinline__ int block_cost(const Params& p, int n, int kv, int k) {
   Item it;
-  return max(1, block_tiles(p, n, kv, k, it));
+  const int tiles = max(1, block_tiles(p, n, kv, k, it));
+  return tiles + block_lead(p, it);
 }
 __device__ __forceinline__ int n_blocks(const Params& p, int n) { return (n + 2 * p.tile_tok - 1) / (2 * p.tile_tok); }
 
@@ -582,11 +594,13 @@ __device__ __forceinline__ void plan_role(const Params& p, Smem& sm, int cta, lo
       int t0, n, kv;
       request(p.a, b, t0, n, kv, false);
       const int blocks = n_blocks(p, n);
-      // block k, whose place on the line is [s, s + its cost)
+      // block k, which begins at s on the line; pieces divide its key tiles
       auto emit = [&](int k, long long s) {
         Item it;
         const int tiles = block_tiles(p, n, kv, k, it);
+        s += block_lead(p, it);
         const long long e = s + max(1, tiles);
+        if (s >= u1 || e <= u0) return;
         it.b = b;
         it.kvh = h;
         it.tok = t0 + k * 2 * p.tile_tok;
@@ -700,27 +714,23 @@ __device__ __forceinline__ void join_parts(const Params& p, Smem& sm, int s, con
   for (int u = warp; u < (n_rows + 7) / 8 * 4; u += 8) {
     const bool real = (u >> 2) * 8 + (lane & 7) < n_rows;
     const int row = min((u >> 2) * 8 + (lane & 7), n_rows - 1), c = (u & 3) * 8 + (lane >> 3);
-    // the four lanes of a row look through the references together
-    float top = -CUDART_INF_F;
-#pragma unroll 4
-    for (int k = lane >> 3; k < parts; k += 4) top = fmaxf(top, __ldcg(&p.part_ml[part_row(k, row)]).x);
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-    float l = 0.f, o[8];
+    float top = -CUDART_INF_F, l = 0.f, o[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] = 0.f;
-#pragma unroll 8
+#pragma unroll 4
     for (int k = 0; k < parts; ++k) {
       const size_t at = part_row(k, row);
       const float2 ml = __ldcg(&p.part_ml[at]);
       const float4 x = __ldcg(&p.part_o[part_piece(at, c)]), y = __ldcg(&p.part_o[part_piece(at, c + 4)]);
+      const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
       // a part that has seen nothing stored nothing
       const bool some = ml.x != -CUDART_INF_F;
-      const float w = some ? ex2(ml.x - top) : 0.f;
-      l += some ? w * ml.y : 0.f;
-      const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      const float reach = fmaxf(top, ml.x);
+      const float corr = top == reach ? 1.f : ex2(top - reach), w = some ? ex2(ml.x - reach) : 0.f;
+      l = l * corr + (some ? w * ml.y : 0.f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] += some ? w * z[j] : 0.f;
+      for (int j = 0; j < 8; ++j) o[j] = o[j] * corr + (some ? w * z[j] : 0.f);
+      top = reach;
     }
     if (!real) continue;
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -990,16 +1000,16 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
         }
       }
       if (valid && whole_pair) {
-        int4* out = reinterpret_cast<int4*>(p.a.out + ((int64_t)tok * p.a.hq + head) * D + half * 64 + c * 16);
+        __nv_bfloat16* out = p.a.out + ((int64_t)tok * p.a.hq + head) * D + half * 64 + c * 16;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           v[j] *= inv;
           poison += v[j] * 0.f;  // NaN from then on when one is not finite
         }
+        uint32_t w[8];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          out[j] = make_int4(act_pack2<FP16>(v[8 * j], v[8 * j + 1]), act_pack2<FP16>(v[8 * j + 2], v[8 * j + 3]),
-                             act_pack2<FP16>(v[8 * j + 4], v[8 * j + 5]), act_pack2<FP16>(v[8 * j + 6], v[8 * j + 7]));
+        for (int j = 0; j < 8; ++j) w[j] = act_pack2<FP16>(v[2 * j], v[2 * j + 1]);
+        store32(out, w);
       } else if (valid) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)  // pieces are 8 apart

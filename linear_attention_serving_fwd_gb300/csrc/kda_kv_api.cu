@@ -198,7 +198,7 @@ int kda_paged_attention(const kda_kv_cache* cache, const void* q, int64_t q_stri
   if ((t_total > 1 && q_stride_tok < kda::D) || (hq > 1 && q_stride_head < kda::D))
     return fail(KDA_ERR_INVALID_ARGUMENT, "q rows must not overlap: strides >= 128 elements.");
   if (!out) return fail(KDA_ERR_INVALID_ARGUMENT, "out must not be NULL.");
-  if (!aligned16(out)) return fail(KDA_ERR_INVALID_ARGUMENT, "out must be 16-byte aligned.");
+  if (reinterpret_cast<uintptr_t>(out) & 31u) return fail(KDA_ERR_INVALID_ARGUMENT, "out must be 32-byte aligned.");
   if (!cu_seqlens || !kv_lens) return fail(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens and kv_lens must not be NULL.");
   if ((rc = check_table(block_table, table_stride, table_cols, n_req))) return rc;
   if ((int64_t)table_cols * cache->page_size > 0x7fffffff - 512)

@@ -107,7 +107,7 @@ def test_append(over, text):
     (dict(t=-1), ">= 0"), (dict(n=-1), ">= 0"), (dict(scale=0.0), "scale"), (dict(scale=float("nan")), "scale"),
     (dict(scale=float("inf")), "scale"), (dict(scale=-1.0), "scale"), (dict(window=-1), "window"),
     (dict(sinks=-1), "sinks"), (dict(q=None), "q must not be NULL"), (dict(q=FAKE + 4), "aligned"),
-    (dict(qt=4), "multiples of 8"), (dict(out=None), "out must not"), (dict(out=FAKE + 8), "out must be 16"),
+    (dict(qt=4), "multiples of 8"), (dict(out=None), "out must not"), (dict(out=FAKE + 16), "out must be 32"),
     (dict(cu=None), "cu_seqlens"), (dict(lens=None), "kv_lens"), (dict(table=None), "block_table"),
     (dict(cols=0), "column"), (dict(stride=7), "table_stride"), (dict(cols=(1 << 27), stride=1 << 27), "2^31"),
     (dict(ws=None), "workspace needs"), (dict(ws_bytes=64), "workspace needs"), (dict(ws=FAKE + 8), "workspace must be"),
