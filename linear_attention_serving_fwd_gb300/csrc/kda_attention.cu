@@ -94,6 +94,12 @@ struct Params {
   int n_cta;
   int min_piece;           // least tiles per CTA
   int boxes;               // pages per key tile (1 when a page holds more)
+  // K and V tiles in shared memory: rows of 128 bytes (64 of the dimensions) in
+  // groups of 8; bytes from group to group and from half to half of a row.  With
+  // joined copies a box holds whole rows, half after half in each group, and a
+  // page's box begins at group page * page_groups and outer place
+  // page * page_outer + head of the map.
+  int joined, group_bytes, half_bytes, page_groups, page_outer;
   unsigned* counters;      // [n_cta][2], zero between calls
   float2* part_ml;         // [n_cta][2 slots][2 tiles][ROWS]
   float4* part_o;          // [n_cta][2 slots][2 tiles][ROWS / 8][32][8]: 16-byte pieces of 8 rows side by side
@@ -145,6 +151,11 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8]) {
                "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
+__device__ __forceinline__ void tma_load5(void* dst, const CUtensorMap* map, int c3, int c4, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], [%5];"
+      ::"r"(smem_u32(dst)), "l"(map), "r"(0), "r"(c3), "r"(c4), "r"(smem_u32(bar)) : "memory");
+}
 __device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
@@ -159,14 +170,15 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b_de
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
       "}\n" ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
-// 128-byte-swizzled MN-major operand as the copies leave it: 64 dimensions (128
-// bytes) a row, 8-row groups 1024 bytes apart, the other 64 dimensions
-// HALF_BYTES further.
-__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
+// 128-byte-swizzled operands as the copies leave them: 64 dimensions (128
+// bytes) a row, 8-row groups ``group`` bytes apart, the other 64 dimensions
+// ``half`` bytes further.  K-major (the dimensions are summed over; the leading
+// offset is not used) or MN-major (the rows are).
+__device__ __forceinline__ uint64_t smem_desc_rows(uint32_t saddr, uint32_t group, uint32_t half, bool mn) {
   uint64_t d = 0;
   d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)(HALF_BYTES >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)(mn ? half >> 4 : 1u) << 16;
+  d |= (uint64_t)(group >> 4) << 32;
   d |= (uint64_t)1u << 46;
   d |= (uint64_t)2u << 61;
   return d;
@@ -379,7 +391,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
     // keys and values
     for (int i = it.i0; i < it.i1; ++i, ++tiles) {
       const int row = (list_tile(it, i) * KT) & (page - 1) & ~(box - 1);
-      const int c_page = __shfl_sync(0xffffffffu, pg < 0 ? p.a.n_pages : pg, lane >> 1);
+      const int c_page = __shfl_sync(0xffffffffu, pg < 0 ? p.a.n_pages : pg, p.joined ? lane : lane >> 1);
       const unsigned held = __ballot_sync(0xffffffffu, pg >= 0);
       pg = page_of(i + 1);
 #pragma unroll 1
@@ -391,7 +403,11 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
           mbar_arrive_expect_tx(&sm.kv_full[st], TILE_BYTES);
         }
         __syncwarp();
-        if (lane < 2 * p.boxes)  // a lane a box: page, half
+        if (p.joined) {  // a lane a box
+          if (lane < p.boxes)
+            tma_load5(kv_smem + st * TILE_BYTES + lane * box * 256, kv == 0 ? &maps.k : &maps.v,
+                      c_page * p.page_groups + (row >> 3), c_page * p.page_outer + it.kvh, &sm.kv_full[st]);
+        } else if (lane < 2 * p.boxes)  // page, half
           tma_load4(kv_smem + st * TILE_BYTES + (lane & 1) * HALF_BYTES + (lane >> 1) * box * 128, kv == 0 ? &maps.k : &maps.v,
                     (lane & 1) * 64, row, it.kvh, c_page, &sm.kv_full[st]);
       }
@@ -441,6 +457,9 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
   const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * 128;
   Stage next;  // of list index i0 of the next item
   uint32_t q_parity = 0, p_parity = 0, o_parity = 1;
+  const uint64_t k_desc = smem_desc_rows(kv_addr, p.group_bytes, p.half_bytes, false);
+  const uint64_t v_desc = smem_desc_rows(kv_addr, p.group_bytes, p.half_bytes, true);
+  const uint32_t k_half = (uint32_t)p.half_bytes >> 4, v_step = (uint32_t)p.group_bytes >> 3;  // 16 keys: two groups
   auto await = [&](uint64_t* bar, uint32_t parity) { warp_wait(bar, parity, sm, err); };
   // In blocks of two tiles the streams take turns at the tensor cores, key tile
   // by key tile: a product of one and its next scores go in a row.  Left to mix,
@@ -475,12 +494,12 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
     Stage st = next;
     bool scored = false;  // this tile's scores have been issued behind the last tile's product
     auto scores = [&](int i, const Stage& at) {
-      const uint64_t kd = tc::smem_desc_sw128(kv_addr + at.at * TILE_BYTES);
+      const uint64_t kd = k_desc + at.at * (TILE_BYTES >> 4);
       if (elect_one()) {
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
-          const uint32_t off = ((j >> 2) * HALF_BYTES + (j & 3) * 32) >> 4;
-          tc::mma_f16(t_s, qd + off, kd + off, id_qk, j > 0 ? 1u : 0u);
+          const uint32_t in = (j & 3) * 2;  // 32 bytes
+          tc::mma_f16(t_s, qd + (j >> 2) * (HALF_BYTES >> 4) + in, kd + (j >> 2) * k_half + in, id_qk, j > 0 ? 1u : 0u);
         }
         tc::mma_commit(&sm.s_full[s]);
         // the first stream's last scores of a block of one tile: from here on the
@@ -525,7 +544,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
         await(&sm.o_free[s], o_parity);
         o_parity ^= 1;
       }
-      const uint64_t vd = smem_desc_mn(kv_addr + sv.at * TILE_BYTES);
+      const uint64_t vd = v_desc + sv.at * (TILE_BYTES >> 4);
       if (two) {
         await(&sm.turn[s], turn);
         turn ^= 1;
@@ -536,7 +555,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
       if (elect_one()) {
 #pragma unroll
         for (int j = 0; j < KT / 16; ++j)  // 16 keys: two 8-row groups of V
-          mma_f16_ts(t_o, t_s + (j >> 2) * 64 + (j & 3) * 8, vd + j * (2048 >> 4), id_pv, (j > 0 || !first) ? 1u : 0u);
+          mma_f16_ts(t_o, t_s + (j >> 2) * 64 + (j & 3) * 8, vd + j * v_step, id_pv, (j > 0 || !first) ? 1u : 0u);
         tc::mma_commit(&sm.kv_empty[sv.at]);
       }
       __syncwarp();
@@ -808,9 +827,12 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
         const uint32_t f = fills + 2 * (i - i0) + 1;
         wait(&sm.kv_full[f % STAGES], (f / STAGES) & 1, sm, err);
         const int from = max(0, kv - key);
-        unsigned char* v = kv_smem + (f % STAGES) * TILE_BYTES + (half * 64 + from) * 128;
-        for (int c = r; c < (64 - from) * 16; c += 128)
-          *reinterpret_cast<int4*>(v + ((c >> 3) & 1) * HALF_BYTES + (c >> 4) * 128 + (c & 7) * 16) = make_int4(0, 0, 0, 0);
+        unsigned char* v = kv_smem + (f % STAGES) * TILE_BYTES;
+        for (int c = r; c < (64 - from) * 16; c += 128) {
+          const int row = half * 64 + from + (c >> 4);
+          *reinterpret_cast<int4*>(v + (row >> 3) * p.group_bytes + ((c >> 3) & 1) * p.half_bytes + (row & 7) * 128 + (c & 7) * 16) =
+              make_int4(0, 0, 0, 0);
+        }
         fence_proxy_async_smem();
         __syncwarp();
       }
@@ -1170,6 +1192,18 @@ bool encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, bool fp16, 
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same rows for joined copies: boxes of 64 x 8 rows x both halves x groups,
+// from n_groups groups of 8 rows (stride 8 s1) and an outer dimension.
+bool encode_joined(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, bool fp16, const void* base, int64_t s1,
+                   int64_t n_groups, int64_t n_outer, int64_t s_outer, uint32_t groups) {
+  const cuuint64_t dims[5] = {64, 8, 2, (cuuint64_t)n_groups, (cuuint64_t)n_outer};
+  const cuuint64_t strides[4] = {(cuuint64_t)s1 * 2, 128, (cuuint64_t)s1 * 16, (cuuint64_t)(n_outer > 1 ? s_outer : D) * 2};
+  const cuuint32_t box[5] = {64, 8, 2, groups, 1}, step[5] = {1, 1, 1, 1, 1};
+  return enc(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base),
+             dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 size_t attention_workspace_bytes() {
@@ -1193,9 +1227,22 @@ int launch_attention(const AttentionParams& a, bool fp16, void* workspace, cudaS
   p.part_o = reinterpret_cast<float4*>(p.part_ml + (size_t)p.n_cta * 4 * ROWS);
   Maps maps;
   const int box = page < KT ? page : KT;
-  if (!encode(enc, &maps.k, fp16, a.kc, page, a.kc_st, a.hkv, a.kc_sh, a.n_pages, a.kc_sp, box, 1, 1) ||
-      !encode(enc, &maps.v, fp16, a.vc, page, a.vc_st, a.hkv, a.vc_sh, a.n_pages, a.vc_sp, box, 1, 1) ||
-      !encode(enc, &maps.q, fp16, a.q, p.group, a.q_sh, a.hkv, a.q_sh * p.group, a.t_total, a.q_st, p.group, 1, p.tile_tok) ||
+  // Joined copies where page and row group, or page and head, are one dimension
+  // (pages of whole token-major or head-major rows without gaps).
+  const bool by_rows = a.kc_sp == page * a.kc_st && a.vc_sp == page * a.vc_st;
+  const bool by_heads = a.kc_sp == a.hkv * a.kc_sh && a.vc_sp == a.hkv * a.vc_sh;
+  p.joined = by_rows || by_heads;
+  p.group_bytes = p.joined ? 2048 : 1024;
+  p.half_bytes = p.joined ? 1024 : HALF_BYTES;
+  p.page_groups = by_rows ? page / 8 : 0;
+  p.page_outer = by_rows ? 0 : a.hkv;
+  const int64_t groups = by_rows ? (int64_t)a.n_pages * (page / 8) : page / 8, outer = by_rows ? a.hkv : (int64_t)a.n_pages * a.hkv;
+  const bool ok =
+      p.joined ? encode_joined(enc, &maps.k, fp16, a.kc, a.kc_st, groups, outer, a.kc_sh, box / 8) &&
+                     encode_joined(enc, &maps.v, fp16, a.vc, a.vc_st, groups, outer, a.vc_sh, box / 8)
+               : encode(enc, &maps.k, fp16, a.kc, page, a.kc_st, a.hkv, a.kc_sh, a.n_pages, a.kc_sp, box, 1, 1) &&
+                     encode(enc, &maps.v, fp16, a.vc, page, a.vc_st, a.hkv, a.vc_sh, a.n_pages, a.vc_sp, box, 1, 1);
+  if (!ok || !encode(enc, &maps.q, fp16, a.q, p.group, a.q_sh, a.hkv, a.q_sh * p.group, a.t_total, a.q_st, p.group, 1, p.tile_tok) ||
       !encode(enc, &maps.q1, fp16, a.q, p.group, a.q_sh, a.hkv, a.q_sh * p.group, a.t_total, a.q_st, p.group, 1, 1))
     return -1;
   cudaLaunchConfig_t cfg = {};
