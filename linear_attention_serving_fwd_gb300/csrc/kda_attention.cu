@@ -355,39 +355,43 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
     if (it.i1 == it.i0) continue;
     const int32_t* table = p.a.table + (int64_t)it.b * p.a.table_stride;
     const int page = 1 << p.a.page_shift, box = min(page, KT);
-    // Page of lane's box of key tile t; >= n_pages (the copy then fills with zeros) for a hidden one.
+    // Page of lane's box of list entry i; -1 for one that no row sees (the copy
+    // then asks for a page past the cache, which reads nothing and fills with
+    // zeros): a hidden one, or one outside the window in a tile at its edge.
     auto page_of = [&](int i) {
       if (lane >= p.boxes || i >= it.i1) return -1;
       const int key = list_tile(it, i) * KT + lane * box;
-      if (key >= it.kv) return -1;
+      if (!((key < it.hi && key + box > it.lo) || key < it.sink_hi)) return -1;
       const int pg = table[key >> p.a.page_shift];
-      if (pg >= p.a.n_pages) {
-        const int end = key + box;
-        if ((key < it.hi && end > it.lo) || key < it.sink_hi) set_error(err, ERR_INDEX);
-        return -1;
-      }
-      return pg < 0 ? -1 : pg;
+      if (pg >= p.a.n_pages) set_error(err, ERR_INDEX);
+      return pg < 0 || pg >= p.a.n_pages ? -1 : pg;
     };
     int pg = page_of(it.i0);
-    // queries
-    const bool two = it.n_tok > p.tile_tok;
-    warp_wait(&sm.q_empty, (q_count & 1) ^ 1, sm, err);
-    ++q_count;
-    const bool single = it.n_tok <= 8;
-    const uint32_t box_bytes = (uint32_t)p.group * 128u;
-    if (lane == 0)
-      mbar_arrive_expect_tx(&sm.q_full, single ? 2u * it.n_tok * box_bytes : (two ? 4u : 2u) * p.tile_tok * box_bytes);
-    __syncwarp();
-    if (single) {
-      // the swizzle goes by the shared-memory address, so a box may begin at any row of an 8-row group
-      if (lane < 2 * it.n_tok) {
-        const int i = lane >> 1, half = lane & 1, s = i / p.tile_tok, r = (i % p.tile_tok) * p.group;
-        tma_load4(q_smem + s * TILE_BYTES + half * HALF_BYTES + r * 128, &maps.q1, half * 64, 0, it.kvh, it.tok + i, &sm.q_full);
+    // Queries: their buffer is free only when the item before is through, so the
+    // first keys and values go ahead of them while there is room.
+    bool asked = false;
+    auto queries = [&]() {
+      asked = true;
+      const bool two = it.n_tok > p.tile_tok;
+      warp_wait(&sm.q_empty, (q_count & 1) ^ 1, sm, err);
+      ++q_count;
+      const bool single = it.n_tok <= 8;
+      const uint32_t box_bytes = (uint32_t)p.group * 128u;
+      if (lane == 0)
+        mbar_arrive_expect_tx(&sm.q_full, single ? 2u * it.n_tok * box_bytes : (two ? 4u : 2u) * p.tile_tok * box_bytes);
+      __syncwarp();
+      if (single) {
+        // the swizzle goes by the shared-memory address, so a box may begin at any row of an 8-row group
+        if (lane < 2 * it.n_tok) {
+          const int i = lane >> 1, half = lane & 1, s = i / p.tile_tok, r = (i % p.tile_tok) * p.group;
+          tma_load4(q_smem + s * TILE_BYTES + half * HALF_BYTES + r * 128, &maps.q1, half * 64, 0, it.kvh, it.tok + i, &sm.q_full);
+        }
+      } else if (lane < (two ? 4 : 2)) {
+        const int s = lane >> 1, half = lane & 1;
+        tma_load4(q_smem + s * TILE_BYTES + half * HALF_BYTES, &maps.q, half * 64, 0, it.kvh, it.tok + s * p.tile_tok, &sm.q_full);
       }
-    } else if (lane < (two ? 4 : 2)) {
-      const int s = lane >> 1, half = lane & 1;
-      tma_load4(q_smem + s * TILE_BYTES + half * HALF_BYTES, &maps.q, half * 64, 0, it.kvh, it.tok + s * p.tile_tok, &sm.q_full);
-    }
+      __syncwarp();
+    };
     // keys and values
     for (int i = it.i0; i < it.i1; ++i, ++tiles) {
       const int row = (list_tile(it, i) * KT) & (page - 1) & ~(box - 1);
@@ -397,7 +401,11 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++fills) {
         const uint32_t st = fills % STAGES;
-        warp_wait(&sm.kv_empty[st], ((fills / STAGES) & 1) ^ 1, sm, err);
+        const uint32_t parity = ((fills / STAGES) & 1) ^ 1;
+        if (!asked && __any_sync(0xffffffffu, mbar_test_wait(&sm.q_empty, (q_count & 1) ^ 1) ||
+                                                  !mbar_test_wait(&sm.kv_empty[st], parity)))
+          queries();
+        warp_wait(&sm.kv_empty[st], parity, sm, err);
         if (lane == 0) {
           if (kv == 0) *(volatile int*)&sm.page_mask[tiles % MASKS] = (int)held;
           mbar_arrive_expect_tx(&sm.kv_full[st], TILE_BYTES);
@@ -412,6 +420,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
                     (lane & 1) * 64, row, it.kvh, c_page, &sm.kv_full[st]);
       }
     }
+    if (!asked) queries();
   }
   if (is_dead(sm) && lane == 0) {
     // copies in flight land before the CTA ends
