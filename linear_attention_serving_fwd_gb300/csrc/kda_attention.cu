@@ -40,6 +40,7 @@ constexpr int ROWS = 128;      // rows per query tile
 constexpr int STAGES = 5;      // K or V tiles in shared memory
 constexpr int TILE_BYTES = KT * D * 2;
 constexpr int HALF_BYTES = TILE_BYTES / 2;  // 64 of the 128 dimensions
+constexpr int MERGE_ROWS = 64; // rows whose joining leaves the first query tile alone
 constexpr int RING = 4;        // items ahead
 constexpr int MASKS = 8;       // page masks of the K tiles in flight
 constexpr int THREADS = 640;
@@ -72,7 +73,7 @@ struct Item {
 struct Smem {
   uint64_t kv_full[STAGES], kv_empty[STAGES];
   uint64_t ring_full[RING], ring_empty[RING];
-  uint64_t q_full, q_empty, q_read, merge_full;
+  uint64_t q_full, q_empty, q_read, merge_full, merge_free;
   uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t turn[2], drained[2];
   Item ring[RING];
@@ -83,6 +84,7 @@ struct Smem {
   long long start_before;
   uint32_t tmem;
   int dead;
+  int joined;  // results of two streams joined so far
   int last[2];
   unsigned poisoned[2][2][4];  // rows of a tile with a result that is not finite, by stream and half
   float share[2][2][ROWS];     // what the halves of a row tell each other
@@ -127,6 +129,23 @@ __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, Smem& sm, u
   if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, &sm.dead, err);
 }
 __device__ __forceinline__ bool is_dead(const Smem& sm) { return *(const volatile int*)&sm.dead != 0; }
+__device__ __forceinline__ void wait_joined(Smem& sm, int count, unsigned* err) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0; i < WAIT_CAP; ++i) {
+    int joined;
+    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(joined) : "r"(smem_u32(&sm.joined)) : "memory");
+    if (joined >= count || is_dead(sm)) break;
+    __nanosleep(64);
+    const uint64_t t = globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    else if (t - t0 > WAIT_NS) {
+      *(volatile int*)&sm.dead = 1;
+      set_error(err, ERR_TIMEOUT);
+      break;
+    }
+  }
+  __syncwarp();
+}
 // by a whole warp, which runs warp-wide instructions next
 __device__ __forceinline__ void warp_wait(uint64_t* bar, uint32_t parity, Smem& sm, unsigned* err) {
   wait(bar, parity, sm, err);
@@ -344,6 +363,8 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
   const int lane = threadIdx.x & 31;
   unsigned* err = p.a.err;
   uint32_t fills = 0, tiles = 0, q_count = 0;
+  int merges = 0;       // joined results before this item
+  int rows_before = 0;  // rows of the last block whose results are joined
   for (uint32_t items = 0;; ++items) {
     const uint32_t slot = items % RING;
     wait(&sm.ring_full[slot], (items / RING) & 1, sm, err);
@@ -375,6 +396,13 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
       const bool two = it.n_tok > p.tile_tok;
       warp_wait(&sm.q_empty, (q_count & 1) ^ 1, sm, err);
       ++q_count;
+      // Blocks of one tile join their results in the second tile's place, or in
+      // all of the buffer: the last such joining has to be over if it is in the
+      // way.  (A count and no barrier: this warp does not see every joining.)
+      if (two || rows_before > MERGE_ROWS) wait_joined(sm, merges, err);
+      const bool joins = !two && it.i1 - it.i0 > 1;
+      merges += joins;
+      if (joins) rows_before = it.n_tok * p.group;
       const bool single = it.n_tok <= 8;
       const uint32_t box_bytes = (uint32_t)p.group * 128u;
       if (lane == 0)
@@ -499,6 +527,12 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
     await(&sm.q_full, q_parity);
     q_parity ^= 1;
     const uint64_t qd = tc::smem_desc_sw128(q_addr + (two ? s * TILE_BYTES : 0));
+    int last = it.i1 - 1;  // this stream's last tile
+    if (two) {
+      while (last >= it.i0 && !active(act, last)) --last;
+    } else {
+      last -= (last - it.i0 - s) & 1;
+    }
     bool first = true;
     Stage st = next;
     bool scored = false;  // this tile's scores have been issued behind the last tile's product
@@ -511,10 +545,12 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
           tc::mma_f16(t_s, qd + (j >> 2) * (HALF_BYTES >> 4) + in, kd + (j >> 2) * k_half + in, id_qk, j > 0 ? 1u : 0u);
         }
         tc::mma_commit(&sm.s_full[s]);
-        // the first stream's last scores of a block of one tile: from here on the
-        // other stream's result may take the queries' place
-        if (!two && s == 0 && it.i1 - it.i0 > 1 && i + 2 >= it.i1) tc::mma_commit(&sm.q_read);
         tc::mma_commit(&sm.kv_empty[at.at]);
+        if (i == last) {
+          tc::mma_commit(&sm.q_empty);  // this stream's products have read the queries
+          // .. and the other stream's result may take their place, where it does
+          if (!two && s == 0 && it.i1 - it.i0 > 1 && it.n_tok * p.group > MERGE_ROWS) tc::mma_commit(&sm.q_read);
+        }
       }
       __syncwarp();
     };
@@ -581,10 +617,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
     next = st;
     if (elect_one()) {
       if (!first) tc::mma_commit(&sm.o_full[s]);
-      // the queries' buffer: free once both streams' products have read it; for a
-      // block of one tile the first warpgroup answers for its stream, once the
-      // two results have been joined in the buffer
-      if (two || s == 1) tc::mma_commit(&sm.q_empty);
+      else mbar_arrive(&sm.q_empty);  // nothing for this stream here
     }
     __syncwarp();
   }
@@ -800,7 +833,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
   const float sl = p.a.scale * LOG2E;
   const int all_held = (1 << p.boxes) - 1;
   const int box_shift = p.a.page_shift < 7 ? p.a.page_shift : 7;
-  uint32_t fills = 0, tiles = 0, s_count = 0, o_count = 0, merges = 0;
+  uint32_t fills = 0, tiles = 0, s_count = 0, o_count = 0, merges = 0, q_reads = 0;
   for (uint32_t items = 0;; ++items) {
     const uint32_t slot = items % RING;
     wait(&sm.ring_full[slot], (items / RING) & 1, sm, err);
@@ -823,6 +856,9 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
     const int clear_hi = hi_min - 64 - half * 64, clear_lo = lo_max - half * 64, clear_sink = sink_min - 64 - half * 64;
     float m = -CUDART_INF_F, l = 0.f;  // m is the row's, l this half's
     bool stepped = false;
+    // the other stream has read the last joined results (where they are, and
+    // what it was told with them, is written anew)
+    if (s == 1) warp_wait(&sm.merge_free, (merges & 1) ^ 1, sm, err);
     for (int i = two ? i0 : i0 + s; i < i1; i += two ? 1 : 2) {
       if (two && !active(it.act[s], i)) continue;
       const int first_key = list_tile(it, i) * KT, key = first_key + half * 64;
@@ -946,8 +982,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
     fills += 2 * (i1 - i0);
     tiles += i1 - i0;
     if (stepped) {
-      // the row's sum.  (Without a step the other stream may still be reading
-      // the last item's results here.)
+      // the row's sum
       sm.share[s][half][r] = l;
       named_bar_sync(pair, 64);
       l += sm.share[s][half ^ 1][r];
@@ -958,9 +993,13 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
     // m2: the reference in powers of two, -inf where the row has seen nothing
     float m2 = l == 0.f ? -CUDART_INF_F : m * sl;
     const bool merged = !two && i1 - i0 > 1;
+    unsigned char* merge = q_smem + (it.n_tok * p.group <= MERGE_ROWS ? TILE_BYTES : 0);
     if (!two && s == 1) {
       if (merged) {
-        warp_wait(&sm.q_read, merges & 1, sm, err);
+        if (merge == q_smem) {
+          warp_wait(&sm.q_read, q_reads & 1, sm, err);
+          ++q_reads;
+        }
         ++merges;
         // rows of 512 bytes, their 16-byte pieces rotated by the row: no bank conflicts
 #pragma unroll 1
@@ -970,7 +1009,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
           if (valid) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<float4*>(q_smem + r * 512 + (((half * 16 + c * 4 + j) ^ lane) << 4)) =
+              *reinterpret_cast<float4*>(merge + r * 512 + (((half * 16 + c * 4 + j) ^ lane) << 4)) =
                   make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
           }
           __syncwarp();
@@ -1023,7 +1062,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
       if (merged && valid) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float4 y = *reinterpret_cast<const float4*>(q_smem + r * 512 + (((half * 16 + c * 4 + j) ^ lane) << 4));
+          const float4 y = *reinterpret_cast<const float4*>(merge + r * 512 + (((half * 16 + c * 4 + j) ^ lane) << 4));
           v[4 * j] = v[4 * j] * w0 + y.x * w1;
           v[4 * j + 1] = v[4 * j + 1] * w0 + y.y * w1;
           v[4 * j + 2] = v[4 * j + 2] * w0 + y.z * w1;
@@ -1054,11 +1093,14 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.o_free[s]);
     }
-    if (!two && i1 > i0) {
-      // the next queries may land where the other stream's result was
+    if (merged) {
+      // queries may land where the other stream's result was
       fence_proxy_async_smem();
       named_bar_sync(bar, 256);
-      if ((threadIdx.x & 255) == 0) mbar_arrive(&sm.q_empty);
+      if ((threadIdx.x & 255) == 0) {
+        mbar_arrive(&sm.merge_free);
+        asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(&sm.joined)), "r"((int)merges) : "memory");
+      }
     }
     if (whole_pair) {
       if (half == 0 && valid && p.a.lse)
@@ -1116,6 +1158,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(&sm.q_empty, 2);
     mbar_init(&sm.q_read, 1);
     mbar_init(&sm.merge_full, 8);
+    mbar_init(&sm.merge_free, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.s_full[s], 1);
       mbar_init(&sm.p_full[s], 8);
@@ -1125,6 +1168,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&sm.o_free[s], 8);
     }
     sm.dead = 0;
+    sm.joined = 0;
     fence_mbar_init();
   }
   if (warp == MMA_WARP) {
