@@ -126,7 +126,9 @@ __device__ __noinline__ void wait_slow(uint64_t* bar, uint32_t parity, volatile 
   set_error(err, ERR_TIMEOUT);
 }
 __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, Smem& sm, unsigned* err) {
-  if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, &sm.dead, err);
+  uint32_t ok;
+  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  if (!ok) wait_slow(bar, parity, &sm.dead, err);
 }
 __device__ __forceinline__ bool is_dead(const Smem& sm) { return *(const volatile int*)&sm.dead != 0; }
 __device__ __forceinline__ void wait_joined(Smem& sm, int count, unsigned* err) {
