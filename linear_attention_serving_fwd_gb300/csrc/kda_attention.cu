@@ -78,7 +78,7 @@ struct Smem {
   uint64_t turn[2], drained[2];
   Item ring[RING];
   int page_mask[MASKS];
-  long long sums[THREADS / 32];
+  long long sums[SOFTMAX_WARPS];
   long long total;
   int start_b;
   long long start_before;
@@ -709,29 +709,37 @@ __device__ __forceinline__ void plan_role(const Params& p, Smem& sm, int cta, lo
 }
 
 // Costs of all requests: the line's length, and the request in which this CTA's
-// piece begins.
+// piece begins.  By the softmax warps, while the others set the CTA up; all
+// meet at the barrier inside.
 __device__ __forceinline__ long long measure_line(const Params& p, Smem& sm, int cta) {
+  constexpr int COUNTERS = SOFTMAX_WARPS * 32;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int each = (p.a.n_req + THREADS - 1) / THREADS;
-  long long cost = 0;
-  for (int j = 0; j < each; ++j) cost += request_cost(p, t * each + j, t * each + j < p.a.n_req, cta == 0);
-  long long upto = cost;
+  const bool counts = warp < SOFTMAX_WARPS;
+  const int each = (p.a.n_req + COUNTERS - 1) / COUNTERS;
+  long long cost = 0, upto = 0;
+  if (counts) {
+    for (int j = 0; j < each; ++j) cost += request_cost(p, t * each + j, t * each + j < p.a.n_req, cta == 0);
+    upto = cost;
 #pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, upto, m);
-    if (lane >= m) upto += x;
+    for (int m = 1; m < 32; m <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, m);
+      if (lane >= m) upto += x;
+    }
+    if (lane == 31) sm.sums[warp] = upto;
   }
-  if (lane == 31) sm.sums[warp] = upto;
+  tc::fence_before_sync();
   __syncthreads();
+  tc::fence_after_sync();
   long long total = 0;
-  for (int w = 0; w < THREADS / 32; ++w) {
+#pragma unroll
+  for (int w = 0; w < SOFTMAX_WARPS; ++w) {
     if (w < warp) upto += sm.sums[w];
     total += sm.sums[w];
   }
   const long long all = total * p.a.hkv;
   const long long piece = max(quotient(all + p.n_cta - 1, p.n_cta), (long long)p.min_piece);
   const long long u0 = cta * piece;
-  if (u0 < all) {
+  if (counts && u0 < all) {
     const long long w0 = u0 - quotient(u0, total) * total;
     long long before = upto - cost;
     const bool mine = before <= w0 && w0 < upto;
@@ -1147,7 +1155,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   unsigned char* kv_smem = q_smem + 2 * TILE_BYTES;
   Smem& sm = *reinterpret_cast<Smem*>(kv_smem + STAGES * TILE_BYTES);
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == PLAN_WARP * 32) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&sm.kv_full[i], 1);
       mbar_init(&sm.kv_empty[i], 2);  // both streams
@@ -1181,9 +1189,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   griddep_launch_dependents();
   griddep_wait();
   const long long piece = measure_line(p, sm, blockIdx.x);
-  tc::fence_before_sync();
   __syncthreads();
-  tc::fence_after_sync();
   const uint32_t tmem = sm.tmem;
   if (warp < SOFTMAX_WARPS) {
     softmax_role<FP16>(p, sm, q_smem, kv_smem, tmem);
