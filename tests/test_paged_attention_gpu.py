@@ -342,3 +342,57 @@ def test_refusals():
                                     args.pop("block_table"), **args)
     with pytest.raises(ValueError):
         kda.kda_kv_append(cache, c.q[:, :1], c.q[:1, :1], _i32([0, 1]))
+
+
+# --- mixtures and repetition: what the warps of a block hand to each other ------------
+
+@pytest.mark.parametrize("seed", range(8))
+def test_mixed_batches(seed):
+    """Single tokens, short windows, chunks of one and of several blocks, empty
+    requests and rows before the cache, in one call, groups of all kinds."""
+    r = np.random.default_rng(100 + seed)
+    hkv = int(r.choice([1, 2, 3]))
+    hq = hkv * int(r.choice([1, 2, 3, 5, 8, 16]))
+    new, kv = [], []
+    for _ in range(int(r.integers(3, 40))):
+        n = int(r.choice([0, 1, 1, 2, 5, 8, 9, 17, 40, 65, 130, 200]))
+        new.append(n)
+        kv.append(int(max(0, n + r.choice([-3, 0, 0, 1, 60, 127, 500, 1500]))))
+    c = Case(new, kv, hq, hkv, int(r.choice([16, 32, 64, 128, 256])), FP16 if seed % 2 else BF16,
+             ["tokens", "heads", "pairs"][seed % 3], seed=seed)
+    window, sinks = [(0, 0), (0, 0), (33, 1), (400, 130)][seed % 4]
+    first = c.run(window, sinks)
+    c.check(window, sinks, result=first)
+    ws = kda.paged_attention_workspace()
+    for _ in range(20):
+        again = c.run(window, sinks, workspace=ws)
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+    assert not ws[:4096].any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_scores_that_climb(dtype):
+    """Each row's maximum grows by a little from key to key, by hundreds over the
+    cache: the reference moves many times, in some rows of a warp and not in
+    others."""
+    c = Case([2, 150], [1500, 700], 2, 1, 64, dtype, seed=31)
+    direction = torch.ones(128, device="cuda", dtype=dtype)
+    c.q[::3] = direction  # every third token
+    for b in range(2):
+        for j, (page, row) in enumerate(c.rows(b)):
+            c.k[page, row] = c.k[page, row] * 0.05 + j / 60
+    out, lse = c.run()
+    want, want_lse, weight = paged.attention(_np(c.q), _np(c.k), _np(c.v), c.cu, c.kv, c.table, c.scale)
+    reach = float(np.abs(_np(c.q)).sum(-1).max() * np.abs(_np(c.k)).max() * c.scale)
+    eps, u = 128 * 2.0 ** -24 * reach, torch.finfo(dtype).eps / 2
+    small = 1500 * 2.0 ** -25 * float(c.v.float().abs().max()) if dtype == FP16 else 0.0
+    assert (np.abs(_np(out) - want) <= u * np.abs(want) + (u + 2 * eps) * weight * (1 + u) + small + 1e-30).all()
+    assert (np.abs(_np(lse) - want_lse) <= eps + 2.0 ** -22 * np.abs(want_lse)).all()
+
+
+@pytest.mark.parametrize("rows", [63, 64, 65, 100, 128])
+def test_blocks_of_one_tile(rows):
+    """Blocks that fit one tile, up to all of its rows, one after another in a
+    block's queue."""
+    Case([rows] * 40, [400 + rows] * 40, 1, 1, 64, seed=rows).check()
+    Case([rows // 4] * 20, [rows // 4 + 300] * 20, 4, 1, 16, FP16, seed=rows).check()
