@@ -589,7 +589,8 @@ int kda_kv_append(const kda_kv_cache* cache, const void* k, int64_t k_stride_tok
  *   sinks       >= 0: with a window, the first positions that stay visible
  *   workspace   16-byte aligned, kda_paged_attention_workspace_bytes() bytes, whose first
  *               KDA_ATTENTION_ZEROED_BYTES are zero before the first call;
- *               every call leaves them zero.  Calls that overlap on the GPU
+ *               every call leaves them zero (one that reports
+ *               KDA_ERR_DEVICE_TIMEOUT may not: zero them again).  Calls that overlap on the GPU
  *               need workspaces of their own.
  * An entry >= n_pages that a token would see, a kv_lens outside
  * [0, table_cols * page_size] and cu_seqlens that decrease or leave

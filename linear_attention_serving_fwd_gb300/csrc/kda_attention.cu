@@ -11,20 +11,35 @@
 // rows are (token, head of the group) pairs: 128 / G tokens by G heads.  A
 // block is two such tiles.  Keys come in tiles of 128, K and V 32 KB each.
 // Per key tile the tensor cores form S = Q K^T (128 x 128 x 128) and
-// O += P V (128 x 128 x 128); S, P and O live in tensor memory (S and P share
-// columns), Q, K and V in shared memory as the copies left them.
+// O += P V (128 x 128 x 128).  S (fp32), the weights P (16 bits, in the columns
+// of S that are read first) and O (fp32) of both query tiles fill the 512
+// columns of tensor memory; Q, K and V stay in shared memory as the copies left
+// them, 64 KB of queries and a ring of five K and V tiles.
 //
-// Warps.  Two softmax warpgroups (one thread a row), each with an S/P and an O
-// of its own: while one of them works on its S, the tensor cores serve the
-// other.  One warp copies (TMA: a box per page and half row), two issue the
-// matrix products, one lays out the work.  A block of one tile (single tokens,
-// short windows) gives both warpgroups the same rows and every other key tile;
-// their two results are joined in shared memory.
+// Streams.  Each query tile has an S, an O, an issuing warp and two softmax
+// warpgroups, one for each half of a tile's keys (a thread: one row, 64 keys):
+// while one stream works on its scores, the tensor cores serve the other.  A
+// block of one tile (single tokens, short windows) gives both streams the same
+// rows and every other key tile, and their results are joined in shared memory.
+// One warp copies, one lays out the work.  One warpgroup a stream, a thread a
+// whole row, was 4 % slower: the steps between the scores' barrier and the
+// weights' are a chain that the other stream has to cover.  Steps of 64 keys
+// with two S of a stream in tensor memory cover it better, but the products of
+// 64 columns read the queries twice as often, at shared memory's full rate, and
+// lost 5 % on the whole.
 //
-// Work.  The (key head, block) pairs in a row, each as long as its key tiles,
-// form one line that is cut into equal pieces, one per CTA.  A pair that a cut
-// divides leaves partial results (o, m, l) in the workspace; the CTA that
-// finishes the pair last joins them in the order of the line, so results do not depend on timing.
+// Work.  The (key head, block) pairs in a row, each as long as its key tiles
+// (and a lead for what it costs by itself), form one line that is cut into
+// equal pieces, one per CTA.  A pair that a cut divides leaves partial results
+// (o, m, l) in the workspace; the CTA that finishes the pair last joins them in
+// the order of the line, so results do not depend on timing.
+//
+// Bounds.  Prompt chunks are bound by the chain scores - weights - product of
+// two streams on one set of tensor cores: 8192 tokens over 24576 cached, 32
+// heads, take 2.90 ms (1330 TFLOP/s, the chip's power limit in force); 4096
+// over 4096 in a short run 1470 TFLOP/s, tensor cores 65 % busy.  Single tokens
+// are bound by memory: 256 requests over 4.2 GB of keys and values take 623 us
+// (6.8 TB/s).  A single request of 4096 tokens is a chain of latencies, 14.5 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math_constants.h>
@@ -46,6 +61,9 @@ constexpr int MASKS = 8;       // page masks of the K tiles in flight
 constexpr int THREADS = 640;
 constexpr int SOFTMAX_WARPS = 16;  // two warpgroups a stream
 constexpr int LOAD_WARP = 16, PLAN_WARP = 17, MMA_WARP = 18;  // MMA_WARP + 1: the second stream's
+// Lead of a block of two tiles and of one, in key tiles.  Measured against none:
+// prompts of 2048 tokens 246 -> 193 us, a window of 1024 over 8001 tokens 114 ->
+// 83 us, 128 single tokens 393 -> 369 us; 6 and 2, or 4 and 1, are 1 to 5 % behind.
 constexpr int LEAD_TWO = 4, LEAD_ONE = 2;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // The running reference follows the row's maximum only when 64 weights have
@@ -67,7 +85,8 @@ struct Item {
   int lo, hi, sink_hi; // keys that some row sees: [lo, hi) and [0, sink_hi)
   int act[2][3];       // a query tile sees list entries below [0] and in [[1], [2])
   int first, parts;    // CTA of the first part, parts of the pair
-  int part;            // this part's number; < 0 in place of b ends the work
+  int part;            // this part's number
+                       // b < 0 ends the work
 };
 
 struct Smem {
@@ -106,6 +125,10 @@ struct Params {
   float2* part_ml;         // [n_cta][2 slots][2 tiles][ROWS]
   float4* part_o;          // [n_cta][2 slots][2 tiles][ROWS / 8][32][8]: 16-byte pieces of 8 rows side by side
 };
+
+// Joined copies halve the number of boxes: with pages of 16, where the copy
+// engine's boxes are what limits, single tokens over 4096 cached take 343 us
+// instead of 472; with pages of 64 and more the two are alike.
 
 // hardware barriers: a pair of warps that share rows (stream, quarter), a stream's eight warps
 constexpr int PAIR_BAR = 1, STREAM_BAR = 9;
@@ -345,6 +368,7 @@ __device__ __forceinline__ long long request_cost(const Params& p, int b, bool v
 }
 
 // --- the copying warp ------------------------------------------------------------------
+// joined copies: k and v of five dimensions, else of four
 struct Maps {
   CUtensorMap k, v, q, q1;  // q: a tile's tokens in a box, q1: one token
 };
@@ -397,14 +421,15 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
       asked = true;
       const bool two = it.n_tok > p.tile_tok;
       warp_wait(&sm.q_empty, (q_count & 1) ^ 1, sm, err);
-      ++q_count;
       // Blocks of one tile join their results in the second tile's place, or in
       // all of the buffer: the last such joining has to be over if it is in the
       // way.  (A count and no barrier: this warp does not see every joining.)
       if (two || rows_before > MERGE_ROWS) wait_joined(sm, merges, err);
+      if (__any_sync(0xffffffffu, is_dead(sm))) return;
       const bool joins = !two && it.i1 - it.i0 > 1;
       merges += joins;
       if (joins) rows_before = it.n_tok * p.group;
+      ++q_count;
       const bool single = it.n_tok <= 8;
       const uint32_t box_bytes = (uint32_t)p.group * 128u;
       if (lane == 0)
@@ -436,6 +461,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
                                                   !mbar_test_wait(&sm.kv_empty[st], parity)))
           queries();
         warp_wait(&sm.kv_empty[st], parity, sm, err);
+        if (__any_sync(0xffffffffu, is_dead(sm))) goto out;
         if (lane == 0) {
           if (kv == 0) *(volatile int*)&sm.page_mask[tiles % MASKS] = (int)held;
           mbar_arrive_expect_tx(&sm.kv_full[st], TILE_BYTES);
@@ -452,6 +478,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
     }
     if (!asked) queries();
   }
+out:
   if (is_dead(sm) && lane == 0) {
     // copies in flight land before the CTA ends
     for (uint32_t f = fills > STAGES ? fills - STAGES : 0; f < fills; ++f)
@@ -461,8 +488,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
 }
 
 // --- the issuing warps -------------------------------------------------------------------
-// One warp a stream, so that neither waits for the other's softmax; the tensor
-// cores take the products of both as they come.  Every lane runs the role, so
+// One warp a stream, so that neither waits for the other's softmax.  Every lane runs the role, so
 // that its values are uniform and live in the registers that the tensor
 // instructions read; one elected lane issues.
 __device__ __forceinline__ bool elect_one() {
@@ -1281,6 +1307,9 @@ int launch_attention(const AttentionParams& a, bool fp16, void* workspace, cudaS
   p.n_cta = sm_count();
   const int page = 1 << a.page_shift;
   p.boxes = page < KT ? KT / page : 1;
+  // No piece below two key tiles, one a stream.  (Longer least pieces spare
+  // joinings but leave CTAs idle: one token over 4096 cached takes 14.5 us with 2,
+  // 18 with 8; a prompt of 512 tokens 24 and 28.)
   p.min_piece = 2;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   p.counters = reinterpret_cast<unsigned*>(ws);

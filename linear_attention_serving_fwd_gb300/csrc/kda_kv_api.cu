@@ -220,7 +220,10 @@ int kda_paged_attention(const kda_kv_cache* cache, const void* q, int64_t q_stri
   p.table = block_table; p.table_stride = table_stride; p.table_cols = table_cols;
   p.n_req = n_req; p.t_total = t_total; p.hq = hq; p.hkv = cache->hkv;
   p.n_pages = cache->n_pages;
-  p.scale = scale; p.window = window; p.sinks = window ? sinks : 0;
+  // a window of the whole row is no narrower than any: positions less the
+  // window then stay within 32 bits
+  const int32_t row = table_cols * cache->page_size;
+  p.scale = scale; p.window = window < row ? window : row; p.sinks = window ? sinks : 0;
   p.err = kda::device_error_word();
   if (!p.err) return fail(KDA_ERR_CUDA, "cannot resolve the device error word.");
   if (kda::launch_attention(p, cache->dtype == KDA_DTYPE_FP16, workspace, static_cast<cudaStream_t>(stream)) != 0)

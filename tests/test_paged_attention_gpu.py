@@ -396,3 +396,11 @@ def test_blocks_of_one_tile(rows):
     block's queue."""
     Case([rows] * 40, [400 + rows] * 40, 1, 1, 64, seed=rows).check()
     Case([rows // 4] * 20, [rows // 4 + 300] * 20, 4, 1, 16, FP16, seed=rows).check()
+
+
+@pytest.mark.parametrize("window", [2**31 - 1, 10**6, 321])
+def test_windows_past_the_table(window):
+    c = Case([200, 3], [130, 300], 2, 1, 64, seed=41)
+    a, b = c.run(window=window, sinks=3), c.run()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    c.check(result=a)
