@@ -148,10 +148,19 @@ __device__ __noinline__ void wait_slow(uint64_t* bar, uint32_t parity, volatile 
   *dead = 1;
   set_error(err, ERR_TIMEOUT);
 }
-__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, Smem& sm, unsigned* err) {
+// without a time hint: with one, waking took longer
+__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-  if (!ok) wait_slow(bar, parity, &sm.dead, err);
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, Smem& sm, unsigned* err) {
+  if (!try_wait(bar, parity)) wait_slow(bar, parity, &sm.dead, err);
 }
 __device__ __forceinline__ bool is_dead(const Smem& sm) { return *(const volatile int*)&sm.dead != 0; }
 __device__ __forceinline__ void wait_joined(Smem& sm, int count, unsigned* err) {
@@ -170,6 +179,12 @@ __device__ __forceinline__ void wait_joined(Smem& sm, int count, unsigned* err) 
     }
   }
   __syncwarp();
+}
+// the same; false once the CTA is marked
+__device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, Smem& sm, unsigned* err) {
+  if (try_wait(bar, parity)) return true;
+  wait_slow(bar, parity, &sm.dead, err);
+  return !is_dead(sm);
 }
 // by a whole warp, which runs warp-wide instructions next
 __device__ __forceinline__ void warp_wait(uint64_t* bar, uint32_t parity, Smem& sm, unsigned* err) {
@@ -460,8 +475,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
         if (!asked && __any_sync(0xffffffffu, mbar_test_wait(&sm.q_empty, (q_count & 1) ^ 1) ||
                                                   !mbar_test_wait(&sm.kv_empty[st], parity)))
           queries();
-        warp_wait(&sm.kv_empty[st], parity, sm, err);
-        if (__any_sync(0xffffffffu, is_dead(sm))) goto out;
+        if (!__all_sync(0xffffffffu, wait_or_stop(&sm.kv_empty[st], parity, sm, err))) goto out;
         if (lane == 0) {
           if (kv == 0) *(volatile int*)&sm.page_mask[tiles % MASKS] = (int)held;
           mbar_arrive_expect_tx(&sm.kv_full[st], TILE_BYTES);
@@ -799,52 +813,70 @@ __device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xfffff
 // read, whole lines.
 __device__ __forceinline__ size_t part_piece(size_t row, int c) { return ((row >> 3) * 32 + c) * 8 + (row & 7); }
 
-// Joins a tile's parts, by the stream's warpgroups that finished the last of them.
-template <bool FP16>
-__device__ __forceinline__ void join_parts(const Params& p, Smem& sm, int s, const Item& it, int tile, int n_rows) {
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 7, bar = STREAM_BAR + s;
+// Joins rows of a tile's parts: a unit is 8 rows by 4 PIECES pieces, a lane one
+// row and PIECES pieces.
+template <bool FP16, int PIECES>
+__device__ __forceinline__ void join_rows(const Params& p, Smem& sm, int s, const Item& it, int tile, int n_rows) {
+  constexpr int UNITS = 8 / PIECES;  // of 8 rows
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 7;
   const int parts = it.parts, first = it.first;
-  auto part_row = [&](int k, int row) { return (((size_t)(first + k) * 2 + (k == 0 ? 1 : 0)) * 2 + tile) * ROWS + row; };
-  if ((threadIdx.x & 255) < 4) sm.poisoned[s][0][threadIdx.x & 3] = 0;
-  named_bar_sync(bar, 256);
-  // a unit: 8 rows by 8 pieces; a lane: one row, two pieces
-  for (int u = warp; u < (n_rows + 7) / 8 * 4; u += 8) {
-    const bool real = (u >> 2) * 8 + (lane & 7) < n_rows;
-    const int row = min((u >> 2) * 8 + (lane & 7), n_rows - 1), c = (u & 3) * 8 + (lane >> 3);
-    float top = -CUDART_INF_F, l = 0.f, o[8];
+  for (int u = warp; u < (n_rows + 7) / 8 * UNITS; u += 8) {
+    const bool real = u / UNITS * 8 + (lane & 7) < n_rows;
+    const int row = min(u / UNITS * 8 + (lane & 7), n_rows - 1), c = u % UNITS * 4 * PIECES + (lane >> 3);
+    float top = -CUDART_INF_F, l = 0.f, o[4 * PIECES];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = 0.f;
-#pragma unroll 4
+    for (int j = 0; j < 4 * PIECES; ++j) o[j] = 0.f;
+#pragma unroll(PIECES > 2 ? 1 : 4)
     for (int k = 0; k < parts; ++k) {
-      const size_t at = part_row(k, row);
+      const size_t at = (((size_t)(first + k) * 2 + (k == 0 ? 1 : 0)) * 2 + tile) * ROWS + row;
       const float2 ml = __ldcg(&p.part_ml[at]);
-      const float4 x = __ldcg(&p.part_o[part_piece(at, c)]), y = __ldcg(&p.part_o[part_piece(at, c + 4)]);
-      const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      float4 z[PIECES];
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) z[i] = __ldcg(p.part_o + part_piece(at, c) + i * 32);  // 4 pieces on
       // a part that has seen nothing stored nothing
       const bool some = ml.x != -CUDART_INF_F;
       const float reach = fmaxf(top, ml.x);
       const float corr = top == reach ? 1.f : ex2(top - reach), w = some ? ex2(ml.x - reach) : 0.f;
       l = l * corr + (some ? w * ml.y : 0.f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = o[j] * corr + (some ? w * z[j] : 0.f);
+      for (int i = 0; i < PIECES; ++i) {
+        const float v[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[4 * i + j] = o[4 * i + j] * corr + (some ? w * v[j] : 0.f);
+      }
       top = reach;
     }
     if (!real) continue;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     float poison = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4 * PIECES; ++j) {
       o[j] *= inv;
       poison += o[j] * 0.f;  // NaN from then on when one is not finite
     }
     if (poison != 0.f) atomicOr(&sm.poisoned[s][0][row >> 5], 1u << (row & 31));
     const int tok = it.tok + tile * p.tile_tok + row / p.group, head = it.kvh * p.group + row % p.group;
-    __nv_bfloat16* out = p.a.out + ((int64_t)tok * p.a.hq + head) * D;
-    *reinterpret_cast<uint2*>(out + c * 4) = make_uint2(act_pack2<FP16>(o[0], o[1]), act_pack2<FP16>(o[2], o[3]));
-    *reinterpret_cast<uint2*>(out + c * 4 + 16) = make_uint2(act_pack2<FP16>(o[4], o[5]), act_pack2<FP16>(o[6], o[7]));
+    __nv_bfloat16* out = p.a.out + ((int64_t)tok * p.a.hq + head) * D + c * 4;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+      *reinterpret_cast<uint2*>(out + i * 16) =
+          make_uint2(act_pack2<FP16>(o[4 * i], o[4 * i + 1]), act_pack2<FP16>(o[4 * i + 2], o[4 * i + 3]));
     if (p.a.lse && c == 0)
       p.a.lse[(int64_t)tok * p.a.hq + head] = l == 0.f ? -CUDART_INF_F : (top + log2f(l) - WEIGHT_EXP<FP16>) * LN2;
   }
+}
+
+// Joins a tile's parts, by the stream's warpgroups that finished the last of
+// them.  Many rows: a lane takes a quarter of its row, so that each part's loads
+// are many.  Few: a sixteenth, so that all warps have some, and several parts'
+// loads at once.
+template <bool FP16>
+__device__ __forceinline__ void join_parts(const Params& p, Smem& sm, int s, const Item& it, int tile, int n_rows) {
+  const int warp = (threadIdx.x >> 5) & 7, bar = STREAM_BAR + s;
+  if ((threadIdx.x & 255) < 4) sm.poisoned[s][0][threadIdx.x & 3] = 0;
+  named_bar_sync(bar, 256);
+  if (n_rows > 32) join_rows<FP16, 8>(p, sm, s, it, tile, n_rows);
+  else join_rows<FP16, 2>(p, sm, s, it, tile, n_rows);
   __syncwarp();
   named_bar_sync(bar, 256);
   unsigned bad = warp < 4 ? sm.poisoned[s][0][warp] : 0;
@@ -1307,10 +1339,11 @@ int launch_attention(const AttentionParams& a, bool fp16, void* workspace, cudaS
   p.n_cta = sm_count();
   const int page = 1 << a.page_shift;
   p.boxes = page < KT ? KT / page : 1;
-  // No piece below two key tiles, one a stream.  (Longer least pieces spare
-  // joinings but leave CTAs idle: one token over 4096 cached takes 14.5 us with 2,
-  // 18 with 8; a prompt of 512 tokens 24 and 28.)
-  p.min_piece = 2;
+  // No piece below two key tiles, one a stream: one token over 4096 cached takes
+  // 14.5 us with 2, 18 with 8.  Where most blocks are full tiles, joining them
+  // costs more: a prompt of 512 tokens takes 24.1 us with 2, 22.5 with 4 and 28
+  // with 6, one of 299 with 8 heads 20.5, 12.8 and 24.
+  p.min_piece = (int64_t)a.t_total * p.group > (int64_t)ROWS * a.n_req ? 4 : 2;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   p.counters = reinterpret_cast<unsigned*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + KDA_ATTENTION_ZEROED_BYTES);
