@@ -20,7 +20,10 @@
 // warpgroups, one for each half of a tile's keys (a thread: one row, 64 keys):
 // while one stream works on its scores, the tensor cores serve the other.  A
 // block of one tile (single tokens, short windows) gives both streams the same
-// rows and every other key tile, and their results are joined in shared memory.
+// rows and every other key tile, and their results are joined in shared memory;
+// the streams lead such blocks in turn, so that two blocks of one key tile run
+// side by side (106 requests of at most 17 cached tokens 29.8 -> 23.1 us, mixed
+// batches within 2 % either way).
 // One warp copies, one lays out the work.  One warpgroup a stream, a thread a
 // whole row, was 4 % slower: the steps between the scores' barrier and the
 // weights' are a chain that the other stream has to cover.  Steps of 64 keys
@@ -36,10 +39,11 @@
 //
 // Bounds.  Prompt chunks are bound by the chain scores - weights - product of
 // two streams on one set of tensor cores: 8192 tokens over 24576 cached, 32
-// heads, take 2.90 ms (1330 TFLOP/s, the chip's power limit in force); 4096
-// over 4096 in a short run 1470 TFLOP/s, tensor cores 65 % busy.  Single tokens
-// are bound by memory: 256 requests over 4.2 GB of keys and values take 623 us
-// (6.8 TB/s).  A single request of 4096 tokens is a chain of latencies, 14.5 us.
+// heads, take 2.77 to 2.86 ms (1390 to 1344 TFLOP/s, the chip's power limit in
+// force); 4096 over 4096 in a short run 1470 TFLOP/s, tensor cores 65 % busy.
+// Single tokens are bound by memory: 256 requests over 4.2 GB of keys and values
+// take 608 to 623 us (6.9 to 6.8 TB/s).  A single request of 4096 tokens is a
+// chain of latencies, 14.5 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math_constants.h>
@@ -86,6 +90,7 @@ struct Item {
   int act[2][3];       // a query tile sees list entries below [0] and in [[1], [2])
   int first, parts;    // CTA of the first part, parts of the pair
   int part;            // this part's number
+  int lead;            // block of one tile: the stream that takes its even key tiles and the results
                        // b < 0 ends the work
 };
 
@@ -561,6 +566,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
     it.i0 = uniform(from.i0);
     it.i1 = uniform(from.i1);
     const int act[3] = {uniform(from.act[s][0]), uniform(from.act[s][1]), uniform(from.act[s][2])};
+    const int odd = uniform(from.lead) ^ s;  // block of one tile: this stream takes every other key tile
     if (elect_one()) mbar_arrive(&sm.ring_empty[slot]);
     __syncwarp();
     if (it.b < 0) break;
@@ -573,7 +579,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
     if (two) {
       while (last >= it.i0 && !active(act, last)) --last;
     } else {
-      last -= (last - it.i0 - s) & 1;
+      last -= (last - it.i0 - odd) & 1;
     }
     bool first = true;
     Stage st = next;
@@ -591,7 +597,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
         if (i == last) {
           tc::mma_commit(&sm.q_empty);  // this stream's products have read the queries
           // .. and the other stream's result may take their place, where it does
-          if (!two && s == 0 && it.i1 - it.i0 > 1 && it.n_tok * p.group > MERGE_ROWS) tc::mma_commit(&sm.q_read);
+          if (!two && !odd && it.i1 - it.i0 > 1 && it.n_tok * p.group > MERGE_ROWS) tc::mma_commit(&sm.q_read);
         }
       }
       __syncwarp();
@@ -599,7 +605,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
     for (int i = it.i0; i < it.i1; ++i, st.skip(2)) {
       Stage sv = st;
       sv.skip(1);
-      if (two ? !active(act, i) : ((i - it.i0) & 1) != s) {
+      if (two ? !active(act, i) : ((i - it.i0) & 1) != odd) {
         // hidden from every row, or the other stream's: both streams see every
         // fill, so that none is two fills behind (a wait tells odd from even)
         await(&sm.kv_full[st.at], st.parity);
@@ -676,6 +682,7 @@ __device__ __forceinline__ void plan_role(const Params& p, Smem& sm, int cta, lo
   const long long total = sm.total, all = total * p.a.hkv;
   const long long u0 = cta * piece, u1 = min(all, u0 + piece);
   uint32_t items = 0;
+  int turn = 0;
   bool ok = true;
   auto post = [&](const Item& it) {
     const uint32_t slot = items % RING;
@@ -713,6 +720,8 @@ __device__ __forceinline__ void plan_role(const Params& p, Smem& sm, int cta, lo
         it.first = (int)quotient(s, piece);
         it.parts = (int)quotient(e - 1, piece) - it.first + 1;
         it.part = cta - it.first;
+        it.lead = turn;
+        turn ^= 1;
         tile_range(p, it, 0);
         tile_range(p, it, 1);
         post(it);
@@ -909,7 +918,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
     const Item& it = sm.ring[slot];
     if (it.b < 0) break;
     const bool two = it.n_tok > p.tile_tok;
-    const int tile = two ? s : 0, i0 = it.i0, i1 = it.i1, kv = it.kv;
+    const int tile = two ? s : 0, i0 = it.i0, i1 = it.i1, kv = it.kv, odd = it.lead ^ s;
     const int tb = tile * p.tile_tok + row_tok;
     const bool valid = row_tok < p.tile_tok && tb < it.n_tok;
     const int pos = it.pos + tb;
@@ -924,10 +933,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
     const int clear_hi = hi_min - 64 - half * 64, clear_lo = lo_max - half * 64, clear_sink = sink_min - 64 - half * 64;
     float m = -CUDART_INF_F, l = 0.f;  // m is the row's, l this half's
     bool stepped = false;
-    // the other stream has read the last joined results (where they are, and
-    // what it was told with them, is written anew)
-    if (s == 1) warp_wait(&sm.merge_free, (merges & 1) ^ 1, sm, err);
-    for (int i = two ? i0 : i0 + s; i < i1; i += two ? 1 : 2) {
+    // the last joined results have been read (where they are, and what was told
+    // with them, is written anew)
+    warp_wait(&sm.merge_free, (merges & 1) ^ 1, sm, err);
+    for (int i = two ? i0 : i0 + odd; i < i1; i += two ? 1 : 2) {
       if (two && !active(it.act[s], i)) continue;
       const int first_key = list_tile(it, i) * KT, key = first_key + half * 64;
       const bool clear = first_key <= clear_hi && (first_key >= clear_lo || first_key <= clear_sink);
@@ -1062,7 +1071,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
     float m2 = l == 0.f ? -CUDART_INF_F : m * sl;
     const bool merged = !two && i1 - i0 > 1;
     unsigned char* merge = q_smem + (it.n_tok * p.group <= MERGE_ROWS ? TILE_BYTES : 0);
-    if (!two && s == 1) {
+    if (!two && odd) {
       if (merged) {
         if (merge == q_smem) {
           warp_wait(&sm.q_read, q_reads & 1, sm, err);
@@ -1084,13 +1093,13 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
         }
         named_bar_sync(pair, 64);  // both halves have read their sums
         if (half == 0) {
-          sm.share[1][0][r] = m2;
-          sm.share[1][1][r] = l;
+          sm.share[s][0][r] = m2;
+          sm.share[s][1][r] = l;
         }
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&sm.o_free[1]);
+          mbar_arrive(&sm.o_free[s]);
           mbar_arrive(&sm.merge_full);
         }
       }
@@ -1102,7 +1111,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
     if (merged) {
       warp_wait(&sm.merge_full, merges & 1, sm, err);
       ++merges;
-      const float2 other = make_float2(sm.share[1][0][r], sm.share[1][1][r]);
+      if (merge == q_smem) ++q_reads;  // over: the other stream has waited for it
+      const float2 other = make_float2(sm.share[s ^ 1][0][r], sm.share[s ^ 1][1][r]);
       const float top = fmaxf(m2, other.x);
       if (top == -CUDART_INF_F) {
         l = 0.f;
@@ -1341,8 +1351,8 @@ int launch_attention(const AttentionParams& a, bool fp16, void* workspace, cudaS
   p.boxes = page < KT ? KT / page : 1;
   // No piece below two key tiles, one a stream: one token over 4096 cached takes
   // 14.5 us with 2, 18 with 8.  Where most blocks are full tiles, joining them
-  // costs more: a prompt of 512 tokens takes 24.1 us with 2, 22.5 with 4 and 28
-  // with 6, one of 299 with 8 heads 20.5, 12.8 and 24.
+  // costs more: a prompt of 512 tokens takes 20.9 us with 2, 19.2 with 4 and 23.8
+  // with 6, one of 299 with 8 heads 17.4, 12.7 and 21.3.
   p.min_piece = (int64_t)a.t_total * p.group > (int64_t)ROWS * a.n_req ? 4 : 2;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   p.counters = reinterpret_cast<unsigned*>(ws);

@@ -398,6 +398,20 @@ def test_blocks_of_one_tile(rows):
     Case([rows // 4] * 20, [rows // 4 + 300] * 20, 4, 1, 16, FP16, seed=rows).check()
 
 
+@pytest.mark.parametrize("rows", [64, 65, 128])
+def test_many_blocks_of_one_tile(rows):
+    """Several such blocks in each queue, of one key tile to four, so that either
+    stream leads and blocks that join their streams' results follow one another."""
+    r = np.random.default_rng(rows)
+    kv = [int(rows // 2 + n) for n in r.integers(1, 400, 600)]
+    c = Case([rows // 2] * 600, kv, 2, 1, 128, seed=rows)
+    first = c.run()
+    c.check(result=first)
+    for _ in range(10):
+        again = c.run()
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
 @pytest.mark.parametrize("window", [2**31 - 1, 10**6, 321])
 def test_windows_past_the_table(window):
     c = Case([200, 3], [130, 300], 2, 1, 64, seed=41)
