@@ -1059,7 +1059,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
     fills += 2 * (i1 - i0);
     tiles += i1 - i0;
     if (stepped) {
-      // the row's sum
+      // The row's sum goes where the maximum was: the other half may have yet to
+      // read that when the last tile moved the reference.  (No room for a second
+      // array; the last product is still under way.)
+      named_bar_sync(pair, 64);
       sm.share[s][half][r] = l;
       named_bar_sync(pair, 64);
       l += sm.share[s][half ^ 1][r];

@@ -418,3 +418,24 @@ def test_windows_past_the_table(window):
     a, b = c.run(window=window, sinks=3), c.run()
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     c.check(result=a)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("kv", [65, 100, 128, 129])
+def test_halves_of_a_tile_that_differ(kv, dtype):
+    """One or two key tiles, whose last moves the reference, the larger scores in
+    one half of the keys or in the other: both halves have to weigh against the
+    same reference, time after time."""
+    c = Case([1, 30, 2, 128] * 50, [kv] * 200, 2, 2, 32, dtype, seed=kv)
+    c.q[..., :64] = 1.0  # 64 dimensions that set a key's score for all rows alike
+    for b in range(200):
+        rows = torch.tensor(c.rows(b), device="cuda")
+        first_half = torch.arange(kv, device="cuda") % 128 < 64
+        level = torch.where(first_half == (b % 3 == 0), 1.0, -1.0) * (1 + b % 5) / 8
+        c.k[rows[:, 0], rows[:, 1], :, :64] = level[:, None, None].to(dtype)
+    first = c.run()
+    c.check(result=first)
+    ws = kda.paged_attention_workspace()
+    for _ in range(30):
+        again = c.run(workspace=ws)
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
