@@ -1070,8 +1070,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
       ++o_count;
       tc::fence_after_sync();
     }
-    // m2: the reference in powers of two, -inf where the row has seen nothing
-    float m2 = l == 0.f ? -CUDART_INF_F : m * sl;
+    // m2: the reference in powers of two, -inf where the row has seen nothing, and
+    // there alone: scores that are all NaN leave no maximum, but a sum, which has
+    // to reach the parts' joining.
+    float m2 = l == 0.f ? -CUDART_INF_F : m == -CUDART_INF_F ? 0.f : m * sl;
     const bool merged = !two && i1 - i0 > 1;
     unsigned char* merge = q_smem + (it.n_tok * p.group <= MERGE_ROWS ? TILE_BYTES : 0);
     if (!two && odd) {

@@ -439,3 +439,43 @@ def test_halves_of_a_tile_that_differ(kv, dtype):
     for _ in range(30):
         again = c.run(workspace=ws)
         assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
+# --- visible NaN, in blocks that several CTAs or both streams share ---------------------
+
+def _nan_rows(c, bad, window=0, sinks=0):
+    """Rows ``bad`` [T, Hq] are NaN throughout, the others as if nothing were."""
+    out, lse = c.run(window, sinks)
+    assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+    assert torch.isfinite(out[~bad]).all() and torch.isfinite(lse[~bad]).all()
+    k, v, q = [torch.nan_to_num(x.float(), 0.0).double().cpu().numpy() for x in (c.k, c.v, c.q)]
+    want, want_lse, _ = paged.attention(q, k, v, c.cu, c.kv, c.table, c.scale, window, sinks)
+    clean = (torch.from_numpy(want).to(out), torch.from_numpy(want_lse).to(lse))
+    out, lse = torch.where(bad[..., None], clean[0], out), torch.where(bad, clean[1], lse)
+    c.check(window, sinks, result=(out, lse), q=torch.from_numpy(q), k=torch.from_numpy(k), v=torch.from_numpy(v))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("new,kv", [([1], [9000]), ([1], [200]), ([1, 3], [20000, 300]), ([3], [5]), ([160], [5000]),
+                                    ([300, 1], [2600, 1]), ([20] * 40, [600] * 40)])
+def test_a_query_that_is_nan(new, kv, dtype):
+    c = Case(new, kv, 4, 2, 64, dtype, seed=51)
+    bad = torch.zeros(c.q.shape[:2], dtype=torch.bool, device="cuda")
+    bad[0, 1] = bad[-1, 2] = bad[len(bad) // 2, 3] = True
+    c.q[bad.nonzero(as_tuple=True)[0], bad.nonzero(as_tuple=True)[1], 17] = float("nan")
+    _nan_rows(c, bad)
+    _nan_rows(c, bad, window=500, sinks=4)
+
+
+@pytest.mark.parametrize("new,kv,at", [([1, 1], [9000, 9000], (0, 1280)), ([1, 1], [9000, 300], (2000, 3300)),
+                                       ([2, 40], [20000, 700], (17000, 20000)), ([1, 1], [256, 80], (128, 256)),
+                                       ([1, 1], [256, 80], (0, 128)), ([140, 1], [4000, 90], (256, 1800))])
+def test_a_run_of_keys_that_are_nan(new, kv, at):
+    """All keys of several tiles, more than a part of a divided block: the rows of
+    that request and key head are NaN, whatever the other parts hold."""
+    c = Case(new, kv, 4, 2, 64, seed=52)
+    rows = torch.tensor(c.rows(0)[at[0]:at[1]], device="cuda")
+    c.k[rows[:, 0], rows[:, 1], 1] = float("nan")
+    bad = torch.zeros(c.q.shape[:2], dtype=torch.bool, device="cuda")
+    bad[:new[0], 2:] = True
+    _nan_rows(c, bad)
