@@ -8,6 +8,7 @@ rejected drafts and finished requests back.  Argument marshalling only.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional
 
@@ -27,6 +28,15 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def _stream(stream, device):
     return _raw_stream(device) if stream is None else stream.cuda_stream
+
+
+_CURRENT = contextlib.nullcontext()
+
+
+def _makes_on(stream):
+    """What a call makes for itself or returns is made on the stream that it runs
+    on: a workspace is zeroed there first, and memory is reused in its order."""
+    return _CURRENT if stream is None else torch.cuda.stream(stream)
 
 
 def _int32(t, name, numel=None):
@@ -119,15 +129,18 @@ def kda_kv_extend(pages: KvPages, new_lens, max_tokens: int, *, cu_seqlens=None,
     most ``max_tokens`` in all.  Updates ``pages``; returns (cu_seqlens
     [n_req + 1], slot_map [max_tokens], step_lens [n_req]), int32: the packed
     layout, each token's slot (-1 where its request found no pages), and the
-    lengths that attention takes (0 where the request was not admitted)."""
+    lengths that attention takes (0 where the request was not admitted).  What
+    the call makes belongs to ``stream`` where one is given: another stream that
+    uses it waits for that one, and records itself on the tensor."""
     n = pages.n_req
     new = _int32(new_lens, "new_lens", n)
-    if cu_seqlens is None:
-        cu_seqlens = torch.empty(n + 1, dtype=torch.int32, device=pages.device)
-    if slot_map is None:
-        slot_map = torch.empty(max_tokens, dtype=torch.int32, device=pages.device)
-    if step_lens is None:
-        step_lens = torch.empty(n, dtype=torch.int32, device=pages.device)
+    with _makes_on(stream):
+        if cu_seqlens is None:
+            cu_seqlens = torch.empty(n + 1, dtype=torch.int32, device=pages.device)
+        if slot_map is None:
+            slot_map = torch.empty(max_tokens, dtype=torch.int32, device=pages.device)
+        if step_lens is None:
+            step_lens = torch.empty(n, dtype=torch.int32, device=pages.device)
     rc = _native.lib().kda_kv_extend(
         pages._ref, new, _int32(cu_seqlens, "cu_seqlens", n + 1), _int32(slot_map, "slot_map", max_tokens), max_tokens,
         _int32(step_lens, "step_lens", n), _stream(stream, pages._index))
@@ -174,21 +187,23 @@ def kda_paged_attention(cache: KvCache, q, cu_seqlens, kv_lens, block_table, *, 
     ``window`` > 0 a token sees the last ``window`` positions, its own among
     them, and the first ``sinks``.  Returns (out [T, Hq, 128], lse fp32
     [T, Hq] or None).  ``workspace``: :func:`paged_attention_workspace`, made
-    for the call when not given."""
+    for the call when not given.  What the call makes belongs to ``stream``, as
+    in :func:`kda_kv_extend`."""
     t, hq, qp, qt, qh = _rows(q, "q", cache.dtype)
     n = kv_lens.numel()
-    if out is None:
-        out = torch.empty((t, hq, D), dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or not out.is_cuda:
-        raise ValueError("out must be a contiguous CUDA tensor of q's shape and dtype.")
-    if lse is None:
-        lse = torch.empty((t, hq), dtype=torch.float32, device=q.device) if return_lse else None
-    elif tuple(lse.shape) != (t, hq) or lse.dtype != torch.float32 or not lse.is_contiguous() or not lse.is_cuda:
-        raise ValueError("lse must be a contiguous float32 CUDA tensor [T, Hq].")
-    if workspace is None:
-        workspace = paged_attention_workspace(q.device)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or not workspace.is_cuda:
-        raise ValueError("workspace must be a contiguous uint8 CUDA tensor.")
+    with _makes_on(stream):
+        if out is None:
+            out = torch.empty((t, hq, D), dtype=q.dtype, device=q.device)
+        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or not out.is_cuda:
+            raise ValueError("out must be a contiguous CUDA tensor of q's shape and dtype.")
+        if lse is None:
+            lse = torch.empty((t, hq), dtype=torch.float32, device=q.device) if return_lse else None
+        elif tuple(lse.shape) != (t, hq) or lse.dtype != torch.float32 or not lse.is_contiguous() or not lse.is_cuda:
+            raise ValueError("lse must be a contiguous float32 CUDA tensor [T, Hq].")
+        if workspace is None:
+            workspace = paged_attention_workspace(q.device)
+        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or not workspace.is_cuda:
+            raise ValueError("workspace must be a contiguous uint8 CUDA tensor.")
     table, table_stride, cols = _table(block_table, n)
     rc = _native.lib().kda_paged_attention(
         cache._ref, qp, qt, qh, hq, t, out.data_ptr(), None if lse is None else lse.data_ptr(),

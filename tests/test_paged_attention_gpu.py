@@ -479,3 +479,37 @@ def test_a_run_of_keys_that_are_nan(new, kv, at):
     bad = torch.zeros(c.q.shape[:2], dtype=torch.bool, device="cuda")
     bad[:new[0], 2:] = True
     _nan_rows(c, bad)
+
+
+def test_a_call_on_another_stream_makes_what_it_needs_there():
+    """No workspace and no outputs given, the current stream busy: the call on the
+    other stream waits for nothing of it, and finishes right."""
+    c = Case([1, 2, 150], [9000, 700, 300], 4, 2, 64, seed=61)
+    want = c.run()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    n = kda.paged_attention_workspace().numel()
+    for stream in (torch.cuda.current_stream(), s):  # both pools hold blocks of the workspace's size that are not zero
+        with torch.cuda.stream(stream):
+            used = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+            del used
+    pages = kda.KvPages.empty(2, 4, 8, 16)
+    cache, args = kda.KvCache(c.k, c.v), [_i32(x) for x in (c.cu, c.kv, c.table, [5, 20])]
+    lens = pages.kv_lens.clone()
+
+    def calls():
+        got = [kda.kda_paged_attention(cache, c.q, *args[:3], return_lse=True, stream=s) for _ in range(3)]
+        return got, kda.kda_kv_extend(pages, args[3], 25, stream=s)
+
+    calls()  # kernels are loaded and pools grown, which the current stream may have to wait for
+    kda.kda_kv_truncate(pages, lens, stream=s)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)  # about 0.2 s
+    got, (cu, slots, step) = calls()
+    s.synchronize()
+    assert not torch.cuda.current_stream().query()
+    torch.cuda.synchronize()
+    for out, lse in got:
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert cu.tolist() == [0, 5, 25] and step.tolist() == [5, 20]
+    assert slots.tolist() == list(range(5)) + list(range(16, 36))
