@@ -496,6 +496,7 @@ def test_a_call_on_another_stream_makes_what_it_needs_there():
     pages = kda.KvPages.empty(2, 4, 8, 16)
     cache, args = kda.KvCache(c.k, c.v), [_i32(x) for x in (c.cu, c.kv, c.table, [5, 20])]
     lens = pages.kv_lens.clone()
+    torch.cuda.synchronize()
 
     def calls():
         got = [kda.kda_paged_attention(cache, c.q, *args[:3], return_lse=True, stream=s) for _ in range(3)]
