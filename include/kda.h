@@ -531,7 +531,9 @@ int kda_kv_extend(const kda_kv_pages* pages, const int32_t* new_lens, int32_t* c
  * hand the pages past them back: rejected drafts, finished requests (0).
  * Pages return to the stack in descending (request, column) order, so a
  * truncate to the former lengths undoes a kda_kv_extend exactly.  Returned
- * table entries become -1; keep_lens[b] >= kv_lens[b] changes nothing; a
+ * table entries become -1.  A negative entry (a page that left a window, handed
+ * back by whoever took it out) is not handed back, nor is one >= n_pages, which
+ * sets KDA_ERR_DEVICE_INDEX.  keep_lens[b] >= kv_lens[b] changes nothing; a
  * negative one, or a kv_lens outside its row, sets KDA_ERR_DEVICE_INDEX and
  * leaves the request alone; a stack that would pass n_pages sets it too, and
  * the pages past it are not handed back.

@@ -179,13 +179,17 @@ __global__ void __launch_bounds__(PT) kv_extend_kernel(KvPagesParams p) {
   }
 }
 
-// Requests from the last to the first, one per thread and round.
+// Requests from the last to the first, one per thread and round.  The columns
+// they give up are read in the stack's order, a thread each, and those that hold
+// a page move together: a page that left a window has been handed back by
+// whoever put a negative entry in its place.
 __global__ void __launch_bounds__(PT) kv_truncate_kernel(KvPagesParams p) {
   __shared__ long long sums[32][2];
-  __shared__ int page_off[PT], r_have[PT];
-  const int t = threadIdx.x, page = 1 << p.page_shift;
+  __shared__ int page_off[PT], r_have[PT], held[2][32];  // held: pages of each warp, by parity of the step
+  const int t = threadIdx.x, lane = t & 31, page = 1 << p.page_shift;
   const int count = clamped_count(p, t == 0);
   long long base = 0;
+  int step = 0;
   for (int r0 = 0; r0 < p.n_req; r0 += PT) {
     const int b = p.n_req - 1 - (r0 + t), n_round = min(PT, p.n_req - r0);
     long long drop = 0;
@@ -204,19 +208,34 @@ __global__ void __launch_bounds__(PT) kv_truncate_kernel(KvPagesParams p) {
     page_off[t] = (int)(s.b - drop);
     r_have[t] = have;
     __syncthreads();
-    for (long long i = t; i < s.total_b; i += PT) {
-      const int r = owner(page_off, n_round, (int)i);
-      const int col = r_have[r] - 1 - ((int)i - page_off[r]);
-      int32_t* entry = p.table + (int64_t)(p.n_req - 1 - (r0 + r)) * p.table_stride + col;
-      const long long at = count + base + i;
-      if (at < p.n_pages) {
-        p.free_pages[at] = *entry;
-        *entry = -1;
-      } else {
-        set_error(p.err, ERR_INDEX);
+    for (long long i0 = 0; i0 < s.total_b; i0 += PT, step ^= 1) {
+      const long long i = i0 + t;
+      int32_t* entry = nullptr;
+      int pg = -1;
+      if (i < s.total_b) {
+        const int r = owner(page_off, n_round, (int)i);
+        const int col = r_have[r] - 1 - ((int)i - page_off[r]);
+        entry = p.table + (int64_t)(p.n_req - 1 - (r0 + r)) * p.table_stride + col;
+        pg = *entry;
+        if (pg >= p.n_pages) {
+          set_error(p.err, ERR_INDEX);
+          pg = -1;
+        }
       }
+      const unsigned pages = __ballot_sync(0xffffffffu, pg >= 0);
+      if (lane == 0) held[step][t >> 5] = __popc(pages);
+      __syncthreads();
+      const int n = held[step][lane];
+      const int before = __reduce_add_sync(0xffffffffu, lane < (t >> 5) ? n : 0) + __popc(pages & ((1u << lane) - 1));
+      const long long at = count + base + before;
+      if (pg >= 0 && at >= p.n_pages) {
+        set_error(p.err, ERR_INDEX);
+      } else if (entry) {
+        if (pg >= 0) p.free_pages[at] = pg;
+        *entry = -1;
+      }
+      base += __reduce_add_sync(0xffffffffu, n);
     }
-    base += s.total_b;
     __syncthreads();
   }
   if (t == 0) *p.free_count = (int)min(count + base, (long long)p.n_pages);

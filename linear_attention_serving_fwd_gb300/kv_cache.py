@@ -151,7 +151,8 @@ def kda_kv_extend(pages: KvPages, new_lens, max_tokens: int, *, cu_seqlens=None,
 
 def kda_kv_truncate(pages: KvPages, keep_lens, *, stream=None) -> None:
     """Keep the first ``keep_lens`` [n_req] tokens of each request (int32,
-    CUDA) and hand the pages past them back."""
+    CUDA) and hand the pages past them back.  A negative table entry, a page
+    that the caller has handed back itself, is passed over."""
     rc = _native.lib().kda_kv_truncate(pages._ref, _int32(keep_lens, "keep_lens", pages.n_req),
                                        _stream(stream, pages._index))
     if rc:

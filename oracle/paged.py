@@ -25,11 +25,14 @@ def extend(kv_lens, table, free, new_lens, page):
     return cu, slots, step
 
 
-def truncate(kv_lens, table, free, keep_lens, page):
+def truncate(kv_lens, table, free, keep_lens, page, n_pages=None):
+    """Entries that are no page (negative, or ``n_pages`` and above) are not
+    handed back."""
     for b in reversed(range(len(kv_lens))):
         keep = min(keep_lens[b], kv_lens[b])
         for col in reversed(range(-(-keep // page), -(-kv_lens[b] // page))):
-            free.append(table[b][col])
+            if table[b][col] >= 0 and (n_pages is None or table[b][col] < n_pages):
+                free.append(table[b][col])
             table[b][col] = -1
         kv_lens[b] = keep
 

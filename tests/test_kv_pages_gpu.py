@@ -165,6 +165,48 @@ def test_bad_truncations():
     assert kda.kda_device_status(clear=True) == INDEX and b.gpu.kv_lens.tolist() == [100, 16]
 
 
+def _give_up(b, at):
+    """The pages of columns ``at`` [(request, column)] back onto the stack by hand,
+    negative entries in their place."""
+    g = b.gpu
+    for i, (r, col) in enumerate(at):
+        n = len(b.free)
+        g.free_pages[n], g.block_table[r, col] = b.table[r][col], -1 - i
+        b.free.append(b.table[r][col])
+        b.table[r][col] = -1 - i
+    g.free_count.fill_(len(b.free))
+
+
+@pytest.mark.parametrize("lens,cols,at", [
+    ([40, 33], 4, [(0, 0), (1, 1)]),
+    ([700, 64, 1], 60, [(0, c) for c in range(0, 43)] + [(1, 3)]),
+    ([17000, 5, 20000], 1300, [(0, c) for c in range(0, 1062, 3)] + [(2, c) for c in range(1100)]),  # several rounds
+    ([33] * 1500, 4, [(r, 1) for r in range(0, 1500, 7)]),
+])
+def test_pages_given_up_are_not_handed_back(lens, cols, at):
+    b = Both(lens, 16, cols, 9, seed=7)
+    _give_up(b, at)
+    b.truncate([n // 2 if i % 2 else 0 for i, n in enumerate(lens)])
+    assert kda.kda_device_status() == 0
+    b.extend([min(300, 16 * cols - n) if i < 3 else 0 for i, n in enumerate(b.lens)])
+    b.truncate([0] * len(lens))
+    assert kda.kda_device_status() == 0 and sorted(b.free) == list(range(len(b.free)))
+    assert int(b.gpu.free_count) == b.gpu.free_pages.numel()  # all of them, each once
+
+
+def test_entries_past_the_cache_are_not_handed_back():
+    b = Both([40, 33], 16, 4, 1)
+    n = b.gpu.free_pages.numel()
+    for r, col, bad in ((0, 1, n), (1, 0, 2**31 - 1)):
+        b.table[r][col] = bad
+        b.gpu.block_table[r, col] = bad
+    free = list(b.free)
+    paged.truncate(b.lens, b.table, b.free, [0, 0], 16, n_pages=n)
+    kda.kda_kv_truncate(b.gpu, _i32([0, 0]))
+    assert kda.kda_device_status(clear=True) == INDEX and len(b.free) == len(free) + 4
+    b.same()
+
+
 # --- append --------------------------------------------------------------------
 
 def _caches(layout, n_pages, page, hkv, dtype):

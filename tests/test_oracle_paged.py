@@ -77,3 +77,13 @@ def test_the_first_request_without_pages_ends_the_admission():
     lens, table, free = [16, 15, 0, 0], [[1, -1], [2, -1], [-1, -1], [-1, -1]], [3]
     cu, slots, step = paged.extend(lens, table, free, [20, 1, 0, 1], 16)
     assert step == [0, 16, 0, 0] and slots == [-1] * 20 + [2 * 16 + 15, -1] and free == [3] and cu[-1] == 22
+
+
+def test_pages_given_up_are_not_handed_back():
+    lens, table, free = [40, 33], [[7, 3, 5, -1], [1, 2, 9, -1]], [4]
+    table[0][0], free = -1, free + [7]  # left a window: the caller has handed it back
+    table[1][1] = 12                    # no page of a cache of ten
+    paged.truncate(lens, table, free, [0, 1], 16, n_pages=10)
+    assert lens == [0, 1] and table == [[-1] * 4, [1, -1, -1, -1]] and free == [4, 7, 9, 5, 3]
+    _, slots, _ = paged.extend(lens, table, free, [17, 0], 16)
+    assert slots == list(range(48, 64)) + [80] and free == [4, 7, 9]
