@@ -64,7 +64,8 @@ __device__ __forceinline__ Scan2 block_scan2(long long a, long long b, long long
 
 // Last i in [0, n) with off[i] <= x (off non-decreasing, off[0] <= x): the
 // owner of element x when off holds exclusive sums.
-__device__ __forceinline__ int owner(const int* off, int n, int x) {
+template <typename T>
+__device__ __forceinline__ int owner(const T* off, int n, T x) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -98,7 +99,8 @@ __device__ __forceinline__ int clamped_count(const KvPagesParams& p, bool report
 // updates the lengths and the free count, once all have read them.
 __global__ void __launch_bounds__(PT) kv_extend_kernel(KvPagesParams p) {
   __shared__ long long sums[32][2];
-  __shared__ int tok_off[PT], page_off[PT], r_len[PT], r_have[PT];  // r_have < 0: not admitted
+  __shared__ long long page_off[PT];  // what a round asks for can pass 32 bits, though no free list does
+  __shared__ int tok_off[PT], r_len[PT], r_have[PT];  // r_have < 0: not admitted
   const int t = threadIdx.x, page = 1 << p.page_shift;
   const int rank = cluster_rank(), stride = PT * (int)gridDim.x, first = rank * PT + t;
   const int count = clamped_count(p, first == 0);
@@ -125,7 +127,7 @@ __global__ void __launch_bounds__(PT) kv_extend_kernel(KvPagesParams p) {
     const Scan2 s = block_scan2(n_new, add, sums);
     const bool fits = valid && (add == 0 || page_base + s.b <= count);
     tok_off[t] = (int)min(tok_base + s.a - n_new, 0x7fffffffLL);
-    page_off[t] = (int)(s.b - add);
+    page_off[t] = s.b - add;
     r_len[t] = len;
     r_have[t] = fits ? have : -1;
     // admitted pages are a prefix of the sums: the first refusal ends it
@@ -145,9 +147,9 @@ __global__ void __launch_bounds__(PT) kv_extend_kernel(KvPagesParams p) {
     const long long tok_end = min(tok_base + s.total_a, (long long)p.max_tokens);
     const int pages_end = (int)min(s.total_b, max(0LL, count - page_base));
     for (int i = first; i < pages_end; i += stride) {
-      const int r = owner(page_off, n_round, i);
+      const int r = owner(page_off, n_round, (long long)i);
       if (r_have[r] < 0) continue;
-      const int col = r_have[r] + i - page_off[r];
+      const int col = r_have[r] + (int)(i - page_off[r]);
       p.table[(int64_t)(r0 + r) * p.table_stride + col] = p.free_pages[count - 1 - (page_base + i)];
     }
 #pragma unroll 4
@@ -185,7 +187,8 @@ __global__ void __launch_bounds__(PT) kv_extend_kernel(KvPagesParams p) {
 // whoever put a negative entry in its place.
 __global__ void __launch_bounds__(PT) kv_truncate_kernel(KvPagesParams p) {
   __shared__ long long sums[32][2];
-  __shared__ int page_off[PT], r_have[PT], held[2][32];  // held: pages of each warp, by parity of the step
+  __shared__ long long page_off[PT];
+  __shared__ int r_have[PT], held[2][32];  // held: pages of each warp, by parity of the step
   const int t = threadIdx.x, lane = t & 31, page = 1 << p.page_shift;
   const int count = clamped_count(p, t == 0);
   long long base = 0;
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(PT) kv_truncate_kernel(KvPagesParams p) {
       }
     }
     const Scan2 s = block_scan2(0, drop, sums);
-    page_off[t] = (int)(s.b - drop);
+    page_off[t] = s.b - drop;
     r_have[t] = have;
     __syncthreads();
     for (long long i0 = 0; i0 < s.total_b; i0 += PT, step ^= 1) {
@@ -213,8 +216,8 @@ __global__ void __launch_bounds__(PT) kv_truncate_kernel(KvPagesParams p) {
       int32_t* entry = nullptr;
       int pg = -1;
       if (i < s.total_b) {
-        const int r = owner(page_off, n_round, (int)i);
-        const int col = r_have[r] - 1 - ((int)i - page_off[r]);
+        const int r = owner(page_off, n_round, i);
+        const int col = r_have[r] - 1 - (int)(i - page_off[r]);
         entry = p.table + (int64_t)(p.n_req - 1 - (r0 + r)) * p.table_stride + col;
         pg = *entry;
         if (pg >= p.n_pages) {

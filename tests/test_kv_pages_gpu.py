@@ -207,6 +207,19 @@ def test_entries_past_the_cache_are_not_handed_back():
     b.same()
 
 
+def test_a_batch_that_asks_for_more_pages_than_32_bits_count():
+    n, cols = 48, (1 << 27) - 1
+    table = torch.empty(n, cols, dtype=torch.int32, device="cuda")  # rows of 2^31 tokens: 26 GB
+    table[:, :4] = -1
+    g = kda.KvPages(_i32([0] * n), table, _i32(list(range(31, -1, -1))), _i32([32]), 16)
+    new = [20, 5] + [2**31 - 20] * (n - 2)
+    cu, slots, step = kda.kda_kv_extend(g, _i32(new), 25)
+    assert kda.kda_device_status(clear=True) == INDEX  # more tokens than the slot map
+    assert step.tolist() == [20, 5] + [0] * (n - 2) and int(g.free_count) == 29
+    assert table[:3, :3].tolist() == [[0, 1, -1], [2, -1, -1], [-1, -1, -1]]
+    assert slots.tolist() == list(range(20)) + list(range(32, 37))
+
+
 # --- append --------------------------------------------------------------------
 
 def _caches(layout, n_pages, page, hkv, dtype):
