@@ -108,9 +108,10 @@ struct Smem {
   long long start_before;
   uint32_t tmem;
   int dead;
+  int beat;    // changes while rows are formed again, which may take longer than a wait
   int joined;  // results of two streams joined so far
   int last[2];
-  unsigned poisoned[2][2][4];  // rows of a tile with a result that is not finite, by stream and half
+  unsigned poisoned[2][2][4];  // rows of a tile with a sum, and a result that is not finite, by stream and half
   float share[2][2][ROWS];     // what the halves of a row tell each other
 };
 
@@ -142,15 +143,28 @@ constexpr int PAIR_BAR = 1, STREAM_BAR = 9;
 // A wait that expires (bounded as all waits are) marks the CTA: its other waits
 // then return at once, and the roles run out.  What they still do stays inside
 // the CTA's own memory; only the ring of items is not read on.
-__device__ __noinline__ void wait_slow(uint64_t* bar, uint32_t parity, volatile int* dead, unsigned* err) {
+// The time since the last sign of life counts: one row has as many keys as the
+// request, and 32 of them may be formed again between two waits of the others.
+struct Patience {
   uint64_t t0 = 0;
-  for (uint32_t i = 0; i < WAIT_CAP && !*dead; ++i) {
-    if (mbar_try_wait(bar, parity)) return;
+  int beat = 0;
+  __device__ __forceinline__ bool over(const volatile Smem& sm) {
     const uint64_t t = globaltimer_ns();
-    if (t0 == 0) t0 = t;
-    else if (t - t0 > WAIT_NS) break;
+    const int now = sm.beat;
+    if (t0 == 0 || now != beat) {
+      t0 = t;
+      beat = now;
+    }
+    return t - t0 > WAIT_NS;
   }
-  *dead = 1;
+};
+__device__ __noinline__ void wait_slow(uint64_t* bar, uint32_t parity, volatile Smem& sm, unsigned* err) {
+  Patience patience;
+  for (uint32_t i = 0; i < WAIT_CAP && !sm.dead; ++i) {
+    if (mbar_try_wait(bar, parity)) return;
+    if (patience.over(sm)) break;
+  }
+  sm.dead = 1;
   set_error(err, ERR_TIMEOUT);
 }
 // without a time hint: with one, waking took longer
@@ -165,19 +179,17 @@ __device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, Smem& sm, unsigned* err) {
-  if (!try_wait(bar, parity)) wait_slow(bar, parity, &sm.dead, err);
+  if (!try_wait(bar, parity)) wait_slow(bar, parity, sm, err);
 }
 __device__ __forceinline__ bool is_dead(const Smem& sm) { return *(const volatile int*)&sm.dead != 0; }
 __device__ __forceinline__ void wait_joined(Smem& sm, int count, unsigned* err) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 0; i < WAIT_CAP; ++i) {
+  Patience patience;
+  for (uint32_t i = 0;; ++i) {
     int joined;
     asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(joined) : "r"(smem_u32(&sm.joined)) : "memory");
     if (joined >= count || is_dead(sm)) break;
     __nanosleep(64);
-    const uint64_t t = globaltimer_ns();
-    if (t0 == 0) t0 = t;
-    else if (t - t0 > WAIT_NS) {
+    if (i == WAIT_CAP || patience.over(sm)) {
       *(volatile int*)&sm.dead = 1;
       set_error(err, ERR_TIMEOUT);
       break;
@@ -188,7 +200,7 @@ __device__ __forceinline__ void wait_joined(Smem& sm, int count, unsigned* err) 
 // the same; false once the CTA is marked
 __device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, Smem& sm, unsigned* err) {
   if (try_wait(bar, parity)) return true;
-  wait_slow(bar, parity, &sm.dead, err);
+  wait_slow(bar, parity, sm, err);
   return !is_dead(sm);
 }
 // by a whole warp, which runs warp-wide instructions next
@@ -268,13 +280,72 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// --- one row, by one warp ----------------------------------------------------------
-// The definition row by row, four of the 128 dimensions a lane.  The tiles'
-// products multiply the values of hidden keys by a weight of 0, which is not 0
-// where such a value is NaN or infinite: a row whose tiled result is not finite
-// is formed again here from the keys that it sees alone.
+// --- rows whose result is not finite -----------------------------------------------
+// The tiles' products multiply the values of hidden keys by a weight of 0, which
+// is not 0 where such a value is NaN or infinite, and weights against a reference
+// that stands may sum to more than fp32 holds.  (Hidden scores never count: a row
+// whose sum is NaN is NaN.)  So the rest of the rows that are not finite are
+// looked at again: where the values that they see account for it, the result
+// stands; else the row is formed again from the keys that it sees alone.
+// Bound by latency, groups of 8 keys at once.  A NaN or an infinity early in the
+// cache: 8192 tokens over 24576 of 32 heads 13.7 ms (2.6 without it), 512 over
+// 7680 of 8 heads 0.3 ms.  A NaN among the tokens themselves, which half a tile's
+// rows do not see: 126 ms and 26 ms; 256 over 130,816 of 8 heads 548 ms.
+constexpr int GROUP = 8;
+
+// Four dimensions a lane of the rows' values: bits 0-3 NaN, 4-7 inf, 8-11 -inf.
+__device__ __forceinline__ unsigned classify(const float (&v)[4]) {
+  unsigned f = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (v[i] != v[i]) f |= 1u << i;
+    if (v[i] == CUDART_INF_F) f |= 16u << i;
+    if (v[i] == -CUDART_INF_F) f |= 256u << i;
+  }
+  return f;
+}
+
+// What the values of keys [from, to) hold, by a warp that takes every other group
+// of them; ends early where every dimension has a NaN.
 template <bool FP16>
-__device__ __forceinline__ void attend_row(const AttentionParams& p, int b, int tok, int head, int pos, int kv) {
+__device__ __forceinline__ unsigned scan_values(const AttentionParams& p, Smem& sm, const int32_t* table, int kvh, int from, int to,
+                                                int half, unsigned f) {
+  const int lane = threadIdx.x & 31, page = 1 << p.page_shift;
+  const __nv_bfloat16* vc = p.vc + (int64_t)kvh * p.vc_sh + lane * 4;
+#pragma unroll 1
+  for (int g = from / GROUP + ((from / GROUP ^ half) & 1); g * GROUP < to; g += 2) {
+    if (__all_sync(0xffffffffu, (f & 15) == 15)) break;
+    if (lane == 0) *(volatile int*)&sm.beat = (int)clock();
+    const int pg = table[(g * GROUP) >> p.page_shift];  // pages hold whole groups
+    if (pg < 0 || pg >= p.n_pages) continue;
+    float poison = 0.f;
+    uint2 raw[GROUP];
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) {
+      const int row = min(max(g * GROUP + i, from), to - 1) & (page - 1);
+      raw[i] = *reinterpret_cast<const uint2*>(vc + pg * p.vc_sp + row * p.vc_st);
+    }
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) {
+      float v[4];
+      load_act4<FP16>(reinterpret_cast<const __nv_bfloat16*>(&raw[i]), v);
+      poison += v[0] * 0.f + v[1] * 0.f + v[2] * 0.f + v[3] * 0.f;
+    }
+    if (poison != 0.f) {
+#pragma unroll
+      for (int i = 0; i < GROUP; ++i) {
+        float v[4];
+        load_act4<FP16>(reinterpret_cast<const __nv_bfloat16*>(&raw[i]), v);
+        f |= classify(v);
+      }
+    }
+  }
+  return f;
+}
+
+// The definition row by row, by one warp, four of the 128 dimensions a lane.
+template <bool FP16>
+__device__ __forceinline__ void attend_row(const AttentionParams& p, Smem& sm, int b, int tok, int head, int pos, int kv) {
   const int lane = threadIdx.x & 31;
   const int kvh = head / (p.hq / p.hkv), page = 1 << p.page_shift;
   float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -CUDART_INF_F, l = 0.f;
@@ -285,29 +356,43 @@ __device__ __forceinline__ void attend_row(const AttentionParams& p, int b, int 
   const __nv_bfloat16* vc = p.vc + (int64_t)kvh * p.vc_sh + lane * 4;
 #pragma unroll 1
   for (int part = 0; part < 2; ++part) {
-    const int end = part == 0 ? min(min(p.sinks, lo), hi) : hi;
-    int j = part == 0 ? 0 : lo;
-    while (j < end) {
-      const int stop = min(end, ((j >> p.page_shift) + 1) << p.page_shift);
-      const int pg = table[j >> p.page_shift];
-      if (pg < 0 || pg >= p.n_pages) {
-        j = stop;
-        continue;
-      }
+    const int from = part == 0 ? 0 : lo, to = part == 0 ? min(min(p.sinks, lo), hi) : hi;
 #pragma unroll 1
-      for (; j < stop; ++j) {
-        const int row = j & (page - 1);
-        float k[4], v[4];
-        load_act4<FP16>(kc + pg * p.kc_sp + row * p.kc_st, k);
-        load_act4<FP16>(vc + pg * p.vc_sp + row * p.vc_st, v);
-        const float s = p.scale * warp_sum(q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3]);
-        const float top = fmaxf(m, s);
-        if (top == -CUDART_INF_F && s == s) continue;  // e^s = 0, and no maximum yet
-        const float corr = m == -CUDART_INF_F ? 0.f : expf(m - top), w = expf(s - top);
-        l = l * corr + w;
+    for (int g = from / GROUP; g * GROUP < to; ++g) {
+      if (lane == 0) *(volatile int*)&sm.beat = (int)clock();
+      const int pg = table[(g * GROUP) >> p.page_shift];
+      if (pg < 0 || pg >= p.n_pages) continue;
+      uint2 raw[GROUP];
+      float s[GROUP], top = m;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = o[i] * corr + w * v[i];
-        m = top;
+      for (int i = 0; i < GROUP; ++i) {
+        const int row = min(max(g * GROUP + i, from), to - 1) & (page - 1);
+        float k[4];
+        load_act4<FP16>(kc + pg * p.kc_sp + row * p.kc_st, k);
+        raw[i] = *reinterpret_cast<const uint2*>(vc + pg * p.vc_sp + row * p.vc_st);
+        s[i] = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
+      }
+#pragma unroll
+      for (int i = 0; i < GROUP; ++i) {
+        s[i] = p.scale * warp_sum(s[i]);
+        if (g * GROUP + i >= from && g * GROUP + i < to) top = fmaxf(top, s[i]);
+      }
+      // without a maximum every score is -inf (or NaN: not here, the row's sum is a number), e^s = 0
+      if (top == -CUDART_INF_F) continue;
+      const float corr = m == -CUDART_INF_F ? 0.f : expf(m - top);
+      m = top;
+      l *= corr;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] *= corr;
+#pragma unroll
+      for (int i = 0; i < GROUP; ++i) {
+        if (g * GROUP + i < from || g * GROUP + i >= to || s[i] == -CUDART_INF_F) continue;
+        const float w = expf(s[i] - top);
+        float v[4];
+        load_act4<FP16>(reinterpret_cast<const __nv_bfloat16*>(&raw[i]), v);
+        l += w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] += w * v[j];
       }
     }
   }
@@ -315,6 +400,44 @@ __device__ __forceinline__ void attend_row(const AttentionParams& p, int b, int 
   __nv_bfloat16* out = p.out + ((int64_t)tok * p.hq + head) * D + lane * 4;
   *reinterpret_cast<uint2*>(out) = make_uint2(act_pack2<FP16>(o[0] * inv, o[1] * inv), act_pack2<FP16>(o[2] * inv, o[3] * inv));
   if (p.lse && lane == 0) p.lse[(int64_t)tok * p.hq + head] = l == 0.f ? -CUDART_INF_F : m + logf(l);
+}
+
+// Rows ``bad`` of 32 of a tile, whose results stand in memory, by the two warps
+// that share them.  A visible value early in a long cache reaches every row after
+// it: the values that all of them see are read once for all.
+template <bool FP16>
+__device__ __forceinline__ void mend_rows(const Params& p, Smem& sm, int s, int half, int quarter, int bar, const Item& it, int tile,
+                                          unsigned bad) {
+  const int lane = threadIdx.x & 31, r = quarter * 32 + lane;
+  const bool mine = (bad >> lane) & 1;
+  const int tb = tile * p.tile_tok + r / p.group, pos = it.pos + tb;
+  const int hi = __reduce_min_sync(0xffffffffu, mine ? min(pos + 1, it.kv) : 0x7fffffff);
+  const int lo = __reduce_max_sync(0xffffffffu, mine && p.a.window ? max(0, pos + 1 - p.a.window) : 0);
+  const int32_t* table = p.a.table + (int64_t)it.b * p.a.table_stride;
+  unsigned f = 0;
+  f = scan_values<FP16>(p.a, sm, table, it.kvh, 0, min(min(p.a.sinks, lo), hi), half, f);
+  f = scan_values<FP16>(p.a, sm, table, it.kvh, lo, hi, half, f);
+  sm.share[s][half][r] = __uint_as_float(f);
+  named_bar_sync(bar, 64);
+  f |= __float_as_uint(sm.share[s][half ^ 1][r]);
+  int turn = 0;
+  while (bad) {
+    const int src = __ffs(bad) - 1, row = quarter * 32 + src;
+    bad &= bad - 1;
+    if ((turn++ & 1) != half) continue;
+    const int i = tile * p.tile_tok + row / p.group, tok = it.tok + i, head = it.kvh * p.group + row % p.group;
+    float o[4];
+    load_act4<FP16>(p.a.out + ((int64_t)tok * p.a.hq + head) * D + lane * 4, o);
+    bool stands = true;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool nan = (f >> j) & 1, inf = (f >> (4 + j)) & 1, neg = (f >> (8 + j)) & 1;
+      if (o[j] != o[j]) stands = stands && (nan || (inf && neg));
+      else if (o[j] == CUDART_INF_F) stands = stands && inf;
+      else if (o[j] == -CUDART_INF_F) stands = stands && neg;
+    }
+    if (!__all_sync(0xffffffffu, stands)) attend_row<FP16>(p.a, sm, it.b, tok, head, it.pos + i, it.kv);
+  }
 }
 
 // --- the line of work ----------------------------------------------------------------
@@ -863,7 +986,7 @@ __device__ __forceinline__ void join_rows(const Params& p, Smem& sm, int s, cons
       o[j] *= inv;
       poison += o[j] * 0.f;  // NaN from then on when one is not finite
     }
-    if (poison != 0.f) atomicOr(&sm.poisoned[s][0][row >> 5], 1u << (row & 31));
+    if (poison != 0.f && l == l) atomicOr(&sm.poisoned[s][0][row >> 5], 1u << (row & 31));
     const int tok = it.tok + tile * p.tile_tok + row / p.group, head = it.kvh * p.group + row % p.group;
     __nv_bfloat16* out = p.a.out + ((int64_t)tok * p.a.hq + head) * D + c * 4;
 #pragma unroll
@@ -888,13 +1011,9 @@ __device__ __forceinline__ void join_parts(const Params& p, Smem& sm, int s, con
   else join_rows<FP16, 2>(p, sm, s, it, tile, n_rows);
   __syncwarp();
   named_bar_sync(bar, 256);
-  unsigned bad = warp < 4 ? sm.poisoned[s][0][warp] : 0;
-  while (bad) {
-    const int row = warp * 32 + __ffs(bad) - 1;
-    bad &= bad - 1;
-    const int i = tile * p.tile_tok + row / p.group;
-    attend_row<FP16>(p.a, it.b, it.tok + i, it.kvh * p.group + row % p.group, it.pos + i, it.kv);
-  }
+  const int quarter = warp & 3;
+  const unsigned bad = sm.poisoned[s][0][quarter];
+  if (bad) mend_rows<FP16>(p, sm, s, warp >> 2, quarter, PAIR_BAR + s * 4 + quarter, it, tile, bad);
 }
 
 template <bool FP16>
@@ -1188,16 +1307,11 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
     if (whole_pair) {
       if (half == 0 && valid && p.a.lse)
         p.a.lse[(int64_t)tok * p.a.hq + head] = l == 0.f ? -CUDART_INF_F : (m2 + log2f(l) - WEIGHT_EXP<FP16>) * LN2;
-      const unsigned mine = __ballot_sync(0xffffffffu, valid && poison != 0.f);
+      const unsigned mine = __ballot_sync(0xffffffffu, valid && poison != 0.f && l == l);
       if (lane == 0) sm.poisoned[s][half][quarter] = mine;
-      named_bar_sync(pair, 64);  // the row's own stores come before those of attend_row
-      unsigned bad = half == 0 ? mine | sm.poisoned[s][1][quarter] : 0;
-      while (bad) {
-        const int src = __ffs(bad) - 1;
-        bad &= bad - 1;
-        attend_row<FP16>(p.a, it.b, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, head, src),
-                         __shfl_sync(0xffffffffu, pos, src), kv);
-      }
+      named_bar_sync(pair, 64);  // the row's own stores come before what is read of them
+      const unsigned bad = mine | sm.poisoned[s][half ^ 1][quarter];
+      if (bad) mend_rows<FP16>(p, sm, s, half, quarter, pair, it, tile, bad);
     } else {
       if (half == 0 && valid) __stcg(&p.part_ml[part_row], make_float2(m2, l));
       named_bar_sync(bar, 256);
@@ -1250,7 +1364,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&sm.o_full[s], 1);
       mbar_init(&sm.o_free[s], 8);
     }
-    sm.dead = 0;
+    sm.dead = sm.beat = 0;
     sm.joined = 0;
     fence_mbar_init();
   }

@@ -514,3 +514,96 @@ def test_a_call_on_another_stream_makes_what_it_needs_there():
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     assert cu.tolist() == [0, 5, 25] and step.tolist() == [5, 20]
     assert slots.tolist() == list(range(5)) + list(range(16, 36))
+
+
+# --- visible values that are not finite ------------------------------------------------
+
+def _check_values(c, window=0, sinks=0, result=None):
+    """Where the definition in 64 bits is NaN or infinite the result is the same;
+    elsewhere (a value reaches its own dimension alone) it is as without such
+    values."""
+    out, lse = c.run(window, sinks) if result is None else result
+    with np.errstate(invalid="ignore"):
+        want, _, _ = paged.attention(_np(c.q), _np(c.k), _np(c.v), c.cu, c.kv, c.table, c.scale, window, sinks)
+    clean = torch.nan_to_num(c.v.float(), 0.0, 0.0, 0.0)
+    finite, _, _ = paged.attention(_np(c.q), _np(c.k), _np(clean), c.cu, c.kv, c.table, c.scale, window, sinks)
+    bad = ~np.isfinite(want)
+    np.testing.assert_array_equal(_np(out)[bad], want[bad])
+    out = torch.where(torch.from_numpy(bad).cuda(), torch.from_numpy(finite).cuda(), out.double())
+    c.check(window, sinks, result=(out, lse), v=clean)
+    return bad
+
+
+def _poison(c, b, head, marks):
+    for at, dim, value in marks:
+        page, row = c.rows(b)[at]
+        c.v[page, row, head, dim] = float(value)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("new,kv", [([1, 1], [9000, 700]), ([2, 1], [300, 40]), ([150, 3], [700, 90]), ([300], [2600]),
+                                    ([60] * 30, [500] * 30)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (250, 20)])
+def test_visible_values_that_are_not_finite(new, kv, dtype, window, sinks):
+    c = Case(new, kv, 4, 2, 64, dtype, seed=71)
+    last = kv[0] - new[0]
+    _poison(c, 0, 1, [(3, 5, "nan"), (4, 6, "inf"), (5, 7, "-inf"), (6, 8, "inf"), (7, 8, "-inf"), (last, 9, "nan"),
+                      (last, 6, "inf"), (max(0, last - 200), 10, "inf"), (kv[0] - 1, 11, "nan"), (last + new[0] // 2, 12, "-inf")])
+    _poison(c, len(kv) - 1, 0, [(kv[-1] - 1, slice(None), "nan")])
+    assert _check_values(c, window, sinks).any()
+
+
+def test_infinite_values_with_the_smallest_weights():
+    """e^-40 of the largest: 0 in 16 bits, but not in the definition."""
+    c = Case([1, 140], [1000, 700], 2, 1, 64, FP16, seed=72)
+    c.q[...], c.k[...] = 1.0, 0.0
+    for b in range(2):
+        for j, (page, row) in enumerate(c.rows(b)):
+            if j == 2:
+                c.k[page, row] = -40 / 128 / c.scale
+    _poison(c, 0, 0, [(2, 3, "inf"), (2, 4, "nan")])
+    _poison(c, 1, 0, [(2, 3, "-inf"), (2, 4, "nan"), (600, 5, "inf")])
+    bad = _check_values(c)
+    assert bad[:, :, 3].all()
+
+
+def test_large_values_under_a_reference_that_stands():
+    """Weights that sum to thousands times values near the largest number."""
+    c = Case([1, 130], [3000, 700], 2, 1, 64, BF16, seed=73)
+    c.q[..., :64], c.q[..., 64:] = 1.0, 0.0
+    for b in range(2):
+        rows = torch.tensor(c.rows(b), device="cuda")
+        c.k[rows[:, 0], rows[:, 1]] = torch.where(torch.arange(c.kv[b], device="cuda") < 128, 0.0, 1.0625).to(BF16)[:, None, None]
+    c.v *= 1e36
+    c.check()
+
+
+def test_many_rows_of_a_long_cache_beside_others():
+    """A chunk over 120,000 cached tokens in which one token's values are NaN: half
+    of a tile's rows do not see it and are formed again, which takes long; nothing
+    else does without its result."""
+    n, kv, nan = 256, 120_000, 130
+    c = Case([n, 2, 1], [kv, 500, 9000], 4, 1, 256, BF16, seed=74)
+    _poison(c, 0, 0, [(kv - n + nan, slice(0, 64), "nan"), (70, 100, "inf"), (90, 101, "nan")])
+    out, lse = c.run()
+    assert kda.kda_device_status() == 0
+    at = torch.tensor(c.rows(0), device="cuda")
+    k, v = c.k[at[:, 0], at[:, 1], 0].double(), c.v[at[:, 0], at[:, 1], 0].double()
+    clean, u = torch.nan_to_num(v, 0.0, 0.0, 0.0), torch.finfo(BF16).eps / 2
+    for i in list(range(0, n, 16)) + [nan - 1, nan, n - 1]:
+        end = kv - n + i + 1
+        s = (c.q[i].double() @ k[:end].T) * c.scale
+        w = torch.softmax(s, -1)
+        want, weight = w @ clean[:end], w @ clean[:end].abs()
+        want[:, 100], want[:, 101] = float("inf"), float("nan")
+        if i >= nan:
+            want[:, :64] = float("nan")
+        fine = torch.isfinite(want)
+        assert torch.equal(torch.isnan(out[i]), torch.isnan(want)) and torch.isinf(out[i, :, 100]).all()
+        off = (out[i].double() - want).abs() - u * want.abs() - (u + 2.0 ** -12) * weight * (1 + u)
+        assert off[fine].max() <= 0
+        ref = torch.logsumexp(s, -1)
+        assert ((lse[i].double() - ref).abs() <= 2.0 ** -13 + 2.0 ** -22 * ref.abs()).all()
+    rest = slice(n, n + 3)
+    c.cu, c.kv, c.table, c.q, c.k, c.v = [0, 2, 3], c.kv[1:], c.table[1:], c.q[rest], c.k, torch.nan_to_num(c.v, 0.0, 0.0, 0.0)
+    c.check(result=(out[rest], lse[rest]))
