@@ -4,11 +4,13 @@ serving program keeps, and the calls of include/kda.h on them.
 A step of such a program is: :func:`kda_kv_extend` takes pages for its new
 tokens, each layer writes its keys and values with :func:`kda_kv_append` and
 runs :func:`kda_paged_attention`; :func:`kda_kv_truncate` hands the pages of
-rejected drafts and finished requests back.  Argument marshalling only.
+rejected drafts and finished requests back.  Argument marshalling only.  A
+call's tensors and its stream are on its handle's device, which is the current
+one; what a call makes for itself or returns is made on its stream, so that a
+workspace is zeroed there first and memory is reused in its order.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional
 
@@ -26,42 +28,57 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _stream(stream, device):
-    return _raw_stream(device) if stream is None else stream.cuda_stream
+# The current device's number, without the set-up checks around it: a handle's
+# tensors are there already.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-_CURRENT = contextlib.nullcontext()
+def _stream(stream, index):
+    """The handle of the call's stream.  The launch, the error word and the
+    workspace's size are the current device's: it has to be the handles'."""
+    if _current_device() != index:
+        raise ValueError(f"the current device must be the handles' device cuda:{index}.")
+    if stream is None:
+        return _raw_stream(index)
+    _check_stream(stream, index)
+    return stream.cuda_stream
 
 
-def _makes_on(stream):
-    """What a call makes for itself or returns is made on the stream that it runs
-    on: a workspace is zeroed there first, and memory is reused in its order."""
-    return _CURRENT if stream is None else torch.cuda.stream(stream)
+def _check_stream(stream, index):
+    if stream.device.index != index:
+        raise ValueError(f"stream must be of cuda:{index} (got {stream.device}).")
 
 
-def _int32(t, name, numel=None):
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous int32 CUDA tensor.")
+def _refuse(t, name, index, kind):
+    """The error for a tensor that is not ``kind``, or not on cuda:``index``."""
+    if t.is_cuda and t.get_device() != index:
+        return ValueError(f"{name} must be on cuda:{index} with the handles (got {t.device}).")
+    return TypeError(f"{name} must be {kind} (got {t.dtype} on {t.device}).")
+
+
+def _int32(t, name, index, numel=None):
+    if t.dtype != torch.int32 or t.get_device() != index or not t.is_contiguous():
+        raise _refuse(t, name, index, "a contiguous int32 CUDA tensor")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} must have {numel} entries (got {t.numel()}).")
     return t.data_ptr()
 
 
-def _table(t, n_req):
+def _table(t, n_req, index):
     """(pointer, row stride, columns)"""
-    if t.dtype != torch.int32 or not t.is_cuda:
-        raise TypeError("block_table must be an int32 CUDA tensor.")
+    if t.dtype != torch.int32 or t.get_device() != index:
+        raise _refuse(t, "block_table", index, "an int32 CUDA tensor")
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or shape[0] != n_req or (shape[1] > 1 and stride[1] != 1):
         raise ValueError(f"block_table must be [{n_req}, columns] with contiguous rows (got {tuple(shape)}).")
     return t.data_ptr(), stride[0], shape[1]
 
 
-def _rows(t, name, dtype, heads=None):
+def _rows(t, name, dtype, index, heads=None):
     """(tokens, heads, pointer, token stride, head stride) of [T, H, 128] in the
     cache's type; a size-1 dimension's stride is free."""
-    if t.dtype != dtype or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor of the cache's dtype {dtype} (got {t.dtype} on {t.device}).")
+    if t.dtype != dtype or t.get_device() != index:
+        raise _refuse(t, name, index, f"a CUDA tensor of the cache's dtype {dtype}")
     shape, stride = t.shape, t.stride()
     if len(shape) != 3 or shape[2] != D or stride[2] != 1 or (heads is not None and shape[1] != heads):
         want = "H" if heads is None else heads
@@ -80,12 +97,12 @@ class KvPages:
     def __init__(self, kv_lens, block_table, free_pages, free_count, page_size: int):
         n = kv_lens.numel()
         g = self._struct = _native.KdaKvPages()
-        g.kv_lens = _int32(kv_lens, "kv_lens")
-        g.block_table, g.table_stride, g.table_cols = _table(block_table, n)
-        g.free_pages, g.free_count = _int32(free_pages, "free_pages"), _int32(free_count, "free_count", 1)
+        index = self._index = max(0, kv_lens.get_device())
+        g.kv_lens = _int32(kv_lens, "kv_lens", index)
+        g.block_table, g.table_stride, g.table_cols = _table(block_table, n, index)
+        g.free_pages, g.free_count = _int32(free_pages, "free_pages", index), _int32(free_count, "free_count", index, 1)
         g.n_req, g.n_pages, g.page_size = n, free_pages.numel(), page_size
         self.n_req, self.device = n, kv_lens.device
-        self._index = kv_lens.get_device()
         self.kv_lens, self.block_table = kv_lens, block_table
         self.free_pages, self.free_count, self.page_size = free_pages, free_count, page_size
         self._ref = ctypes.byref(g)
@@ -132,18 +149,21 @@ def kda_kv_extend(pages: KvPages, new_lens, max_tokens: int, *, cu_seqlens=None,
     lengths that attention takes (0 where the request was not admitted).  What
     the call makes belongs to ``stream`` where one is given: another stream that
     uses it waits for that one, and records itself on the tensor."""
-    n = pages.n_req
-    new = _int32(new_lens, "new_lens", n)
-    with _makes_on(stream):
-        if cu_seqlens is None:
-            cu_seqlens = torch.empty(n + 1, dtype=torch.int32, device=pages.device)
-        if slot_map is None:
-            slot_map = torch.empty(max_tokens, dtype=torch.int32, device=pages.device)
-        if step_lens is None:
-            step_lens = torch.empty(n, dtype=torch.int32, device=pages.device)
+    index, n = pages._index, pages.n_req
+    if stream is not None:
+        _check_stream(stream, index)
+        with torch.cuda.stream(stream):
+            return kda_kv_extend(pages, new_lens, max_tokens, cu_seqlens=cu_seqlens, slot_map=slot_map, step_lens=step_lens)
+    handle, new = _stream(None, index), _int32(new_lens, "new_lens", index, n)
+    if cu_seqlens is None:
+        cu_seqlens = torch.empty(n + 1, dtype=torch.int32, device=pages.device)
+    if slot_map is None:
+        slot_map = torch.empty(max_tokens, dtype=torch.int32, device=pages.device)
+    if step_lens is None:
+        step_lens = torch.empty(n, dtype=torch.int32, device=pages.device)
     rc = _native.lib().kda_kv_extend(
-        pages._ref, new, _int32(cu_seqlens, "cu_seqlens", n + 1), _int32(slot_map, "slot_map", max_tokens), max_tokens,
-        _int32(step_lens, "step_lens", n), _stream(stream, pages._index))
+        pages._ref, new, _int32(cu_seqlens, "cu_seqlens", index, n + 1), _int32(slot_map, "slot_map", index, max_tokens),
+        max_tokens, _int32(step_lens, "step_lens", index, n), handle)
     if rc:
         _native.check(rc)
     return cu_seqlens, slot_map, step_lens
@@ -153,8 +173,8 @@ def kda_kv_truncate(pages: KvPages, keep_lens, *, stream=None) -> None:
     """Keep the first ``keep_lens`` [n_req] tokens of each request (int32,
     CUDA) and hand the pages past them back.  A negative table entry, a page
     that the caller has handed back itself, is passed over."""
-    rc = _native.lib().kda_kv_truncate(pages._ref, _int32(keep_lens, "keep_lens", pages.n_req),
-                                       _stream(stream, pages._index))
+    index = pages._index
+    rc = _native.lib().kda_kv_truncate(pages._ref, _int32(keep_lens, "keep_lens", index, pages.n_req), _stream(stream, index))
     if rc:
         _native.check(rc)
 
@@ -162,12 +182,13 @@ def kda_kv_truncate(pages: KvPages, keep_lens, *, stream=None) -> None:
 def kda_kv_append(cache: KvCache, k, v, slot_map, *, stream=None) -> None:
     """Write k and v [T, Hkv, 128] to the slots ``slot_map`` [T] (int32, -1
     skips the token)."""
-    t, _, kp, kt, kh = _rows(k, "k", cache.dtype, cache.n_kv_heads)
-    tv, _, vp, vt, vh = _rows(v, "v", cache.dtype, cache.n_kv_heads)
+    index = cache._index
+    t, _, kp, kt, kh = _rows(k, "k", cache.dtype, index, cache.n_kv_heads)
+    tv, _, vp, vt, vh = _rows(v, "v", cache.dtype, index, cache.n_kv_heads)
     if tv != t:
         raise ValueError("k and v must have the same number of tokens.")
-    rc = _native.lib().kda_kv_append(cache._ref, kp, kt, kh, vp, vt, vh, _int32(slot_map, "slot_map", t), t,
-                                     _stream(stream, cache._index))
+    rc = _native.lib().kda_kv_append(cache._ref, kp, kt, kh, vp, vt, vh, _int32(slot_map, "slot_map", index, t), t,
+                                     _stream(stream, index))
     if rc:
         _native.check(rc)
 
@@ -175,8 +196,10 @@ def kda_kv_append(cache: KvCache, k, v, slot_map, *, stream=None) -> None:
 def paged_attention_workspace(device=None) -> torch.Tensor:
     """A workspace for :func:`kda_paged_attention`.  One serves any sequence
     of calls on one stream; calls that overlap need their own."""
-    n = int(_native.lib().kda_paged_attention_workspace_bytes())
-    return torch.zeros(n, dtype=torch.uint8, device="cuda" if device is None else device)
+    device = "cuda" if device is None else device
+    with torch.cuda.device(device):  # the size goes by the current device
+        n = int(_native.lib().kda_paged_attention_workspace_bytes())
+    return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
 def kda_paged_attention(cache: KvCache, q, cu_seqlens, kv_lens, block_table, *, scale: Optional[float] = None,
@@ -190,27 +213,32 @@ def kda_paged_attention(cache: KvCache, q, cu_seqlens, kv_lens, block_table, *, 
     [T, Hq] or None).  ``workspace``: :func:`paged_attention_workspace`, made
     for the call when not given.  What the call makes belongs to ``stream``, as
     in :func:`kda_kv_extend`."""
-    t, hq, qp, qt, qh = _rows(q, "q", cache.dtype)
+    index = cache._index
+    if stream is not None:
+        _check_stream(stream, index)
+        with torch.cuda.stream(stream):
+            return kda_paged_attention(cache, q, cu_seqlens, kv_lens, block_table, scale=scale, window=window, sinks=sinks,
+                                       out=out, lse=lse, return_lse=return_lse, workspace=workspace)
+    handle = _stream(None, index)
+    t, hq, qp, qt, qh = _rows(q, "q", cache.dtype, index)
     n = kv_lens.numel()
-    with _makes_on(stream):
-        if out is None:
-            out = torch.empty((t, hq, D), dtype=q.dtype, device=q.device)
-        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or not out.is_cuda:
-            raise ValueError("out must be a contiguous CUDA tensor of q's shape and dtype.")
-        if lse is None:
-            lse = torch.empty((t, hq), dtype=torch.float32, device=q.device) if return_lse else None
-        elif tuple(lse.shape) != (t, hq) or lse.dtype != torch.float32 or not lse.is_contiguous() or not lse.is_cuda:
-            raise ValueError("lse must be a contiguous float32 CUDA tensor [T, Hq].")
-        if workspace is None:
-            workspace = paged_attention_workspace(q.device)
-        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or not workspace.is_cuda:
-            raise ValueError("workspace must be a contiguous uint8 CUDA tensor.")
-    table, table_stride, cols = _table(block_table, n)
+    if out is None:
+        out = torch.empty((t, hq, D), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.get_device() != index:
+        raise ValueError(f"out must be a contiguous tensor of q's shape and dtype on cuda:{index}.")
+    if lse is None:
+        lse = torch.empty((t, hq), dtype=torch.float32, device=q.device) if return_lse else None
+    elif tuple(lse.shape) != (t, hq) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.get_device() != index:
+        raise ValueError(f"lse must be a contiguous float32 tensor [T, Hq] on cuda:{index}.")
+    if workspace is None:
+        workspace = paged_attention_workspace(q.device)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != index:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{index}.")
+    table, table_stride, cols = _table(block_table, n, index)
     rc = _native.lib().kda_paged_attention(
         cache._ref, qp, qt, qh, hq, t, out.data_ptr(), None if lse is None else lse.data_ptr(),
-        _int32(cu_seqlens, "cu_seqlens", n + 1), _int32(kv_lens, "kv_lens"), table, table_stride, cols, n,
-        D ** -0.5 if scale is None else scale, window, sinks, workspace.data_ptr(), workspace.numel(),
-        _stream(stream, cache._index))
+        _int32(cu_seqlens, "cu_seqlens", index, n + 1), _int32(kv_lens, "kv_lens", index), table, table_stride, cols, n,
+        D ** -0.5 if scale is None else scale, window, sinks, workspace.data_ptr(), workspace.numel(), handle)
     if rc:
         _native.check(rc)
     return out, lse

@@ -44,12 +44,15 @@ class Library:
 class Stream:
     cuda_stream = 0x77
 
+    def __init__(self, index=0):
+        self.device = torch.device("cuda", index)
+
 
 @pytest.fixture
 def world(monkeypatch):
     """The library, and the stream that each tensor of a call was made on (None:
     the current one)."""
-    w = types.SimpleNamespace(lib=Library(), made=[], current=None)
+    w = types.SimpleNamespace(lib=Library(), made=[], current=None, device=0)
 
     @contextlib.contextmanager
     def on(stream):
@@ -64,7 +67,9 @@ def world(monkeypatch):
         return f
 
     monkeypatch.setattr(_native, "lib", lambda: w.lib)
-    monkeypatch.setattr(kv_cache, "_raw_stream", lambda device: 0x55)
+    monkeypatch.setattr(kv_cache, "_raw_stream", lambda device: w.current.cuda_stream if w.current else 0x55)
+    monkeypatch.setattr(kv_cache, "_current_device", lambda: w.device)
+    monkeypatch.setattr(torch.cuda, "device", lambda device: contextlib.nullcontext())
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(kv_cache.torch, "empty", making(torch.empty))
     monkeypatch.setattr(kv_cache.torch, "zeros", making(torch.zeros))
@@ -104,3 +109,51 @@ def test_what_a_call_makes_belongs_to_its_stream(world, stream):
     kda.kda_paged_attention(_cache(), _rows(3, 4), _i32(3), _i32(2), _i32(2, 4), out=_rows(3, 4), workspace=ws,
                             stream=stream)
     assert len(world.made) == 6
+
+
+def _calls():
+    """Each call, its tensors by name."""
+    pages, cache = _pages(), _cache()
+    return [
+        (lambda **t: kda.kda_kv_extend(pages, t.pop("new_lens"), 3, **t),
+         dict(new_lens=_i32(2), cu_seqlens=_i32(3), slot_map=_i32(3), step_lens=_i32(2))),
+        (lambda **t: kda.kda_kv_truncate(pages, t.pop("keep_lens"), **t), dict(keep_lens=_i32(2))),
+        (lambda **t: kda.kda_kv_append(cache, t.pop("k"), t.pop("v"), t.pop("slot_map"), **t),
+         dict(k=_rows(3, 2), v=_rows(3, 2), slot_map=_i32(3))),
+        (lambda **t: kda.kda_paged_attention(cache, t.pop("q"), t.pop("cu_seqlens"), t.pop("kv_lens"), t.pop("block_table"), **t),
+         dict(q=_rows(3, 4), cu_seqlens=_i32(3), kv_lens=_i32(2), block_table=_i32(2, 4), out=_rows(3, 4),
+              lse=fake(torch.ones(3, 4)), workspace=fake(torch.ones(1 << 16, dtype=torch.uint8)))),
+    ]
+
+
+def test_tensors_of_another_device_are_refused(world):
+    for call, tensors in _calls():
+        call(**tensors)
+        done = len(world.lib.calls)
+        for name, t in tensors.items():
+            with pytest.raises(ValueError, match=f"{name}.*cuda:0"):
+                call(**{**tensors, name: fake(t.as_subclass(torch.Tensor), 1)})
+        assert len(world.lib.calls) == done
+
+
+def test_handles_of_two_devices_are_refused(world):
+    good = [_i32(2), _i32(2, 4), _i32(8), _i32(1)]
+    for i in range(1, 4):
+        with pytest.raises(ValueError, match="cuda:0"):
+            kda.KvPages(*good[:i], fake(good[i].as_subclass(torch.Tensor), 1), *good[i + 1:], 16)
+    kv = torch.ones(2, 8, 16, 2, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="one device"):
+        kda.KvCache(fake(kv[0]), fake(kv[1], 1))
+
+
+def test_the_current_device_and_the_stream_are_the_handles(world):
+    for call, tensors in _calls():
+        done = len(world.lib.calls)
+        with pytest.raises(ValueError, match="stream.*cuda:0"):
+            call(**tensors, stream=Stream(1))
+        world.device = 1
+        with pytest.raises(ValueError, match="current device.*cuda:0"):
+            call(**tensors)
+        world.device = 0
+        assert len(world.lib.calls) == done
+        call(**tensors, stream=Stream(0))
