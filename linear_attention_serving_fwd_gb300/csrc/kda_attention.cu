@@ -305,11 +305,12 @@ __device__ __forceinline__ unsigned classify(const float (&v)[4]) {
   return f;
 }
 
-// What the values of keys [from, to) hold, by a warp that takes every other group
-// of them; ends early where every dimension has a NaN.
+// What the values of keys [from, to) hold (none where from >= to: rows of a narrow
+// window may share no key), by a warp that takes every other group of them; ends early where every dimension has a NaN.
 template <bool FP16>
 __device__ __forceinline__ unsigned scan_values(const AttentionParams& p, Smem& sm, const int32_t* table, int kvh, int from, int to,
                                                 int half, unsigned f) {
+  if (from >= to) return f;
   const int lane = threadIdx.x & 31, page = 1 << p.page_shift;
   const __nv_bfloat16* vc = p.vc + (int64_t)kvh * p.vc_sh + lane * 4;
 #pragma unroll 1

@@ -607,3 +607,15 @@ def test_many_rows_of_a_long_cache_beside_others():
     rest = slice(n, n + 3)
     c.cu, c.kv, c.table, c.q, c.k, c.v = [0, 2, 3], c.kv[1:], c.table[1:], c.q[rest], c.k, torch.nan_to_num(c.v, 0.0, 0.0, 0.0)
     c.check(result=(out[rest], lse[rest]))
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 4), (2, 100), (33, 0), (33, 130)])
+@pytest.mark.parametrize("new,kv,hq,hkv", [([150, 3, 4], [700, 90, 9], 6, 3), ([129, 8], [129, 500], 16, 1)])
+def test_rows_of_a_narrow_window_share_no_key(new, kv, hq, hkv, window, sinks):
+    """A value that is not finite reaches the rows whose window holds it, and none
+    beside them in their tile."""
+    c = Case(new, kv, hq, hkv, 32, BF16, seed=76)
+    for b in range(len(kv)):
+        for i in range(0, new[b], 7):
+            _poison(c, b, i % hkv, [(kv[b] - new[b] + i, slice(None) if i % 2 else 9, ("nan", "inf", "-inf")[i % 3])])
+    assert _check_values(c, window, sinks).any()
