@@ -378,8 +378,6 @@ __device__ __forceinline__ void attend_row(const AttentionParams& p, Smem& sm, i
         s[i] = p.scale * warp_sum(s[i]);
         if (g * GROUP + i >= from && g * GROUP + i < to) top = fmaxf(top, s[i]);
       }
-      // without a maximum every score is -inf (or NaN: not here, the row's sum is a number), e^s = 0
-      if (top == -CUDART_INF_F) continue;
       const float corr = m == -CUDART_INF_F ? 0.f : expf(m - top);
       m = top;
       l *= corr;
@@ -387,8 +385,9 @@ __device__ __forceinline__ void attend_row(const AttentionParams& p, Smem& sm, i
       for (int j = 0; j < 4; ++j) o[j] *= corr;
 #pragma unroll
       for (int i = 0; i < GROUP; ++i) {
-        if (g * GROUP + i < from || g * GROUP + i >= to || s[i] == -CUDART_INF_F) continue;
-        const float w = expf(s[i] - top);
+        if (g * GROUP + i < from || g * GROUP + i >= to) continue;
+        // a score of -inf has a weight of 0, whether there is a maximum yet or not
+        const float w = s[i] == -CUDART_INF_F ? 0.f : expf(s[i] - top);
         float v[4];
         load_act4<FP16>(reinterpret_cast<const __nv_bfloat16*>(&raw[i]), v);
         l += w;
@@ -397,9 +396,10 @@ __device__ __forceinline__ void attend_row(const AttentionParams& p, Smem& sm, i
       }
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = l == 0.f ? 0.f : o[j] / l;
   __nv_bfloat16* out = p.out + ((int64_t)tok * p.hq + head) * D + lane * 4;
-  *reinterpret_cast<uint2*>(out) = make_uint2(act_pack2<FP16>(o[0] * inv, o[1] * inv), act_pack2<FP16>(o[2] * inv, o[3] * inv));
+  *reinterpret_cast<uint2*>(out) = make_uint2(act_pack2<FP16>(o[0], o[1]), act_pack2<FP16>(o[2], o[3]));
   if (p.lse && lane == 0) p.lse[(int64_t)tok * p.hq + head] = l == 0.f ? -CUDART_INF_F : m + logf(l);
 }
 

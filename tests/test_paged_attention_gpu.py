@@ -609,6 +609,29 @@ def test_many_rows_of_a_long_cache_beside_others():
     c.check(result=(out[rest], lse[rest]))
 
 
+def test_infinite_values_with_no_weight():
+    """Scores of -inf: 0 times an infinite value is NaN where the row sees another
+    key, before the first maximum and after it; a row that has only such scores
+    is 0."""
+    c = Case([4, 140], [40, 400], 2, 1, 64, BF16, seed=75)
+    c.q[..., 0] = 1.0
+    for b, at in ((0, list(range(36))), (1, [0, 1, 300])):
+        for j in at:
+            page, row = c.rows(b)[j]
+            c.k[page, row, 0, 0] = -float("inf")
+    _poison(c, 0, 0, [(3, 5, "inf"), (38, 6, "nan")])
+    _poison(c, 1, 0, [(0, 7, "inf"), (300, 8, "-inf"), (300, 9, "nan"), (200, 10, "inf")])
+    c.q[0, 1] = 0.0  # 0 times inf: this row's scores are NaN
+    out, lse = c.run()
+    assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1])
+    c.q[0, 1, 0] = 1.0
+    bad = _check_values(c)
+    assert bad[:4, :, 5].all() and not bad[:, :, 0].any()
+    c.kv[0] = 36  # request 0 sees scores of -inf alone
+    out, lse = c.run()
+    assert not out[:4].any() and torch.isneginf(lse[:4]).all()
+
+
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 4), (2, 100), (33, 0), (33, 130)])
 @pytest.mark.parametrize("new,kv,hq,hkv", [([150, 3, 4], [700, 90, 9], 6, 3), ([129, 8], [129, 500], 16, 1)])
 def test_rows_of_a_narrow_window_share_no_key(new, kv, hq, hkv, window, sinks):
