@@ -966,25 +966,25 @@ __device__ __forceinline__ void join_rows(const Params& p, Smem& sm, int s, cons
       float4 z[PIECES];
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) z[i] = __ldcg(p.part_o + part_piece(at, c) + i * 32);  // 4 pieces on
-      // a part that has seen nothing stored nothing
-      const bool some = ml.x != -CUDART_INF_F;
+      // a part that has seen nothing has a weight of 0 (and zeros, unless the
+      // values of keys without weight were not finite: the row is then looked at again)
       const float reach = fmaxf(top, ml.x);
-      const float corr = top == reach ? 1.f : ex2(top - reach), w = some ? ex2(ml.x - reach) : 0.f;
-      l = l * corr + (some ? w * ml.y : 0.f);
+      const float corr = top == reach ? 1.f : ex2(top - reach), w = ml.x == -CUDART_INF_F ? 0.f : ex2(ml.x - reach);
+      l = l * corr + w * ml.y;
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
         const float v[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[4 * i + j] = o[4 * i + j] * corr + (some ? w * v[j] : 0.f);
+        for (int j = 0; j < 4; ++j) o[4 * i + j] = o[4 * i + j] * corr + w * v[j];
       }
       top = reach;
     }
     if (!real) continue;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = 1.f / l;
     float poison = 0.f;
 #pragma unroll
     for (int j = 0; j < 4 * PIECES; ++j) {
-      o[j] *= inv;
+      o[j] = l == 0.f ? 0.f : o[j] * inv;
       poison += o[j] * 0.f;  // NaN from then on when one is not finite
     }
     if (poison != 0.f && l == l) atomicOr(&sm.poisoned[s][0][row >> 5], 1u << (row & 31));
@@ -1306,6 +1306,14 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
       }
     }
     if (whole_pair) {
+      if (valid && l == 0.f && poison != 0.f) {
+        // 0 where the sum is 0, whatever the values were
+        __nv_bfloat16* out = p.a.out + ((int64_t)tok * p.a.hq + head) * D + half * 64;
+        const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) store32(out + c * 16, zero);
+        poison = 0.f;
+      }
       if (half == 0 && valid && p.a.lse)
         p.a.lse[(int64_t)tok * p.a.hq + head] = l == 0.f ? -CUDART_INF_F : (m2 + log2f(l) - WEIGHT_EXP<FP16>) * LN2;
       const unsigned mine = __ballot_sync(0xffffffffu, valid && poison != 0.f && l == l);

@@ -642,3 +642,20 @@ def test_rows_of_a_narrow_window_share_no_key(new, kv, hq, hkv, window, sinks):
         for i in range(0, new[b], 7):
             _poison(c, b, i % hkv, [(kv[b] - new[b] + i, slice(None) if i % 2 else 9, ("nan", "inf", "-inf")[i % 3])])
     assert _check_values(c, window, sinks).any()
+
+
+@pytest.mark.parametrize("new,kv", [([3], [60]), ([2], [9000]), ([140, 1], [1500, 300])])
+@pytest.mark.parametrize("value", ["nan", "inf"])
+def test_rows_whose_scores_are_all_minus_infinity(new, kv, value):
+    """Their sum is 0: out 0 and lse -inf, whatever the values that they see, and
+    wherever their block is divided.  With one key more the values count."""
+    c = Case(new, kv, 2, 1, 64, BF16, seed=77)
+    c.q[..., 0] = 1.0
+    rows = torch.tensor(c.rows(0), device="cuda")
+    c.k[rows[:, 0], rows[:, 1], 0, 0] = -float("inf")
+    _poison(c, 0, 0, [(1, slice(0, 40), value), (kv[0] // 2, 50, value), (kv[0] - new[0], 60, value)])
+    out, lse = c.run()
+    assert not out[:new[0]].any() and torch.isneginf(lse[:new[0]]).all()
+    page, row = c.rows(0)[kv[0] - new[0] - 1]
+    c.k[page, row, 0, 0] = 0.0
+    _check_values(c)
