@@ -574,9 +574,10 @@ int kda_kv_append(const kda_kv_cache* cache, const void* k, int64_t k_stride_tok
  * keys).  With s_j = scale <q, k_j> over the visible j:
  *   out = sum_j e^{s_j} v_j / sum_j e^{s_j},   lse = ln sum_j e^{s_j}
  * and out = 0, lse = -inf where that sum is 0: a token that sees nothing
- * (p < 0 among them).
+ * (p < 0 among them), or scores of -inf alone.
  * What is hidden has no influence, whatever it holds (NaN and infinities
- * included).  One call serves single tokens, short windows and prompt chunks
+ * included); what is seen counts as the formula has it, wherever the work is
+ * divided.  One call serves single tokens, short windows and prompt chunks
  * in any mix.
  *   q           [t_total, Hq, 128], 16-byte aligned, token and head strides
  *               multiples of 8 elements and >= 128

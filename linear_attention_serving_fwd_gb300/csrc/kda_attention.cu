@@ -39,11 +39,17 @@
 //
 // Bounds.  Prompt chunks are bound by the chain scores - weights - product of
 // two streams on one set of tensor cores: 8192 tokens over 24576 cached, 32
-// heads, take 2.77 to 2.86 ms (1390 to 1344 TFLOP/s, the chip's power limit in
-// force); 4096 over 4096 in a short run 1470 TFLOP/s, tensor cores 65 % busy.
-// Single tokens are bound by memory: 256 requests over 4.2 GB of keys and values
-// take 608 to 623 us (6.9 to 6.8 TB/s).  A single request of 4096 tokens is a
-// chain of latencies, 14.5 us.
+// heads, take 2.77 to 2.96 ms by the chip (1390 to 1300 TFLOP/s, its power limit
+// in force); 4096 over 4096 in a short run 1470 to 1515 TFLOP/s, tensor cores
+// 64 % busy.  Single tokens are bound by memory: 256 requests over 4.2 GB of keys
+// and values take 608 to 626 us (6.9 to 6.75 TB/s).  A single request of 4096
+// tokens is a chain of latencies, 14.2 us.
+//
+// Fewer bits.  The weights are rounded to the values' 16-bit type, which the
+// tensor cores ask of both operands: 32-bit weights in two 16-bit parts would
+// double the second product.  It takes the outputs' error against 64 bits from
+// 1.7e-3 (their own rounding) to 1.8e-3 of their norm in bf16, from 2.1e-4 to
+// 2.2e-4 in fp16.  Sums take the weights before they are rounded.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math_constants.h>

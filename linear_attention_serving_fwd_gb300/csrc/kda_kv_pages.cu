@@ -5,10 +5,10 @@
 // writes found by a search in them.  A few hundred bytes to a few hundred
 // kilobytes move, so the time is latency: launch, length loads, the block's
 // sums, the search, a table or free-list load.  Measured on the device, extend
-// and truncate together: 6.9 us for one token each of 16 requests, 7.8 for 256,
-// 14.5 for four each of 2048 (two rounds of 1024), 18.4 for 98,000 tokens of 48.
-// append moves 256 bytes per token and head of keys and of values: 2.4 us for
-// 256 tokens of 8 heads, 41.6 us for 32768 (268 MB, 6.5 TB/s, a copy's rate).
+// and truncate together: 6.8 us for one token each of 16 requests, 8.3 for 256,
+// 17.8 for four each of 2048 (two rounds of 1024), 17.1 for 98,000 tokens of 48.
+// append moves 256 bytes per token and head of keys and of values: 1.8 us for
+// 256 tokens of 8 heads, 40.9 us for 32768 (268 MB, 6.6 TB/s, a copy's rate).
 #include "kda_kv.cuh"
 
 namespace kda {
@@ -16,9 +16,9 @@ namespace {
 
 constexpr int PT = 1024;  // threads: one request each per round
 // One CTA writes up to EXTEND_ONE slots, a thread each, a cluster of EXTEND_CTAS
-// more (extend and truncate together, one CTA against eight): 16 slots 6.9 us
-// against 7.2, 256 slots 7.8 against 8.1, 4096 slots 11.4 against 8.9, 98,000
-// slots 70 against 18.4.
+// more (extend and truncate together, one CTA against eight): 16 slots 6.8 us
+// against 7.0, 1000 slots 9.4 against 9.8, 1200 slots 10.8 against 10.2, 4096
+// slots 12.9 against 10.3, 98,000 slots 60 against 17.1.
 constexpr int EXTEND_CTAS = 8, EXTEND_ONE = PT;
 
 // Inclusive sums of two values over the block, and both totals.
