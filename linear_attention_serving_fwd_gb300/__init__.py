@@ -19,6 +19,7 @@ every step of the computation runs in the library's CUDA kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -48,6 +49,20 @@ def _stream_handle(stream=None):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _on_its_stream(call):
+    """``call`` with its ``stream`` current: what it makes for itself or returns
+    is zeroed, converted and reused in that stream's order."""
+    @functools.wraps(call)
+    def on(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream)
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return on
 
 
 def _as_tokens(x: torch.Tensor, name: str, heads_dim: bool = True) -> torch.Tensor:
@@ -175,6 +190,7 @@ def chunk_workspace_bytes(n_seqs: int, t_total: int, hv: int, groups: int = 0) -
     return int(_native.lib().kda_chunk_workspace_bytes(n_seqs, t_total, hv, groups))
 
 
+@_on_its_stream
 def kda_chunk_fwd(q, k, v, g, beta, *, A_log=None, dt_bias=None, scale=None, lower_bound=-5.0,
                   cu_seqlens=None, n_seqs=None, initial_state=None, output_final_state=False,
                   final_state=None, out=None, state_cache=None, state_indices=None,
@@ -286,6 +302,7 @@ def kda_chunk_fwd(q, k, v, g, beta, *, A_log=None, dt_bias=None, scale=None, low
     return out, final_state
 
 
+@_on_its_stream
 def kda_chunk_fwd_host(q, k, v, g, beta, *, A_log=None, dt_bias=None, scale=None, lower_bound=-5.0,
                        cu_seqlens=None, n_seqs=None, initial_state=None, output_final_state=False,
                        final_state=None, out=None, segment_tokens: int = 0, groups: int = 0,
@@ -368,6 +385,7 @@ def chunk_fwd_host_workspace_bytes(q, k, v, g, beta, *, A_log=None, dt_bias=None
     return need
 
 
+@_on_its_stream
 def kda_chunk_fwd_noalloc(q, k, v, g, beta, *, out, A_log=None, dt_bias=None, scale=None,
                           lower_bound=-5.0, cu_seqlens=None, n_seqs=None, initial_state=None,
                           final_state=None, state_cache=None, state_indices=None,
@@ -459,6 +477,7 @@ def _window_call(verify, q, k, v, g, beta, state_pool, query_start, slots, windo
     return out, corr, kg
 
 
+@_on_its_stream
 def kda_decode(q, k, v, g, beta, state_pool, query_start, slots, window, *, A_log=None,
                dt_bias=None, scale=None, lower_bound=-5.0, out=None, stream=None):
     """In-place decode: request b runs tokens query_start[b]..query_start[b+1]-1
@@ -468,6 +487,7 @@ def kda_decode(q, k, v, g, beta, state_pool, query_start, slots, window, *, A_lo
                         out=out, corr=None, kg=None, work_counter=None, stream=stream)[0]
 
 
+@_on_its_stream
 def kda_decode_steps(q, k, v, g, beta, state_pool, query_start, state_indices, window, *,
                      num_accepted_tokens=None, A_log=None, dt_bias=None, scale=None,
                      lower_bound=-5.0, out=None, stream=None):
@@ -484,6 +504,7 @@ def kda_decode_steps(q, k, v, g, beta, state_pool, query_start, state_indices, w
                         num_accepted_tokens=num_accepted_tokens)[0]
 
 
+@_on_its_stream
 def kda_verify(q, k, v, g, beta, state_pool, query_start, slots, window, *, A_log=None,
                dt_bias=None, scale=None, lower_bound=-5.0, out=None, corr=None, kg=None,
                work_counter=None, stream=None, conv_weight=None, conv_state=None,
@@ -502,6 +523,7 @@ def kda_verify(q, k, v, g, beta, state_pool, query_start, slots, window, *, A_lo
                         conv_state=conv_state, conv_dim_first=conv_dim_first)
 
 
+@_on_its_stream
 def kda_commit(state_pool, slots, num_accepted, corr, kg, window, *, A_log=None, dt_bias=None,
                lower_bound=-5.0, stream=None):
     """Speculative-decode commit: rebuild pool rows slots[b] in place as the
