@@ -39,9 +39,9 @@
 //
 // Bounds.  Prompt chunks are bound by the chain scores - weights - product of
 // two streams on one set of tensor cores: 8192 tokens over 24576 cached, 32
-// heads, take 2.77 to 2.96 ms by the chip (1390 to 1300 TFLOP/s, its power limit
-// in force); 4096 over 4096 in a short run 1470 to 1515 TFLOP/s, tensor cores
-// 64 % busy.  Single tokens are bound by memory: 256 requests over 4.2 GB of keys
+// heads, take 2.77 to 2.97 ms by the chip (1390 to 1295 TFLOP/s) at its power
+// limit and 2.5 ms before it; 4096 over 4096 in a short run 1470 to 1515 TFLOP/s,
+// tensor cores 64 % busy.  Single tokens are bound by memory: 256 requests over 4.2 GB of keys
 // and values take 608 to 626 us (6.9 to 6.75 TB/s).  A single request of 4096
 // tokens is a chain of latencies, 14.2 us.
 //
