@@ -117,7 +117,7 @@ struct Smem {
   int beat;    // changes while rows are formed again, which may take longer than a wait
   int joined;  // results of two streams joined so far
   int last[2];
-  unsigned poisoned[2][2][4];  // rows of a tile with a sum, and a result that is not finite, by stream and half
+  unsigned poisoned[2][2][4];  // rows whose sum is a number but not their result, by stream and half
   float share[2][2][ROWS];     // what the halves of a row tell each other
 };
 
