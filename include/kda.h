@@ -60,7 +60,8 @@ typedef enum kda_status {
   KDA_ERR_DEVICE_INDEX = 5,      /* a kernel met a bad slot / length */
   KDA_ERR_DEVICE_RANGE = 6       /* a prefill without gate parameters met a raw
                                     log decay outside [-10.5, 0]: its outputs
-                                    and states are not valid */
+                                    and states are not valid; or attention
+                                    over an 8-bit cache a scale out of range */
 } kda_status;
 
 enum { KDA_DTYPE_BF16 = 0, KDA_DTYPE_FP16 = 1 };
@@ -608,6 +609,111 @@ int kda_paged_attention(const kda_kv_cache* cache, const void* q, int64_t q_stri
                         int64_t table_stride, int32_t table_cols, int32_t n_req, float scale,
                         int32_t window, int32_t sinks, void* workspace, size_t workspace_bytes,
                         void* stream);
+
+/*
+ * kda_kv_quant_cache - the pages' storage in 8 bits: element (page, row, head,
+ * c) of k at k + page * k_stride_page + row * k_stride_tok + head *
+ * k_stride_head + c (elements of one byte; 16-byte aligned, strides positive
+ * multiples of 16), an e4m3 number: 4 significant bits, at most 448, nothing
+ * between multiples of 2^-9.  It stands for itself times the scale of its
+ * block, KDA_KV_BLOCK rows of a page and one head, at
+ * k_scale[(page * hkv + head) * (page_size / KDA_KV_BLOCK) + row / KDA_KV_BLOCK]
+ * (fp32, contiguous); v likewise.  A scale is positive and within
+ * [2^-48, 2^48]; kda_kv_append_quant writes powers of two, other numbers (a
+ * cache filled elsewhere) are taken as they are.  kda_kv_extend and
+ * kda_kv_truncate serve such a cache as they serve kda_kv_cache.
+ */
+#define KDA_KV_BLOCK 16
+typedef struct kda_kv_quant_cache {
+  void* k; int64_t k_stride_page, k_stride_tok, k_stride_head; float* k_scale;
+  void* v; int64_t v_stride_page, v_stride_tok, v_stride_head; float* v_scale;
+  int32_t dtype;   /* KDA_DTYPE_BF16 or KDA_DTYPE_FP16: q, k, v and out */
+  int32_t n_pages, page_size, hkv;
+} kda_kv_quant_cache;
+
+/*
+ * kda_kv_append_quant - write k and v [t_total, Hkv, 128] (as in kda_kv_append)
+ * to the slots slot_map[t] in 8 bits.  The tokens of one block stand side by
+ * side with ascending slots, as kda_kv_extend lays them out; the rows of the
+ * block before the first of them hold its earlier tokens, those after the last
+ * hold nothing.  Per block and head, with m the largest finite magnitude of
+ * the new tokens and e the least in [-48, 48] with m <= 448 2^e:
+ *   the block's scale is 2^e, or what it was before, where that is larger and
+ *   there are earlier tokens (a truncated block keeps the scale that it grew to);
+ *   x becomes x times the scale's reciprocal, rounded to the nearest, ties to even; what lies past
+ *   448 (infinities too) becomes 448, NaN stays NaN;
+ *   where the scale has grown, the earlier tokens are rounded to it once more
+ *   (powers of two: without loss, but for numbers of less than 2^-6 scales).
+ * A negative slot skips the token; a slot past the cache sets
+ * KDA_ERR_DEVICE_INDEX and skips it; one in its predecessor's
+ * block that does not follow it does so too, for itself and the rest of the
+ * block.  Tokens of a block that stand apart race.
+ */
+int kda_kv_append_quant(const kda_kv_quant_cache* cache, const void* k, int64_t k_stride_tok, int64_t k_stride_head,
+                        const void* v, int64_t v_stride_tok, int64_t v_stride_head, const int32_t* slot_map,
+                        int32_t t_total, void* stream);
+
+/*
+ * kda_kv_read, kda_kv_read_quant - the keys and values at the slots
+ * slot_map[t], k and v [t_total, Hkv, 128] contiguous in the cache's 16-bit
+ * type, 16-byte aligned, written: a request that moves to another pool, a
+ * prefix that is kept elsewhere.  In 8 bits: number times scale, rounded once
+ * (exact for powers of two, unless fp16 ends before).  A negative slot gives
+ * zeros; so does a slot past the cache, which sets KDA_ERR_DEVICE_INDEX.
+ */
+int kda_kv_read(const kda_kv_cache* cache, const int32_t* slot_map, int32_t t_total, void* k, void* v, void* stream);
+int kda_kv_read_quant(const kda_kv_quant_cache* cache, const int32_t* slot_map, int32_t t_total, void* k, void* v,
+                      void* stream);
+
+/*
+ * kda_paged_attention_quant - kda_paged_attention over the 8-bit cache: k_j and
+ * v_j are the numbers that the cache stands for; the other arguments, the rules
+ * and the results are those of kda_paged_attention.  A query row with an
+ * infinity or a NaN counts as NaN.  A visible scale outside [2^-48, 2^48] (or
+ * NaN) sets KDA_ERR_DEVICE_RANGE and counts as the nearest number inside (1).
+ *   workspace   16-byte aligned, kda_paged_attention_quant_workspace_bytes(t_total,
+ *               hq) bytes or more, else as kda_paged_attention's: one workspace
+ *               serves both
+ */
+size_t kda_paged_attention_quant_workspace_bytes(int32_t t_total, int32_t hq);
+int kda_paged_attention_quant(const kda_kv_quant_cache* cache, const void* q, int64_t q_stride_tok,
+                              int64_t q_stride_head, int32_t hq, int32_t t_total, void* out, float* lse,
+                              const int32_t* cu_seqlens, const int32_t* kv_lens, const int32_t* block_table,
+                              int64_t table_stride, int32_t table_cols, int32_t n_req, float scale,
+                              int32_t window, int32_t sinks, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
+ * kda_rope - rotary positions of a step's queries and keys, before they are
+ * written and attended to.  In a row of 128, ``pairs`` pairs are turned,
+ * (x_i, x_{i + pairs}) or with ``interleaved`` (x_2i, x_{2i+1}): by the angle
+ * a = 2 pi p turns[i] / 2^64 of position p,
+ *   x' = amplitude (x cos a - y sin a),  y' = amplitude (y cos a + x sin a),
+ * and dimensions from 2 pairs on stay.  A turn's fraction in 64 bits makes p
+ * turns[i] exact for every 32-bit p.  Formed in fp32, rounded once.
+ *   turns       device uint64 [pairs]: radians a position / 2 pi, times 2^64
+ *   pairs       1 .. 64
+ *   q, q_out    [t_total, hq, 128], and k, k_out [t_total, hk, 128] (hq or hk
+ *               may be 0): 16-byte aligned, token and head strides multiples of
+ *               8 elements, rows that do not overlap; an output that is its
+ *               input, strides and all, is turned in place, else they do not
+ *               overlap
+ *   positions   device int32 [t_total], or NULL: then token i of the n packed
+ *               tokens of request b stands at kv_lens[b] - n + i, as in
+ *               kda_paged_attention, and tokens of no request are left alone
+ *   cu_seqlens  device int32 [n_req + 1], kv_lens device int32 [n_req]; used
+ *               without positions
+ */
+typedef struct kda_rotation {
+  const uint64_t* turns;
+  int32_t pairs, interleaved; /* interleaved: 0 or 1 */
+  float amplitude;            /* finite; 1 usual */
+} kda_rotation;
+int kda_rope(const kda_rotation* rotation, int32_t dtype, const void* q, int64_t q_stride_tok, int64_t q_stride_head,
+             int32_t hq, void* q_out, int64_t q_out_stride_tok, int64_t q_out_stride_head, const void* k,
+             int64_t k_stride_tok, int64_t k_stride_head, int32_t hk, void* k_out, int64_t k_out_stride_tok,
+             int64_t k_out_stride_head, int32_t t_total, const int32_t* positions, const int32_t* cu_seqlens,
+             const int32_t* kv_lens, int32_t n_req, void* stream);
 
 /* Thread-local text of the last error returned on this thread ("" if none).
  * kda_last_error_message is the same function under the name the serving

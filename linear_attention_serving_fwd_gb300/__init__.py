@@ -12,8 +12,11 @@ every step of the computation runs in the library's CUDA kernels.
 * :func:`kda_verify` - speculative verify (state read only, correction
   records).
 * :func:`kda_kv_extend`, :func:`kda_kv_truncate`, :func:`kda_kv_append`,
-  :func:`kda_paged_attention` on :class:`KvPages` / :class:`KvCache` - the paged
-  key/value cache of softmax-attention layers beside the recurrent ones.
+  :func:`kda_kv_read`, :func:`kda_paged_attention` on :class:`KvPages` /
+  :class:`KvCache` - the paged key/value cache, in 16 or 8 bits, of
+  softmax-attention layers beside the recurrent ones.
+* :func:`kda_rope` on a :class:`Rope` - rotary positions of their queries and
+  keys.
 * :func:`kda_device_status` - read (and clear) the device error word.
 """
 from __future__ import annotations
@@ -26,15 +29,16 @@ import torch
 
 from . import _native
 from ._native import KdaError
-from .kv_cache import (KvCache, KvPages, kda_kv_append, kda_kv_extend, kda_kv_truncate, kda_paged_attention,
-                       paged_attention_workspace)
+from .kv_cache import (KvCache, KvPages, kda_kv_append, kda_kv_extend, kda_kv_read, kda_kv_truncate,
+                       kda_paged_attention, paged_attention_workspace)
+from .rope import Rope, kda_rope, rope_frequencies
 
 D = 128
 __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_noalloc", "kda_chunk_fwd_host", "kda_decode", "kda_decode_steps",
            "kda_verify", "kda_commit", "kda_device_status", "chunk_workspace_bytes",
            "chunk_fwd_host_workspace_bytes", "conv_scratch_bytes", "KdaError", "library_path",
            "KvPages", "KvCache", "kda_kv_extend", "kda_kv_truncate", "kda_kv_append", "kda_paged_attention",
-           "paged_attention_workspace"]
+           "paged_attention_workspace", "kda_kv_read", "Rope", "kda_rope", "rope_frequencies"]
 
 
 def library_path() -> str:

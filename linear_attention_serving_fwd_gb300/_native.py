@@ -32,7 +32,8 @@ EXPORTS = ("kda_chunk_workspace_bytes", "kda_chunk_fwd", "kda_decode", "kda_veri
            "kda_decode_steps", "kda_verify_ex", "kda_commit_ex", "kda_chunk_fwd_host",
            "kda_chunk_fwd_host_workspace_bytes", "kda_conv_scratch_bytes", "kda_selftest_wait_timeout",
            "kda_kv_extend", "kda_kv_truncate", "kda_kv_append", "kda_paged_attention",
-           "kda_paged_attention_workspace_bytes")
+           "kda_paged_attention_workspace_bytes", "kda_kv_append_quant", "kda_kv_read", "kda_kv_read_quant",
+           "kda_paged_attention_quant", "kda_paged_attention_quant_workspace_bytes", "kda_rope")
 
 
 class KdaActivations(ctypes.Structure):
@@ -85,6 +86,24 @@ class KdaKvCache(ctypes.Structure):
     ]
 
 
+class KdaKvQuantCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("k_stride_page", ctypes.c_int64), ("k_stride_tok", ctypes.c_int64),
+        ("k_stride_head", ctypes.c_int64), ("k_scale", ctypes.c_void_p),
+        ("v", ctypes.c_void_p), ("v_stride_page", ctypes.c_int64), ("v_stride_tok", ctypes.c_int64),
+        ("v_stride_head", ctypes.c_int64), ("v_scale", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("hkv", ctypes.c_int32),
+    ]
+
+
+class KdaRotation(ctypes.Structure):
+    _fields_ = [
+        ("turns", ctypes.c_void_p), ("pairs", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+        ("amplitude", ctypes.c_float),
+    ]
+
+
 class KdaError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"[kda status {code}] {msg}")
@@ -134,6 +153,20 @@ def _declare(lib):
     lib.kda_paged_attention.argtypes = [KC, P, I64, I64, I32, I32, P, P, P, P, P, I64, I32, I32,
                                         ctypes.c_float, I32, I32, P, SZ, P]
     lib.kda_paged_attention.restype = ctypes.c_int
+    KQ, KR = ctypes.POINTER(KdaKvQuantCache), ctypes.POINTER(KdaRotation)
+    lib.kda_kv_append_quant.argtypes = [KQ, P, I64, I64, P, I64, I64, P, I32, P]
+    lib.kda_kv_append_quant.restype = ctypes.c_int
+    lib.kda_kv_read.argtypes = [KC, P, I32, P, P, P]
+    lib.kda_kv_read.restype = ctypes.c_int
+    lib.kda_kv_read_quant.argtypes = [KQ, P, I32, P, P, P]
+    lib.kda_kv_read_quant.restype = ctypes.c_int
+    lib.kda_paged_attention_quant_workspace_bytes.argtypes = [I32, I32]
+    lib.kda_paged_attention_quant_workspace_bytes.restype = SZ
+    lib.kda_paged_attention_quant.argtypes = [KQ, P, I64, I64, I32, I32, P, P, P, P, P, I64, I32, I32,
+                                              ctypes.c_float, I32, I32, P, SZ, P]
+    lib.kda_paged_attention_quant.restype = ctypes.c_int
+    lib.kda_rope.argtypes = [KR, I32, P, I64, I64, I32, P, I64, I64, P, I64, I64, I32, P, I64, I64, I32, P, P, P, I32, P]
+    lib.kda_rope.restype = ctypes.c_int
     lib.kda_last_error.argtypes = []
     lib.kda_last_error.restype = ctypes.c_char_p
     lib.kda_last_error_message.argtypes = []

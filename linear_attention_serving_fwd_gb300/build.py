@@ -22,7 +22,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libkda.so")
 VARIANTS = {None: [], "phase_timing": ["-DKDA_PHASE_TIMING"]}
 SOURCES = ["kda_api.cu", "kda_window.cu", "kda_chunk.cu", "kda_noalloc.cu", "kda_commit.cu", "kda_conv.cu",
-           "kda_kv_api.cu", "kda_kv_pages.cu", "kda_attention.cu"]
+           "kda_kv_api.cu", "kda_kv_pages.cu", "kda_attention.cu",
+           "kda_kv_quant.cu", "kda_rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-diag-suppress", "550"]

@@ -945,7 +945,8 @@ int kda_device_status(void* stream, int32_t clear) {
     return fail(KDA_ERR_DEVICE_INDEX, "a kernel met an out-of-range slot or sequence length.");
   if (word & kda::ERR_RANGE)
     return fail(KDA_ERR_DEVICE_RANGE,
-                "a prefill without gate parameters met a raw log decay outside [-10.5, 0].");
+                "a prefill without gate parameters met a raw log decay outside [-10.5, 0], or attention a scale of an "
+                "8-bit cache outside [2^-48, 2^48].");
   return ok();
 }
 

@@ -4,7 +4,9 @@ serving program keeps, and the calls of include/kda.h on them.
 A step of such a program is: :func:`kda_kv_extend` takes pages for its new
 tokens, each layer writes its keys and values with :func:`kda_kv_append` and
 runs :func:`kda_paged_attention`; :func:`kda_kv_truncate` hands the pages of
-rejected drafts and finished requests back.  Argument marshalling only.  A
+rejected drafts and finished requests back; :func:`kda_kv_read` reads cached
+tokens back.  A :class:`KvCache` holds them in 16 or in 8 bits, and the calls
+go by what it holds.  Argument marshalling only.  A
 call's tensors and its stream are on its handle's device, which is the current
 one; what a call makes for itself or returns is made on its stream, so that a
 workspace is zeroed there first and memory is reused in its order.
@@ -19,6 +21,7 @@ import torch
 from . import _native
 
 D = 128
+BLOCK = 16  # rows of a page that share a scale in an 8-bit cache
 _DTYPES = {torch.bfloat16: _native.KDA_DTYPE_BF16, torch.float16: _native.KDA_DTYPE_FP16}
 
 
@@ -116,28 +119,56 @@ class KvPages:
 
 class KvCache:
     """The pages' storage: ``k`` and ``v`` as [n_pages, page_size, Hkv, 128]
-    CUDA tensors of any strides that are multiples of 8 elements with a
+    CUDA tensors of any strides that are multiples of 16 bytes with a
     contiguous last dimension (a permuted view of head-major pages, halves of
-    one tensor), bf16 or fp16."""
+    one tensor), bf16 or fp16; or in 8 bits, torch.float8_e4m3fn, with
+    ``k_scale`` and ``v_scale``, contiguous fp32 [n_pages, Hkv, page_size / 16],
+    one for each block of 16 tokens and head, and ``dtype``, the 16-bit type
+    of what is written, read and attended with.  :meth:`empty` makes one."""
 
-    def __init__(self, k, v):
-        if k.dtype not in _DTYPES or v.dtype != k.dtype:
-            raise TypeError("the cache must be torch.bfloat16 or torch.float16, k and v alike.")
+    def __init__(self, k, v, k_scale=None, v_scale=None, *, dtype=None):
+        quant = k.dtype == torch.float8_e4m3fn
+        if (not quant and k.dtype not in _DTYPES) or v.dtype != k.dtype:
+            raise TypeError("the cache must be torch.bfloat16 or torch.float16, or torch.float8_e4m3fn, k and v alike.")
         if k.dim() != 4 or k.shape != v.shape or k.shape[3] != D or k.stride(3) != 1 or v.stride(3) != 1:
             raise ValueError("k and v must be [n_pages, page_size, Hkv, 128] alike with a contiguous last dimension.")
         if not k.is_cuda or v.device != k.device:
             raise ValueError("k and v must be CUDA tensors on one device.")
-        c = self._struct = _native.KdaKvCache()
+        c = self._struct = _native.KdaKvQuantCache() if quant else _native.KdaKvCache()
         for name, t in (("k", k), ("v", v)):
             setattr(c, name, t.data_ptr())
             for dim, what in ((0, "page"), (1, "tok"), (2, "head")):
                 # the stride of a dimension of size 1 is never used
                 setattr(c, f"{name}_stride_{what}", t.stride(dim) if t.shape[dim] > 1 else D)
-        c.dtype = _DTYPES[k.dtype]
+        if quant:
+            if dtype not in _DTYPES:
+                raise TypeError("an 8-bit cache needs dtype, torch.bfloat16 or torch.float16.")
+            scales = (k.shape[0], k.shape[2], k.shape[1] // BLOCK)
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if t is None or t.dtype != torch.float32 or tuple(t.shape) != scales or not t.is_contiguous() or t.device != k.device:
+                    raise ValueError(f"{name} must be a contiguous float32 tensor {list(scales)} on {k.device}.")
+                setattr(c, name, t.data_ptr())
+        elif k_scale is not None or v_scale is not None or dtype not in (None, k.dtype):
+            raise ValueError("a 16-bit cache has no scales, and its own dtype.")
+        self.dtype = dtype if quant else k.dtype
+        c.dtype = _DTYPES[self.dtype]
         c.n_pages, c.page_size, c.hkv = k.shape[:3]
-        self.k, self.v, self.dtype, self.n_kv_heads = k, v, k.dtype, k.shape[2]
+        self.k, self.v, self.k_scale, self.v_scale, self.quantized = k, v, k_scale, v_scale, quant
+        self.n_kv_heads = k.shape[2]
         self._index = k.get_device()
         self._ref = ctypes.byref(c)
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, n_kv_heads: int, *, dtype=torch.bfloat16, quantized: bool = False,
+              device="cuda") -> "KvCache":
+        """Token-major pages, zeroed; ``quantized``: in 8 bits."""
+        shape = (2, n_pages, page_size, n_kv_heads, D)
+        if not quantized:
+            return cls(*torch.zeros(shape, dtype=dtype, device=device))
+        # float8 has no zeros everywhere: from bytes
+        kv = torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+        scales = torch.ones((2, n_pages, n_kv_heads, page_size // BLOCK), dtype=torch.float32, device=device)
+        return cls(kv[0], kv[1], scales[0], scales[1], dtype=dtype)
 
 
 def kda_kv_extend(pages: KvPages, new_lens, max_tokens: int, *, cu_seqlens=None, slot_map=None, step_lens=None,
@@ -181,24 +212,57 @@ def kda_kv_truncate(pages: KvPages, keep_lens, *, stream=None) -> None:
 
 def kda_kv_append(cache: KvCache, k, v, slot_map, *, stream=None) -> None:
     """Write k and v [T, Hkv, 128] to the slots ``slot_map`` [T] (int32, -1
-    skips the token)."""
+    skips the token).  In an 8-bit cache the scales of the tokens' blocks are
+    set or grown; the tokens of one block stand side by side, as
+    :func:`kda_kv_extend` lays them out."""
     index = cache._index
     t, _, kp, kt, kh = _rows(k, "k", cache.dtype, index, cache.n_kv_heads)
     tv, _, vp, vt, vh = _rows(v, "v", cache.dtype, index, cache.n_kv_heads)
     if tv != t:
         raise ValueError("k and v must have the same number of tokens.")
-    rc = _native.lib().kda_kv_append(cache._ref, kp, kt, kh, vp, vt, vh, _int32(slot_map, "slot_map", index, t), t,
-                                     _stream(stream, index))
+    lib = _native.lib()
+    append = lib.kda_kv_append_quant if cache.quantized else lib.kda_kv_append
+    rc = append(cache._ref, kp, kt, kh, vp, vt, vh, _int32(slot_map, "slot_map", index, t), t, _stream(stream, index))
     if rc:
         _native.check(rc)
 
 
-def paged_attention_workspace(device=None) -> torch.Tensor:
+def kda_kv_read(cache: KvCache, slot_map, *, k=None, v=None, stream=None):
+    """The keys and values at the slots ``slot_map`` [T] (int32; -1 gives
+    zeros), [T, Hkv, 128] each in the cache's 16-bit type.  What the call makes
+    belongs to ``stream``, as in :func:`kda_kv_extend`."""
+    index = cache._index
+    if stream is not None:
+        _check_stream(stream, index)
+        with torch.cuda.stream(stream):
+            return kda_kv_read(cache, slot_map, k=k, v=v)
+    handle, slots = _stream(None, index), _int32(slot_map, "slot_map", index)
+    shape = (slot_map.numel(), cache.n_kv_heads, D)
+    out = []
+    for name, t in (("k", k), ("v", v)):
+        if t is None:
+            t = torch.empty(shape, dtype=cache.dtype, device=cache.k.device)
+        elif tuple(t.shape) != shape or t.dtype != cache.dtype or not t.is_contiguous() or t.get_device() != index:
+            raise ValueError(f"{name} must be a contiguous tensor {list(shape)} of {cache.dtype} on cuda:{index}.")
+        out.append(t)
+    lib = _native.lib()
+    read = lib.kda_kv_read_quant if cache.quantized else lib.kda_kv_read
+    rc = read(cache._ref, slots, shape[0], out[0].data_ptr(), out[1].data_ptr(), handle)
+    if rc:
+        _native.check(rc)
+    return out[0], out[1]
+
+
+def paged_attention_workspace(device=None, *, tokens: int = 0, heads: int = 0) -> torch.Tensor:
     """A workspace for :func:`kda_paged_attention`.  One serves any sequence
-    of calls on one stream; calls that overlap need their own."""
+    of calls on one stream; calls that overlap need their own.  Over an 8-bit
+    cache, for calls of up to ``tokens`` tokens of ``heads`` query heads."""
     device = "cuda" if device is None else device
     with torch.cuda.device(device):  # the size goes by the current device
-        n = int(_native.lib().kda_paged_attention_workspace_bytes())
+        if tokens:
+            n = int(_native.lib().kda_paged_attention_quant_workspace_bytes(tokens, heads))
+        else:
+            n = int(_native.lib().kda_paged_attention_workspace_bytes())
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
@@ -231,11 +295,14 @@ def kda_paged_attention(cache: KvCache, q, cu_seqlens, kv_lens, block_table, *, 
     elif tuple(lse.shape) != (t, hq) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.get_device() != index:
         raise ValueError(f"lse must be a contiguous float32 tensor [T, Hq] on cuda:{index}.")
     if workspace is None:
-        workspace = paged_attention_workspace(q.device)
+        workspace = paged_attention_workspace(q.device, tokens=t, heads=hq) if cache.quantized else \
+            paged_attention_workspace(q.device)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != index:
         raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{index}.")
     table, table_stride, cols = _table(block_table, n, index)
-    rc = _native.lib().kda_paged_attention(
+    lib = _native.lib()
+    attend = lib.kda_paged_attention_quant if cache.quantized else lib.kda_paged_attention
+    rc = attend(
         cache._ref, qp, qt, qh, hq, t, out.data_ptr(), None if lse is None else lse.data_ptr(),
         _int32(cu_seqlens, "cu_seqlens", index, n + 1), _int32(kv_lens, "kv_lens", index), table, table_stride, cols, n,
         D ** -0.5 if scale is None else scale, window, sinks, workspace.data_ptr(), workspace.numel(), handle)
