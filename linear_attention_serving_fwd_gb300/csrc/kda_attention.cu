@@ -54,6 +54,8 @@
 #include <cudaTypedefs.h>
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "kda_kv.cuh"
 #include "kda_tc.cuh"
 
@@ -121,8 +123,42 @@ struct Smem {
   float share[2][2][ROWS];     // what the halves of a row tell each other
 };
 
+// Over an 8-bit cache: tiles of 16 KB, and the scales of the key tiles in flight.
+// A query tile takes two places of 16 KB (bf16) or three (fp16).
+constexpr int TILE8_BYTES = KT * D, BLOCKS8 = KT / KDA_KV_BLOCK;
+template <bool FP16>
+constexpr int Q_PARTS = FP16 ? 3 : 2;
+template <bool FP16>
+constexpr int W_PARTS = FP16 ? 3 : 2;
+template <bool FP16>
+constexpr int STAGES8 = FP16 ? 7 : 9;
+struct QuantSmem : Smem {
+  uint64_t full8[9], empty8[9];
+  float4 k_scale[MASKS][BLOCKS8 / 4];    // of each block of 16 keys
+  float4 v_log[MASKS][BLOCKS8 / 4];      // the scale of its values in powers of two,
+  float4 v_inverse[MASKS][BLOCKS8 / 4];  // and what takes it out of their weights' sum
+};
+// What differs between the two caches.
+template <bool FP16, bool QUANT>
+struct Kind {
+  static constexpr int stages = QUANT ? STAGES8<FP16> : STAGES;
+  static constexpr int tile = QUANT ? TILE8_BYTES : TILE_BYTES;             // bytes of a K or V tile
+  static constexpr int q_tile = QUANT ? Q_PARTS<FP16> * TILE8_BYTES : TILE_BYTES;
+  static constexpr float weight_exp = WEIGHT_EXP<FP16 || QUANT>;
+  static __device__ __forceinline__ uint64_t* full(Smem& sm, uint32_t i) {
+    if constexpr (QUANT) return &static_cast<QuantSmem&>(sm).full8[i];
+    else return &sm.kv_full[i];
+  }
+  static __device__ __forceinline__ uint64_t* empty(Smem& sm, uint32_t i) {
+    if constexpr (QUANT) return &static_cast<QuantSmem&>(sm).empty8[i];
+    else return &sm.kv_empty[i];
+  }
+};
+
 struct Params {
   AttentionParams a;
+  KvQuantCache c;          // the 8-bit cache
+  const float* q_scale;    // of the rows of its queries' parts, [t_total, hq], with scale and log2 e
   int group, tile_tok;     // G, tokens per query tile
   int n_cta;
   int min_piece;           // least tiles per CTA
@@ -252,6 +288,33 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b_de
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
       "}\n" ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
+// the same products of 8-bit operands, 32 of the summed dimension at once
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void mma_f8_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n"
+      "}\n" ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+// Instruction descriptor of kind::f8f6f4 with fp32 accumulation; B is e4m3.
+constexpr uint32_t E4M3 = 0, E5M2 = 1;
+__host__ __device__ constexpr uint32_t idesc_f8(uint32_t M, uint32_t N, uint32_t a) {
+  return (1u << 4) | (a << 7) | (E4M3 << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+__device__ __forceinline__ void tma_load5(void* dst, const CUtensorMap* map, int c1, int c2, int c3, int c4, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+      ::"r"(smem_u32(dst)), "l"(map), "r"(0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar)) : "memory");
+}
 // 128-byte-swizzled operands as the copies leave them: 64 dimensions (128
 // bytes) a row, 8-row groups ``group`` bytes apart, the other 64 dimensions
 // ``half`` bytes further.  K-major (the dimensions are summed over; the leading
@@ -311,14 +374,50 @@ __device__ __forceinline__ unsigned classify(const float (&v)[4]) {
   return f;
 }
 
+// Four numbers of 8 bits.
+__device__ __forceinline__ void widen4(uint32_t w, float (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w >> 16 * i)));
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    v[2 * i] = x.x;
+    v[2 * i + 1] = x.y;
+  }
+}
+// A scale as the calls take it: within the range that they ask for.
+constexpr float SCALE_MIN = 0x1p-48f, SCALE_MAX = 0x1p48f;
+__device__ __forceinline__ float in_range(float s) { return s != s ? 1.f : fminf(fmaxf(s, SCALE_MIN), SCALE_MAX); }
+// Four dimensions a lane of a key's or value's row, as they are in the cache.
+template <bool QUANT>
+using Raw4 = typename std::conditional<QUANT, uint32_t, uint2>::type;
+template <bool FP16, bool QUANT>
+__device__ __forceinline__ Raw4<QUANT> load_row4(const Params& p, bool values, int kvh, int pg, int row) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (QUANT) {
+    const uint8_t* x = values ? p.c.v + pg * p.c.v_sp + row * p.c.v_st + kvh * p.c.v_sh : p.c.k + pg * p.c.k_sp + row * p.c.k_st + kvh * p.c.k_sh;
+    return *reinterpret_cast<const uint32_t*>(x + lane * 4);
+  } else {
+    const AttentionParams& a = p.a;
+    const __nv_bfloat16* x = (values ? a.vc + (int64_t)kvh * a.vc_sh : a.kc + (int64_t)kvh * a.kc_sh) + lane * 4;
+    return *reinterpret_cast<const uint2*>(values ? x + pg * a.vc_sp + row * a.vc_st : x + pg * a.kc_sp + row * a.kc_st);
+  }
+}
+template <bool FP16>
+__device__ __forceinline__ void widen_row4(const uint2& raw, float (&v)[4]) {
+  load_act4<FP16>(reinterpret_cast<const __nv_bfloat16*>(&raw), v);
+}
+template <bool FP16>
+__device__ __forceinline__ void widen_row4(uint32_t raw, float (&v)[4]) { widen4(raw, v); }
+
 // What the values of keys [from, to) hold (none where from >= to: rows of a narrow
 // window may share no key), by a warp that takes every other group of them; ends early where every dimension has a NaN.
-template <bool FP16>
-__device__ __forceinline__ unsigned scan_values(const AttentionParams& p, Smem& sm, const int32_t* table, int kvh, int from, int to,
+template <bool FP16, bool QUANT>
+__device__ __forceinline__ unsigned scan_values(const Params& q, Smem& sm, const int32_t* table, int kvh, int from, int to,
                                                 int half, unsigned f) {
   if (from >= to) return f;
+  const AttentionParams& p = q.a;
   const int lane = threadIdx.x & 31, page = 1 << p.page_shift;
-  const __nv_bfloat16* vc = p.vc + (int64_t)kvh * p.vc_sh + lane * 4;
 #pragma unroll 1
   for (int g = from / GROUP + ((from / GROUP ^ half) & 1); g * GROUP < to; g += 2) {
     if (__all_sync(0xffffffffu, (f & 15) == 15)) break;
@@ -326,23 +425,23 @@ __device__ __forceinline__ unsigned scan_values(const AttentionParams& p, Smem& 
     const int pg = table[(g * GROUP) >> p.page_shift];  // pages hold whole groups
     if (pg < 0 || pg >= p.n_pages) continue;
     float poison = 0.f;
-    uint2 raw[GROUP];
+    Raw4<QUANT> raw[GROUP];
 #pragma unroll
     for (int i = 0; i < GROUP; ++i) {
       const int row = min(max(g * GROUP + i, from), to - 1) & (page - 1);
-      raw[i] = *reinterpret_cast<const uint2*>(vc + pg * p.vc_sp + row * p.vc_st);
+      raw[i] = load_row4<FP16, QUANT>(q, true, kvh, pg, row);
     }
 #pragma unroll
     for (int i = 0; i < GROUP; ++i) {
       float v[4];
-      load_act4<FP16>(reinterpret_cast<const __nv_bfloat16*>(&raw[i]), v);
+      widen_row4<FP16>(raw[i], v);
       poison += v[0] * 0.f + v[1] * 0.f + v[2] * 0.f + v[3] * 0.f;
     }
     if (poison != 0.f) {
 #pragma unroll
       for (int i = 0; i < GROUP; ++i) {
         float v[4];
-        load_act4<FP16>(reinterpret_cast<const __nv_bfloat16*>(&raw[i]), v);
+        widen_row4<FP16>(raw[i], v);
         f |= classify(v);
       }
     }
@@ -351,16 +450,15 @@ __device__ __forceinline__ unsigned scan_values(const AttentionParams& p, Smem& 
 }
 
 // The definition row by row, by one warp, four of the 128 dimensions a lane.
-template <bool FP16>
-__device__ __forceinline__ void attend_row(const AttentionParams& p, Smem& sm, int b, int tok, int head, int pos, int kv) {
+template <bool FP16, bool QUANT>
+__device__ __forceinline__ void attend_row(const Params& all, Smem& sm, int b, int tok, int head, int pos, int kv) {
+  const AttentionParams& p = all.a;
   const int lane = threadIdx.x & 31;
   const int kvh = head / (p.hq / p.hkv), page = 1 << p.page_shift;
   float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -CUDART_INF_F, l = 0.f;
   load_act4<FP16>(p.q + (int64_t)tok * p.q_st + (int64_t)head * p.q_sh + lane * 4, q);
   const int hi = min(pos + 1, kv), lo = p.window ? max(0, pos + 1 - p.window) : 0;
   const int32_t* table = p.table + (int64_t)b * p.table_stride;
-  const __nv_bfloat16* kc = p.kc + (int64_t)kvh * p.kc_sh + lane * 4;
-  const __nv_bfloat16* vc = p.vc + (int64_t)kvh * p.vc_sh + lane * 4;
 #pragma unroll 1
   for (int part = 0; part < 2; ++part) {
     const int from = part == 0 ? 0 : lo, to = part == 0 ? min(min(p.sinks, lo), hi) : hi;
@@ -369,19 +467,24 @@ __device__ __forceinline__ void attend_row(const AttentionParams& p, Smem& sm, i
       if (lane == 0) *(volatile int*)&sm.beat = (int)clock();
       const int pg = table[(g * GROUP) >> p.page_shift];
       if (pg < 0 || pg >= p.n_pages) continue;
-      uint2 raw[GROUP];
-      float s[GROUP], top = m;
+      Raw4<QUANT> raw[GROUP];
+      float s[GROUP], top = m, scale = p.scale, v_scale = 1.f;
+      if constexpr (QUANT) {  // a group lies in one block
+        const int64_t at = (((int64_t)pg * p.hkv + kvh) << (p.page_shift - 4)) + ((g * GROUP) & (page - 1)) / KDA_KV_BLOCK;
+        scale *= in_range(all.c.k_scale[at]);
+        v_scale = in_range(all.c.v_scale[at]);
+      }
 #pragma unroll
       for (int i = 0; i < GROUP; ++i) {
         const int row = min(max(g * GROUP + i, from), to - 1) & (page - 1);
         float k[4];
-        load_act4<FP16>(kc + pg * p.kc_sp + row * p.kc_st, k);
-        raw[i] = *reinterpret_cast<const uint2*>(vc + pg * p.vc_sp + row * p.vc_st);
+        widen_row4<FP16>(load_row4<FP16, QUANT>(all, false, kvh, pg, row), k);
+        raw[i] = load_row4<FP16, QUANT>(all, true, kvh, pg, row);
         s[i] = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
       }
 #pragma unroll
       for (int i = 0; i < GROUP; ++i) {
-        s[i] = p.scale * warp_sum(s[i]);
+        s[i] = scale * warp_sum(s[i]);
         if (g * GROUP + i >= from && g * GROUP + i < to) top = fmaxf(top, s[i]);
       }
       const float corr = m == -CUDART_INF_F ? 0.f : expf(m - top);
@@ -395,10 +498,10 @@ __device__ __forceinline__ void attend_row(const AttentionParams& p, Smem& sm, i
         // a score of -inf has a weight of 0, whether there is a maximum yet or not
         const float w = s[i] == -CUDART_INF_F ? 0.f : expf(s[i] - top);
         float v[4];
-        load_act4<FP16>(reinterpret_cast<const __nv_bfloat16*>(&raw[i]), v);
+        widen_row4<FP16>(raw[i], v);
         l += w;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] += w * v[j];
+        for (int j = 0; j < 4; ++j) o[j] += w * (QUANT ? v[j] * v_scale : v[j]);
       }
     }
   }
@@ -412,7 +515,7 @@ __device__ __forceinline__ void attend_row(const AttentionParams& p, Smem& sm, i
 // Rows ``bad`` of 32 of a tile, whose results stand in memory, by the two warps
 // that share them.  A visible value early in a long cache reaches every row after
 // it: the values that all of them see are read once for all.
-template <bool FP16>
+template <bool FP16, bool QUANT>
 __device__ __forceinline__ void mend_rows(const Params& p, Smem& sm, int s, int half, int quarter, int bar, const Item& it, int tile,
                                           unsigned bad) {
   const int lane = threadIdx.x & 31, r = quarter * 32 + lane;
@@ -422,8 +525,8 @@ __device__ __forceinline__ void mend_rows(const Params& p, Smem& sm, int s, int 
   const int lo = __reduce_max_sync(0xffffffffu, mine && p.a.window ? max(0, pos + 1 - p.a.window) : 0);
   const int32_t* table = p.a.table + (int64_t)it.b * p.a.table_stride;
   unsigned f = 0;
-  f = scan_values<FP16>(p.a, sm, table, it.kvh, 0, min(min(p.a.sinks, lo), hi), half, f);
-  f = scan_values<FP16>(p.a, sm, table, it.kvh, lo, hi, half, f);
+  f = scan_values<FP16, QUANT>(p, sm, table, it.kvh, 0, min(min(p.a.sinks, lo), hi), half, f);
+  f = scan_values<FP16, QUANT>(p, sm, table, it.kvh, lo, hi, half, f);
   sm.share[s][half][r] = __uint_as_float(f);
   named_bar_sync(bar, 64);
   f |= __float_as_uint(sm.share[s][half ^ 1][r]);
@@ -443,7 +546,7 @@ __device__ __forceinline__ void mend_rows(const Params& p, Smem& sm, int s, int 
       else if (o[j] == CUDART_INF_F) stands = stands && inf;
       else if (o[j] == -CUDART_INF_F) stands = stands && neg;
     }
-    if (!__all_sync(0xffffffffu, stands)) attend_row<FP16>(p.a, sm, it.b, tok, head, it.pos + i, it.kv);
+    if (!__all_sync(0xffffffffu, stands)) attend_row<FP16, QUANT>(p, sm, it.b, tok, head, it.pos + i, it.kv);
   }
 }
 
@@ -518,7 +621,8 @@ __device__ __forceinline__ long long request_cost(const Params& p, int b, bool v
 }
 
 // --- the copying warp ------------------------------------------------------------------
-// joined copies: k and v of five dimensions, else of four
+// joined copies: k and v of five dimensions, else of four; q of four, in 8 bits
+// (its parts) of five
 struct Maps {
   CUtensorMap k, v, q, q1;  // q: a tile's tokens in a box, q1: one token
 };
@@ -535,7 +639,9 @@ __device__ __forceinline__ void tile_range(const Params& p, Item& it, int s) {
 }
 __device__ __forceinline__ bool active(const int (&act)[3], int i) { return i < act[0] || (i >= act[1] && i < act[2]); }
 
+template <bool FP16, bool QUANT>
 __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Smem& sm, unsigned char* q_smem, unsigned char* kv_smem) {
+  using K = Kind<FP16, QUANT>;
   const int lane = threadIdx.x & 31;
   unsigned* err = p.a.err;
   uint32_t fills = 0, tiles = 0, q_count = 0;
@@ -563,7 +669,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
       if (pg >= p.a.n_pages) set_error(err, ERR_INDEX);
       return pg < 0 || pg >= p.a.n_pages ? -1 : pg;
     };
-    int pg = page_of(it.i0);
+    int pg = QUANT ? -1 : page_of(it.i0);
     // Queries: their buffer is free only when the item before is through, so the
     // first keys and values go ahead of them while there is room.
     bool asked = false;
@@ -582,6 +688,23 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
       ++q_count;
       const bool single = it.n_tok <= 8;
       const uint32_t box_bytes = (uint32_t)p.group * 128u;
+      if constexpr (QUANT) {
+        constexpr int PARTS = Q_PARTS<FP16>;
+        if (lane == 0)
+          mbar_arrive_expect_tx(&sm.q_full, PARTS * (single ? it.n_tok : (two ? 2u : 1u) * p.tile_tok) * box_bytes);
+        __syncwarp();
+        if (single) {
+          if (lane < PARTS * it.n_tok) {
+            const int i = lane / PARTS, part = lane % PARTS, s = i / p.tile_tok, r = (i % p.tile_tok) * p.group;
+            tma_load5(q_smem + s * K::q_tile + part * TILE8_BYTES + r * 128, &maps.q1, 0, it.kvh, it.tok + i, part, &sm.q_full);
+          }
+        } else if (lane < (two ? 2 : 1) * PARTS) {
+          const int s = lane / PARTS, part = lane % PARTS;
+          tma_load5(q_smem + s * K::q_tile + part * TILE8_BYTES, &maps.q, 0, it.kvh, it.tok + s * p.tile_tok, part, &sm.q_full);
+        }
+        __syncwarp();
+        return;
+      }
       if (lane == 0)
         mbar_arrive_expect_tx(&sm.q_full, single ? 2u * it.n_tok * box_bytes : (two ? 4u : 2u) * p.tile_tok * box_bytes);
       __syncwarp();
@@ -597,6 +720,73 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
       }
       __syncwarp();
     };
+    if constexpr (QUANT) {
+      // Four key tiles at once, a lane a block of 16 keys: its page, then its
+      // scales, are fetched while the four before are copied.
+      QuantSmem& qs = static_cast<QuantSmem&>(sm);
+      auto key_of = [&](int i) { return list_tile(it, i) * KT + (lane & 7) * KDA_KV_BLOCK; };
+      auto block_page = [&](int i) {  // i: the four's first; -1 for a block that no row sees
+        i += lane >> 3;
+        if (i >= it.i1) return -1;
+        const int key = key_of(i);
+        if (!((key < it.hi && key + KDA_KV_BLOCK > it.lo) || key < it.sink_hi)) return -1;
+        const int pg = table[key >> p.a.page_shift];
+        if (pg >= p.a.n_pages) set_error(err, ERR_INDEX);
+        return pg < 0 || pg >= p.a.n_pages ? -1 : pg;
+      };
+      auto block_scales = [&](int i, int pg) {
+        if (pg < 0) return make_float2(1.f, 1.f);
+        const int64_t at = (((int64_t)pg * p.a.hkv + it.kvh) << (p.a.page_shift - 4)) +
+                           ((key_of(i + (lane >> 3)) & (page - 1)) / KDA_KV_BLOCK);
+        return make_float2(p.c.k_scale[at], p.c.v_scale[at]);
+      };
+      int pages = block_page(it.i0), pages_next = -1;
+      float2 scales = make_float2(0.f, 0.f), scales_next = scales;
+      for (int i = it.i0; i < it.i1; ++i, ++tiles) {
+        const int sub = (i - it.i0) & 3;
+        if (sub == 0 && i > it.i0) {
+          pages = pages_next;
+          scales = scales_next;
+        }
+        // the page of a box of 16 to 128 keys, wherever one of its blocks is seen
+        int box_page = pages;
+        for (int d = 1; d < 8 / p.boxes; d <<= 1) box_page = max(box_page, __shfl_xor_sync(0xffffffffu, box_page, d));
+        const int c_page = __shfl_sync(0xffffffffu, box_page < 0 ? p.a.n_pages : box_page, (sub * 8 + lane * (8 / p.boxes)) & 31);
+        const unsigned held = __ballot_sync(0xffffffffu, pages >= 0) >> (sub * 8) & 0xff;
+        const int row = (list_tile(it, i) * KT) & (page - 1) & ~(box - 1);
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv, ++fills) {
+          const uint32_t st = fills % K::stages;
+          const uint32_t parity = ((fills / K::stages) & 1) ^ 1;
+          if (!asked && __any_sync(0xffffffffu, mbar_test_wait(&sm.q_empty, (q_count & 1) ^ 1) ||
+                                                    !mbar_test_wait(K::empty(sm, st), parity)))
+            queries();
+          if (!__all_sync(0xffffffffu, wait_or_stop(K::empty(sm, st), parity, sm, err))) goto out;
+          // the copy's bytes are announced after it: the arrival that ends the phase comes with them
+          if (lane < p.boxes)
+            tma_load4(kv_smem + st * K::tile + lane * box * 128, kv == 0 ? &maps.k : &maps.v, 0, row, it.kvh, c_page, K::full(sm, st));
+          if (kv == 0) {
+            if (i == it.i0) scales = block_scales(i, pages);
+            if (lane >> 3 == sub) {
+              const float ks = in_range(scales.x), vs = in_range(scales.y);
+              if (ks != scales.x || vs != scales.y) set_error(err, ERR_RANGE);
+              const int place = tiles % MASKS, b = lane & 7;
+              reinterpret_cast<float*>(qs.k_scale[place])[b] = ks;
+              reinterpret_cast<float*>(qs.v_log[place])[b] = log2f(vs);
+              reinterpret_cast<float*>(qs.v_inverse[place])[b] = 1.f / vs;
+            }
+            if (lane == 0) *(volatile int*)&sm.page_mask[tiles % MASKS] = (int)held;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(K::full(sm, st), K::tile);
+          __syncwarp();
+        }
+        if (sub == 0) pages_next = block_page(i + 4);
+        if (sub == 2) scales_next = block_scales(i + 2, pages_next);
+      }
+      if (!asked) queries();
+      continue;
+    }
     // keys and values
     for (int i = it.i0; i < it.i1; ++i, ++tiles) {
       const int row = (list_tile(it, i) * KT) & (page - 1) & ~(box - 1);
@@ -630,8 +820,8 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
 out:
   if (is_dead(sm) && lane == 0) {
     // copies in flight land before the CTA ends
-    for (uint32_t f = fills > STAGES ? fills - STAGES : 0; f < fills; ++f)
-      mbar_wait_bounded(&sm.kv_full[f % STAGES], (f / STAGES) & 1, err);
+    for (uint32_t f = fills > K::stages ? fills - K::stages : 0; f < fills; ++f)
+      mbar_wait_bounded(K::full(sm, f % K::stages), (f / K::stages) & 1, err);
     if (q_count > 0) mbar_wait_bounded(&sm.q_full, (q_count - 1) & 1, err);
   }
 }
@@ -653,21 +843,26 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // A place in the ring of K and V tiles and the parity of its fill.
+template <int N>
 struct Stage {
   uint32_t at = 0, parity = 0;
   __device__ __forceinline__ void skip(uint32_t n) {
     at += n;
-    if (at >= STAGES) {
-      at -= STAGES;
+    if (at >= N) {
+      at -= N;
       parity ^= 1;
     }
   }
 };
 
+template <bool FP16, bool QUANT>
 __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint32_t q_addr, uint32_t kv_addr, uint32_t tmem,
                                          uint32_t bf16) {
+  using K = Kind<FP16, QUANT>;
+  using Stage = Stage<K::stages>;
   unsigned* err = p.a.err;
-  const uint32_t id_qk = tc::idesc_f16(ROWS, KT, bf16), id_pv = tc::idesc_f16(ROWS, D, bf16) | (1u << 16);
+  const uint32_t id_qk = QUANT ? idesc_f8(ROWS, KT, E4M3) : tc::idesc_f16(ROWS, KT, bf16);
+  const uint32_t id_pv = (QUANT ? idesc_f8(ROWS, D, E5M2) : tc::idesc_f16(ROWS, D, bf16)) | (1u << 16);
   const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * 128;
   Stage next;  // of list index i0 of the next item
   uint32_t q_parity = 0, p_parity = 0, o_parity = 1;
@@ -704,7 +899,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
     const bool two = it.n_tok > p.tile_tok;
     await(&sm.q_full, q_parity);
     q_parity ^= 1;
-    const uint64_t qd = tc::smem_desc_sw128(q_addr + (two ? s * TILE_BYTES : 0));
+    const uint64_t qd = tc::smem_desc_sw128(q_addr + (two ? s * K::q_tile : 0));
     int last = it.i1 - 1;  // this stream's last tile
     if (two) {
       while (last >= it.i0 && !active(act, last)) --last;
@@ -715,15 +910,21 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
     Stage st = next;
     bool scored = false;  // this tile's scores have been issued behind the last tile's product
     auto scores = [&](int i, const Stage& at) {
-      const uint64_t kd = k_desc + at.at * (TILE_BYTES >> 4);
+      const uint64_t kd = k_desc + at.at * (K::tile >> 4);
       if (elect_one()) {
+        if constexpr (QUANT) {
+#pragma unroll
+          for (int j = 0; j < Q_PARTS<FP16> * (D / 32); ++j)  // the queries' parts one after another
+            mma_f8(t_s, qd + (j >> 2) * (TILE8_BYTES >> 4) + (j & 3) * 2, kd + (j & 3) * 2, id_qk, j > 0 ? 1u : 0u);
+        } else {
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
           const uint32_t in = (j & 3) * 2;  // 32 bytes
           tc::mma_f16(t_s, qd + (j >> 2) * (HALF_BYTES >> 4) + in, kd + (j >> 2) * k_half + in, id_qk, j > 0 ? 1u : 0u);
         }
+        }
         tc::mma_commit(&sm.s_full[s]);
-        tc::mma_commit(&sm.kv_empty[at.at]);
+        tc::mma_commit(K::empty(sm, at.at));
         if (i == last) {
           tc::mma_commit(&sm.q_empty);  // this stream's products have read the queries
           // .. and the other stream's result may take their place, where it does
@@ -738,11 +939,11 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
       if (two ? !active(act, i) : ((i - it.i0) & 1) != odd) {
         // hidden from every row, or the other stream's: both streams see every
         // fill, so that none is two fills behind (a wait tells odd from even)
-        await(&sm.kv_full[st.at], st.parity);
-        await(&sm.kv_full[sv.at], sv.parity);
+        await(K::full(sm, st.at), st.parity);
+        await(K::full(sm, sv.at), sv.parity);
         if (elect_one()) {
-          mbar_arrive(&sm.kv_empty[st.at]);
-          mbar_arrive(&sm.kv_empty[sv.at]);
+          mbar_arrive(K::empty(sm, st.at));
+          mbar_arrive(K::empty(sm, sv.at));
         }
         __syncwarp();
         if (two) {
@@ -753,7 +954,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
         continue;
       }
       if (!scored) {
-        await(&sm.kv_full[st.at], st.parity);
+        await(K::full(sm, st.at), st.parity);
         tc::fence_after_sync();
         scores(i, st);
       }
@@ -762,12 +963,12 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
       const bool more = two && i + 1 < it.i1 && active(act, i + 1);
       Stage sk = sv;
       sk.skip(1);
-      await(&sm.kv_full[sv.at], sv.parity);
+      await(K::full(sm, sv.at), sv.parity);
       if (first) {
         await(&sm.o_free[s], o_parity);
         o_parity ^= 1;
       }
-      const uint64_t vd = v_desc + sv.at * (TILE_BYTES >> 4);
+      const uint64_t vd = v_desc + sv.at * (K::tile >> 4);
       if (two) {
         await(&sm.turn[s], turn);
         turn ^= 1;
@@ -776,14 +977,23 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
       p_parity ^= 1;
       tc::fence_after_sync();
       if (elect_one()) {
+        if constexpr (QUANT) {
 #pragma unroll
-        for (int j = 0; j < KT / 16; ++j)  // 16 keys: two 8-row groups of V
-          mma_f16_ts(t_o, t_s + (j >> 2) * 64 + (j & 3) * 8, vd + j * v_step, id_pv, (j > 0 || !first) ? 1u : 0u);
-        tc::mma_commit(&sm.kv_empty[sv.at]);
+          for (int j = 0; j < KT / 32; ++j)  // 32 keys: four 8-row groups of V, 8 columns of each part of the weights
+#pragma unroll
+            for (int part = 0; part < W_PARTS<FP16>; ++part)
+              mma_f8_ts(t_o, t_s + (j >> 1) * 64 + part * 16 + (j & 1) * 8, vd + j * 2 * v_step, id_pv,
+                        (j > 0 || part > 0 || !first) ? 1u : 0u);
+        } else {
+#pragma unroll
+          for (int j = 0; j < KT / 16; ++j)  // 16 keys: two 8-row groups of V
+            mma_f16_ts(t_o, t_s + (j >> 2) * 64 + (j & 3) * 8, vd + j * v_step, id_pv, (j > 0 || !first) ? 1u : 0u);
+        }
+        tc::mma_commit(K::empty(sm, sv.at));
       }
       __syncwarp();
       if (more) {
-        scored = __all_sync(0xffffffffu, mbar_test_wait(&sm.kv_full[sk.at], sk.parity));
+        scored = __all_sync(0xffffffffu, mbar_test_wait(K::full(sm, sk.at), sk.parity));
         if (scored) {
           tc::fence_after_sync();
           scores(i + 1, sk);
@@ -944,6 +1154,39 @@ __device__ __forceinline__ long long measure_line(const Params& p, Smem& sm, int
   return piece;
 }
 
+// --- weights in 8 bits ---------------------------------------------------------------------
+// A score's factor of its row and its key's block, not 0 (hidden scores are -inf).
+__device__ __forceinline__ float row_factor(float sl, float ks) { return fmaxf(sl * ks, 1e-37f); }
+
+// Weights as sums of PARTS e5m2 numbers, from the largest on: e5m2 is the upper
+// half of fp16 with its exponents, so that small weights keep their relative
+// precision.  Each part takes what is left to its nearest 3 significant bits (half
+// up, in fp16's bits): of an fp16 weight two parts leave at most 2^-7 of it, three 2^-11.
+// Four keys to a column, 16 columns to a part, w[c] are 32 keys two by two.
+template <int PARTS>
+__device__ __forceinline__ void store_parts(uint32_t t_s, uint32_t (&w)[2][16]) {
+#pragma unroll
+  for (int part = 0; part < PARTS; ++part) {
+    uint32_t y[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      uint32_t r[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t& h = w[i >> 3][(i & 7) * 2 + k];
+        r[k] = h + 0x00800080u;
+        if (part + 1 < PARTS) {
+          const uint32_t top = r[k] & 0xff00ff00u;
+          const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&top));
+          h = *reinterpret_cast<const uint32_t*>(&rest);
+        }
+      }
+      y[i] = __byte_perm(r[0], r[1], 0x7531);
+    }
+    tmem_st16(t_s + part * 16, y);
+  }
+}
+
 // --- a softmax warpgroup -----------------------------------------------------------------
 __device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
@@ -954,7 +1197,7 @@ __device__ __forceinline__ size_t part_piece(size_t row, int c) { return ((row >
 
 // Joins rows of a tile's parts: a unit is 8 rows by 4 PIECES pieces, a lane one
 // row and PIECES pieces.
-template <bool FP16, int PIECES>
+template <bool FP16, bool QUANT, int PIECES>
 __device__ __forceinline__ void join_rows(const Params& p, Smem& sm, int s, const Item& it, int tile, int n_rows) {
   constexpr int UNITS = 8 / PIECES;  // of 8 rows
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 7;
@@ -1001,7 +1244,7 @@ __device__ __forceinline__ void join_rows(const Params& p, Smem& sm, int s, cons
       *reinterpret_cast<uint2*>(out + i * 16) =
           make_uint2(act_pack2<FP16>(o[4 * i], o[4 * i + 1]), act_pack2<FP16>(o[4 * i + 2], o[4 * i + 3]));
     if (p.a.lse && c == 0)
-      p.a.lse[(int64_t)tok * p.a.hq + head] = l == 0.f ? -CUDART_INF_F : (top + log2f(l) - WEIGHT_EXP<FP16>) * LN2;
+      p.a.lse[(int64_t)tok * p.a.hq + head] = l == 0.f ? -CUDART_INF_F : (top + log2f(l) - Kind<FP16, QUANT>::weight_exp) * LN2;
   }
 }
 
@@ -1009,23 +1252,24 @@ __device__ __forceinline__ void join_rows(const Params& p, Smem& sm, int s, cons
 // them.  Many rows: a lane takes a quarter of its row, so that each part's loads
 // are many.  Few: a sixteenth, so that all warps have some, and several parts'
 // loads at once.
-template <bool FP16>
+template <bool FP16, bool QUANT>
 __device__ __forceinline__ void join_parts(const Params& p, Smem& sm, int s, const Item& it, int tile, int n_rows) {
   const int warp = (threadIdx.x >> 5) & 7, bar = STREAM_BAR + s;
   if ((threadIdx.x & 255) < 4) sm.poisoned[s][0][threadIdx.x & 3] = 0;
   named_bar_sync(bar, 256);
-  if (n_rows > 32) join_rows<FP16, 8>(p, sm, s, it, tile, n_rows);
-  else join_rows<FP16, 2>(p, sm, s, it, tile, n_rows);
+  if (n_rows > 32) join_rows<FP16, QUANT, 8>(p, sm, s, it, tile, n_rows);
+  else join_rows<FP16, QUANT, 2>(p, sm, s, it, tile, n_rows);
   __syncwarp();
   named_bar_sync(bar, 256);
   const int quarter = warp & 3;
   const unsigned bad = sm.poisoned[s][0][quarter];
-  if (bad) mend_rows<FP16>(p, sm, s, warp >> 2, quarter, PAIR_BAR + s * 4 + quarter, it, tile, bad);
+  if (bad) mend_rows<FP16, QUANT>(p, sm, s, warp >> 2, quarter, PAIR_BAR + s * 4 + quarter, it, tile, bad);
 }
 
-template <bool FP16>
+template <bool FP16, bool QUANT>
 __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned char* q_smem, unsigned char* kv_smem,
                                              uint32_t tmem) {
+  using K = Kind<FP16, QUANT>;
   unsigned* err = p.a.err;
   const int s = threadIdx.x >> 8, half = (threadIdx.x >> 7) & 1;  // stream; half of the tile's keys, and of the dimensions
   const int r = threadIdx.x & 127, lane = r & 31, quarter = r >> 5;
@@ -1033,8 +1277,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
   const uint32_t lane_base = tmem + ((uint32_t)(r & 96) << 16);
   const uint32_t t_s = lane_base + s * 128 + half * 64, t_o = lane_base + 256 + s * 128 + half * 64;
   const int row_tok = r / p.group, row_head = r % p.group;
-  const float sl = p.a.scale * LOG2E;
-  const int all_held = (1 << p.boxes) - 1;
+  float sl = p.a.scale * LOG2E;
+  const int all_held = QUANT ? (1 << BLOCKS8) - 1 : (1 << p.boxes) - 1;
   const int box_shift = p.a.page_shift < 7 ? p.a.page_shift : 7;
   uint32_t fills = 0, tiles = 0, s_count = 0, o_count = 0, merges = 0, q_reads = 0;
   for (uint32_t items = 0;; ++items) {
@@ -1050,6 +1294,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
     const int pos = it.pos + tb;
     const int hi = valid ? max(0, min(pos + 1, kv)) : 0, lo = p.a.window ? max(0, pos + 1 - p.a.window) : 0;
     const int sink = min(p.a.sinks, hi);
+    if constexpr (QUANT) sl = valid ? p.q_scale[(int64_t)(it.tok + tb) * p.a.hq + it.kvh * p.group + row_head] : 1.f;
     const bool any_row = __any_sync(0xffffffffu, valid);
     const int hi_min = __reduce_min_sync(0xffffffffu, valid ? hi : 0x7fffffff);
     const int lo_max = __reduce_max_sync(0xffffffffu, valid ? lo : 0);
@@ -1057,7 +1302,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
     // key tiles that every row of the warp sees whole: up to clear_hi, from
     // clear_lo on or below clear_sink
     const int clear_hi = hi_min - 64 - half * 64, clear_lo = lo_max - half * 64, clear_sink = sink_min - 64 - half * 64;
-    float m = -CUDART_INF_F, l = 0.f;  // m is the row's, l this half's
+    float m = -CUDART_INF_F, l = 0.f;  // m is the row's (in 8 bits: in powers of two), l this half's
     bool stepped = false;
     // the last joined results have been read (where they are, and what was told
     // with them, is written anew)
@@ -1073,13 +1318,17 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
         // the rows past the cached tokens hold whatever was there: zeros there
         // keep the products finite
         const uint32_t f = fills + 2 * (i - i0) + 1;
-        wait(&sm.kv_full[f % STAGES], (f / STAGES) & 1, sm, err);
+        wait(K::full(sm, f % K::stages), (f / K::stages) & 1, sm, err);
         const int from = max(0, kv - key);
-        unsigned char* v = kv_smem + (f % STAGES) * TILE_BYTES;
+        unsigned char* v = kv_smem + (f % K::stages) * K::tile;
+        if constexpr (QUANT) {
+          for (int c = r; c < (64 - from) * 8; c += 128) *reinterpret_cast<int4*>(v + (half * 64 + from) * 128 + c * 16) = make_int4(0, 0, 0, 0);
+        } else {
         for (int c = r; c < (64 - from) * 16; c += 128) {
           const int row = half * 64 + from + (c >> 4);
           *reinterpret_cast<int4*>(v + (row >> 3) * p.group_bytes + ((c >> 3) & 1) * p.half_bytes + (row & 7) * 128 + (c & 7) * 16) =
               make_int4(0, 0, 0, 0);
+        }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -1094,7 +1343,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
             tc::tmem_ld32_async(t_s + c * 32, x);
             const int k0 = key + c * 32, box = half * 2 + c;
             uint32_t seen = bits_below(hi - k0) & (~bits_below(lo - k0) | bits_below(sink - k0));
-            if (box_shift == 4)
+            if (QUANT || box_shift == 4)
               seen &= ((held >> (2 * box)) & 1 ? 0xffffu : 0u) | ((held >> (2 * box + 1)) & 1 ? 0xffff0000u : 0u);
             else if (!((held >> ((box * 32) >> box_shift)) & 1))
               seen = 0;
@@ -1121,6 +1370,39 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
 #pragma unroll 1
         for (int pass = 0;; ++pass) {
           if (stepped || pass > 0) {
+            float total;  // of the weights, which has to stay below LIMIT
+            if constexpr (QUANT) {
+              // The values' scale is part of the score here, so that a weight is what
+              // their number is multiplied by, and is taken out of the row's sum.
+              const QuantSmem& qs = static_cast<const QuantSmem&>(sm);
+              const int place = (tiles + i - i0) % MASKS;
+              const float ref = K::weight_exp - (m == -CUDART_INF_F ? 0.f : m);
+              total = 0.f;
+              sum[0].x = 0.f;
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                load(c);
+                const float2 ks = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(&qs.k_scale[place][half]) + c * 2);
+                const float2 lv = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(&qs.v_log[place][half]) + c * 2);
+                const float2 iv = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(&qs.v_inverse[place][half]) + c * 2);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                  const float a = row_factor(sl, b ? ks.y : ks.x), r0 = ref + (b ? lv.y : lv.x);
+                  const float2 a2 = make_float2(a, a), r2 = make_float2(r0, r0);
+                  float2 block = make_float2(0.f, 0.f);
+#pragma unroll
+                  for (int j = b * 8; j < b * 8 + 8; ++j) {
+                    const float2 e = ffma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), a2, r2);
+                    const float2 y = make_float2(ex2(e.x), ex2(e.y));
+                    block = fadd2(block, y);
+                    w[c][j] = act_pack2<true>(y.x, y.y);
+                  }
+                  const float t = block.x + block.y;
+                  total += t;
+                  sum[0].x += t * (b ? iv.y : iv.x);
+                }
+              }
+            } else {
             const float ref = WEIGHT_EXP<FP16> - (m == -CUDART_INF_F ? 0.f : m * sl);
             const float2 sl2 = make_float2(sl, sl), ref2 = make_float2(ref, ref);
             sum[0] = sum[1] = make_float2(0.f, 0.f);
@@ -1137,13 +1419,29 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
             }
             sum[0] = fadd2(sum[0], sum[1]);
             sum[0].x += sum[0].y;
+            total = sum[0].x;
+            }
             // rows past the block hold anything and have no say
-            if (pass > 0 || !named_bar_or(pair, 64, valid && (m == -CUDART_INF_F || !(sum[0].x <= LIMIT)))) break;
+            if (pass > 0 || !named_bar_or(pair, 64, valid && (m == -CUDART_INF_F || !(total <= LIMIT)))) break;
           }
           float m_new = m;
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
             load(c);
+            if constexpr (QUANT) {
+              const QuantSmem& qs = static_cast<const QuantSmem&>(sm);
+              const int place = (tiles + i - i0) % MASKS;
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const float ks = reinterpret_cast<const float*>(&qs.k_scale[place][half])[c * 2 + b];
+                const float lv = reinterpret_cast<const float*>(&qs.v_log[place][half])[c * 2 + b];
+                float top = -CUDART_INF_F;
+#pragma unroll
+                for (int j = b * 16; j < b * 16 + 16; j += 2)
+                  top = max3(top, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+                m_new = fmaxf(m_new, fmaf(top, row_factor(sl, ks), lv));
+              }
+            } else {
             float top[2] = {m_new, m_new};
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
@@ -1151,11 +1449,12 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
               top[1] = max3(top[1], __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
             }
             m_new = fmaxf(top[0], top[1]);
+            }
           }
           sm.share[s][half][r] = m_new;
           named_bar_sync(pair, 64);
           m_new = fmaxf(m_new, sm.share[s][half ^ 1][r]);
-          const float corr = m_new == -CUDART_INF_F ? 1.f : ex2((m - m_new) * sl);
+          const float corr = m_new == -CUDART_INF_F ? 1.f : ex2(QUANT ? m - m_new : (m - m_new) * sl);
           m = m_new;
           l *= corr;
           if (stepped) {
@@ -1173,8 +1472,12 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
         }
         l += sum[0].x;
         // they take the place of the first 32 of this half's columns of S
-        tmem_st16(t_s, w[0]);
-        tmem_st16(t_s + 16, w[1]);
+        if constexpr (QUANT) {
+          store_parts<W_PARTS<FP16>>(t_s, w);
+        } else {
+          tmem_st16(t_s, w[0]);
+          tmem_st16(t_s + 16, w[1]);
+        }
         tmem_wait_st();
       }
       stepped = true;
@@ -1199,9 +1502,9 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
     // m2: the reference in powers of two, -inf where the row has seen nothing, and
     // there alone: scores that are all NaN leave no maximum, but a sum, which has
     // to reach the parts' joining.
-    float m2 = l == 0.f ? -CUDART_INF_F : m == -CUDART_INF_F ? 0.f : m * sl;
+    float m2 = l == 0.f ? -CUDART_INF_F : m == -CUDART_INF_F ? 0.f : QUANT ? m : m * sl;
     const bool merged = !two && i1 - i0 > 1;
-    unsigned char* merge = q_smem + (it.n_tok * p.group <= MERGE_ROWS ? TILE_BYTES : 0);
+    unsigned char* merge = q_smem + (it.n_tok * p.group <= MERGE_ROWS ? K::q_tile : 0);
     if (!two && odd) {
       if (merged) {
         if (merge == q_smem) {
@@ -1321,12 +1624,12 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
         poison = 0.f;
       }
       if (half == 0 && valid && p.a.lse)
-        p.a.lse[(int64_t)tok * p.a.hq + head] = l == 0.f ? -CUDART_INF_F : (m2 + log2f(l) - WEIGHT_EXP<FP16>) * LN2;
+        p.a.lse[(int64_t)tok * p.a.hq + head] = l == 0.f ? -CUDART_INF_F : (m2 + log2f(l) - K::weight_exp) * LN2;
       const unsigned mine = __ballot_sync(0xffffffffu, valid && poison != 0.f && l == l);
       if (lane == 0) sm.poisoned[s][half][quarter] = mine;
       named_bar_sync(pair, 64);  // the row's own stores come before what is read of them
       const unsigned bad = mine | sm.poisoned[s][half ^ 1][quarter];
-      if (bad) mend_rows<FP16>(p, sm, s, half, quarter, pair, it, tile, bad);
+      if (bad) mend_rows<FP16, QUANT>(p, sm, s, half, quarter, pair, it, tile, bad);
     } else {
       if (half == 0 && valid) __stcg(&p.part_ml[part_row], make_float2(m2, l));
       named_bar_sync(bar, 256);
@@ -1342,7 +1645,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
       }
       named_bar_sync(bar, 256);
       if (sm.last[s]) {
-        join_parts<FP16>(p, sm, s, it, tile, min(p.tile_tok, it.n_tok - tile * p.tile_tok) * p.group);
+        join_parts<FP16, QUANT>(p, sm, s, it, tile, min(p.tile_tok, it.n_tok - tile * p.tile_tok) * p.group);
       }
     }
     __syncwarp();
@@ -1350,17 +1653,19 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
   }
 }
 
-template <bool FP16>
+template <bool FP16, bool QUANT>
 __global__ void __launch_bounds__(THREADS, 1)
     attention_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
   extern __shared__ __align__(1024) unsigned char q_smem[];  // the swizzle repeats every 1024 bytes
-  unsigned char* kv_smem = q_smem + 2 * TILE_BYTES;
-  Smem& sm = *reinterpret_cast<Smem*>(kv_smem + STAGES * TILE_BYTES);
+  using K = Kind<FP16, QUANT>;
+  unsigned char* kv_smem = q_smem + 2 * K::q_tile;
+  using Shared = typename std::conditional<QUANT, QuantSmem, Smem>::type;
+  Shared& sm = *reinterpret_cast<Shared*>(kv_smem + K::stages * K::tile);
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
   if (threadIdx.x == PLAN_WARP * 32) {
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&sm.kv_full[i], 1);
-      mbar_init(&sm.kv_empty[i], 2);  // both streams
+    for (int i = 0; i < K::stages; ++i) {
+      mbar_init(K::full(sm, i), 1);
+      mbar_init(K::empty(sm, i), 2);  // both streams
     }
     for (int i = 0; i < RING; ++i) {
       mbar_init(&sm.ring_full[i], 1);
@@ -1394,11 +1699,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   const uint32_t tmem = sm.tmem;
   if (warp < SOFTMAX_WARPS) {
-    softmax_role<FP16>(p, sm, q_smem, kv_smem, tmem);
+    softmax_role<FP16, QUANT>(p, sm, q_smem, kv_smem, tmem);
   } else if (warp == LOAD_WARP) {
-    load_role(p, maps, sm, q_smem, kv_smem);
+    load_role<FP16, QUANT>(p, maps, sm, q_smem, kv_smem);
   } else if (warp >= MMA_WARP) {
-    mma_role(p, sm, warp - MMA_WARP, smem_u32(q_smem), smem_u32(kv_smem), tmem, FP16 ? 0u : 1u);
+    mma_role<FP16, QUANT>(p, sm, warp - MMA_WARP, smem_u32(q_smem), smem_u32(kv_smem), tmem, FP16 ? 0u : 1u);
   } else if (warp == PLAN_WARP) {
     plan_role(p, sm, blockIdx.x, piece);
   }
@@ -1411,6 +1716,66 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 constexpr size_t SMEM_BYTES = (2 + STAGES) * TILE_BYTES + sizeof(Smem);
 static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
+template <bool FP16>
+constexpr size_t SMEM_BYTES8 = 2 * Kind<FP16, true>::q_tile + STAGES8<FP16> * TILE8_BYTES + sizeof(QuantSmem);
+static_assert(SMEM_BYTES8<false> <= 232448 && SMEM_BYTES8<true> <= 232448, "shared memory of one CTA");
+
+// The queries of a call in 8-bit parts, [part][token][head][128], and each row's
+// factor: a row is taken to [2^7, 2^8) by a power of two, and every part what is
+// left to the nearest e4m3 (4 significant bits).  Two parts are a bf16 number,
+// three an fp16 one, down to 2^-17 of the row's largest.  16 lanes a row.  Moves
+// 1.5 (bf16) or 2 times... bytes of the queries once.
+template <bool FP16>
+__global__ void __launch_bounds__(256) split_queries_kernel(AttentionParams p, uint8_t* parts, float* factors) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t i = blockIdx.x * 256ll + threadIdx.x, row = i >> 4, rows = (int64_t)p.t_total * p.hq;
+  const int c = (int)(i & 15) * 8;
+  if (row >= rows) return;  // 16 lanes alike
+  const int64_t tok = row / p.hq;
+  const int head = (int)(row % p.hq);
+  const uint4 raw = *reinterpret_cast<const uint4*>(p.q + tok * p.q_st + head * p.q_sh + c);
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  float x[8], top = 0.f;
+  bool finite = true;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 v = act_f2<FP16>(reinterpret_cast<const __nv_bfloat16*>(&w[k]));
+    x[2 * k] = v.x;
+    x[2 * k + 1] = v.y;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    top = fmaxf(top, fabsf(x[k]));
+    finite = finite && fabsf(x[k]) < CUDART_INF_F;
+  }
+  const unsigned group = 0xffffu << (threadIdx.x & 16);
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(group, top, d));
+  finite = __all_sync(group, finite);
+  const int e = max(-110, (__float_as_int(top) >> 23) - 127 - 7);  // of the row's power of two (0 and what is not finite: any)
+  const float down = __int_as_float((127 - (finite ? e : 0)) << 23);
+#pragma unroll
+  for (int part = 0; part < Q_PARTS<FP16>; ++part) {
+    uint32_t y[2];
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      float a = part == 0 ? x[k] * down : x[k], b = part == 0 ? x[k + 1] * down : x[k + 1];
+      uint16_t two;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(b), "f"(a));
+      uint32_t h;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+      const float2 taken = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      x[k] = a - taken.x;
+      x[k + 1] = b - taken.y;
+      if (!finite) two = 0x7f7f;
+      if (k & 2) y[k >> 2] |= (uint32_t)two << 16;
+      else y[k >> 2] = two;
+    }
+    *reinterpret_cast<uint2*>(parts + ((int64_t)part * rows + row) * D + c) = make_uint2(y[0], y[1]);
+  }
+  if (c == 0) factors[row] = p.scale * LOG2E * __int_as_float((127 + (finite ? e : 0)) << 23);
+}
 
 int sm_count() {
   static int counts[64] = {0};
@@ -1419,8 +1784,10 @@ int sm_count() {
   const bool have = once_per_device(done, [&](int d) {
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d) == cudaSuccess) counts[d] = n;
-    cudaFuncSetAttribute(attention_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
-    cudaFuncSetAttribute(attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    cudaFuncSetAttribute(attention_kernel<false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    cudaFuncSetAttribute(attention_kernel<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    cudaFuncSetAttribute(attention_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES8<false>);
+    cudaFuncSetAttribute(attention_kernel<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES8<true>);
   });
   if (!have || cudaGetDevice(&dev) != cudaSuccess || counts[dev] <= 0) {
     cudaGetLastError();  // no device here: size for a full GB300
@@ -1467,16 +1834,20 @@ bool encode_joined(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, bool
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
-
-size_t attention_workspace_bytes() {
-  return KDA_ATTENTION_ZEROED_BYTES + (size_t)sm_count() * 4 * ROWS * (sizeof(float2) + 32 * sizeof(float4));
+// Bytes: [n4, n3, n2, n1, 128], strides s4 .. s1; boxes of whole rows, b1 x b2 x b3 of them.
+bool encode8(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, int rank, const void* base, int64_t n1, int64_t s1, int64_t n2,
+             int64_t s2, int64_t n3, int64_t s3, int64_t n4, int64_t s4, uint32_t b1, uint32_t b2, uint32_t b3) {
+  const cuuint64_t dims[5] = {(cuuint64_t)D, (cuuint64_t)n1, (cuuint64_t)n2, (cuuint64_t)n3, (cuuint64_t)n4};
+  const cuuint64_t strides[4] = {(cuuint64_t)(n1 > 1 ? s1 : D), (cuuint64_t)(n2 > 1 ? s2 : D), (cuuint64_t)(n3 > 1 ? s3 : D),
+                                 (cuuint64_t)(n4 > 1 ? s4 : D)};
+  const cuuint32_t box[5] = {D, b1, b2, b3, 1}, step[5] = {1, 1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int launch_attention(const AttentionParams& a, bool fp16, void* workspace, cudaStream_t stream) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = map_encoder();
-  if (!enc) return -1;
-  Params p;
+// Work and workspace of a call, whatever the cache.
+void plan_call(Params& p, const AttentionParams& a, void* workspace) {
   p.a = a;
   p.group = a.hq / a.hkv;
   p.tile_tok = ROWS / p.group;
@@ -1492,6 +1863,34 @@ int launch_attention(const AttentionParams& a, bool fp16, void* workspace, cudaS
   p.counters = reinterpret_cast<unsigned*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + KDA_ATTENTION_ZEROED_BYTES);
   p.part_o = reinterpret_cast<float4*>(p.part_ml + (size_t)p.n_cta * 4 * ROWS);
+}
+
+void launch_kernel(void (*kernel)(const Params, const Maps), const Params& p, const Maps& maps, size_t smem, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(p.n_cta);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, p, maps);
+}
+
+}  // namespace
+
+size_t attention_workspace_bytes() {
+  return KDA_ATTENTION_ZEROED_BYTES + (size_t)sm_count() * 4 * ROWS * (sizeof(float2) + 32 * sizeof(float4));
+}
+
+int launch_attention(const AttentionParams& a, bool fp16, void* workspace, cudaStream_t stream) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = map_encoder();
+  if (!enc) return -1;
+  Params p = {};
+  plan_call(p, a, workspace);
+  const int page = 1 << a.page_shift;
   Maps maps;
   const int box = page < KT ? page : KT;
   // Joined copies where page and row group, or page and head, are one dimension
@@ -1512,19 +1911,51 @@ int launch_attention(const AttentionParams& a, bool fp16, void* workspace, cudaS
   if (!ok || !encode(enc, &maps.q, fp16, a.q, p.group, a.q_sh, a.hkv, a.q_sh * p.group, a.t_total, a.q_st, p.group, 1, p.tile_tok) ||
       !encode(enc, &maps.q1, fp16, a.q, p.group, a.q_sh, a.hkv, a.q_sh * p.group, a.t_total, a.q_st, p.group, 1, 1))
     return -1;
+  trace_begin("attention", stream);
+  launch_kernel(fp16 ? attention_kernel<true, false> : attention_kernel<false, false>, p, maps, SMEM_BYTES, stream);
+  trace_end(stream);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+size_t attention_quant_workspace_bytes(int t_total, int hq) {
+  return attention_workspace_bytes() + (size_t)t_total * hq * (3 * D + sizeof(float));
+}
+
+int launch_attention_quant(const AttentionParams& a, const KvQuantCache& c, bool fp16, void* workspace, cudaStream_t stream) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = map_encoder();
+  if (!enc) return -1;
+  Params p = {};
+  plan_call(p, a, workspace);
+  p.c = c;
+  const int page = 1 << a.page_shift, box = page < KT ? page : KT, parts = fp16 ? Q_PARTS<true> : Q_PARTS<false>;
+  p.group_bytes = 1024;
+  p.half_bytes = 16;  // a row is whole: not used
+  const int64_t rows = (int64_t)a.t_total * a.hq;
+  uint8_t* q_parts = static_cast<uint8_t*>(workspace) + attention_workspace_bytes();
+  float* factors = reinterpret_cast<float*>(q_parts + 3 * rows * D);
+  p.q_scale = factors;
+  Maps maps;
+  const int64_t head = D, kv_head = (int64_t)p.group * D, tok = (int64_t)a.hq * D;
+  if (!encode8(enc, &maps.k, 4, c.k, page, c.k_st, a.hkv, c.k_sh, a.n_pages, c.k_sp, 1, D, box, 1, 1) ||
+      !encode8(enc, &maps.v, 4, c.v, page, c.v_st, a.hkv, c.v_sh, a.n_pages, c.v_sp, 1, D, box, 1, 1) ||
+      !encode8(enc, &maps.q, 5, q_parts, p.group, head, a.hkv, kv_head, a.t_total, tok, parts, rows * D, p.group, 1, p.tile_tok) ||
+      !encode8(enc, &maps.q1, 5, q_parts, p.group, head, a.hkv, kv_head, a.t_total, tok, parts, rows * D, p.group, 1, 1))
+    return -1;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(p.n_cta);
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.gridDim = dim3((unsigned)((rows + 15) / 16));
+  cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  trace_begin("attention", stream);
-  if (fp16) cudaLaunchKernelEx(&cfg, attention_kernel<true>, p, maps);
-  else cudaLaunchKernelEx(&cfg, attention_kernel<false>, p, maps);
+  trace_begin("split_queries", stream);
+  cudaLaunchKernelEx(&cfg, fp16 ? split_queries_kernel<true> : split_queries_kernel<false>, a, q_parts, factors);
+  trace_end(stream);
+  trace_begin("attention_quant", stream);
+  if (fp16) launch_kernel(attention_kernel<true, true>, p, maps, SMEM_BYTES8<true>, stream);
+  else launch_kernel(attention_kernel<false, true>, p, maps, SMEM_BYTES8<false>, stream);
   trace_end(stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

@@ -202,95 +202,7 @@ __global__ void __launch_bounds__(256) kv_read_kernel(KvReadParams p) {
   to[1] = v[1];
 }
 
-__device__ __forceinline__ float checked_scale(float s, unsigned* err) {
-  if (s >= power(LEAST) && s <= power(MOST)) return s;
-  set_error(err, ERR_RANGE);
-  return s != s ? 1.f : fminf(fmaxf(s, power(LEAST)), power(MOST));
-}
-
-// Attention row by row: a warp a (token, head), four of the 128 dimensions a
-// lane, one pass over the keys with a running maximum.
-template <bool FP16>
-__global__ void __launch_bounds__(256) attention_quant_rows(AttentionParams p, KvQuantCache c) {
-  const int lane = threadIdx.x & 31, page = 1 << p.page_shift;
-  const int64_t row = blockIdx.x * 8ll + (threadIdx.x >> 5);
-  if (row >= (int64_t)p.t_total * p.hq) return;
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < p.n_req; i += 256)
-      if (p.cu_seqlens[i] < 0 || p.cu_seqlens[i + 1] < p.cu_seqlens[i] || p.cu_seqlens[i + 1] > p.t_total) set_error(p.err, ERR_INDEX);
-  const int tok = (int)(row / p.hq), head = (int)(row % p.hq), kvh = head / (p.hq / p.hkv);
-  int b = 0;
-  for (int hi = p.n_req - 1; b < hi;) {
-    const int mid = (b + hi + 1) >> 1;
-    if (p.cu_seqlens[mid] <= tok) b = mid;
-    else hi = mid - 1;
-  }
-  const int t0 = p.cu_seqlens[b], t1 = p.cu_seqlens[b + 1];
-  int kv = p.kv_lens[b];
-  if (kv < 0 || kv > p.table_cols * page) {
-    set_error(p.err, ERR_INDEX);
-    kv = max(0, min(kv, p.table_cols * page));
-  }
-  if (tok < t0 || tok >= t1 || t0 < 0 || t1 > p.t_total) return;
-  const int pos = kv - (t1 - tok);
-  float q[4], o[4] = {}, m = -INFINITY, l = 0.f, part = 0.f;  // part: of the last 128 keys, for the sum's precision
-  load_act4<FP16>(p.q + tok * p.q_st + head * p.q_sh + lane * 4, q);
-  const int hi = min(pos + 1, kv), lo = p.window ? max(0, pos + 1 - p.window) : 0;
-  const int32_t* table = p.table + b * p.table_stride;
-  for (int j = 0; j < hi; ++j) {
-    if (j < lo && j >= p.sinks) {
-      j = lo - 1;
-      continue;
-    }
-    const int pg = table[j >> p.page_shift], r = j & (page - 1);
-    if (pg < 0) continue;
-    if (pg >= p.n_pages) {
-      set_error(p.err, ERR_INDEX);
-      continue;
-    }
-    const int64_t at = (((int64_t)pg * p.hkv + kvh) << (p.page_shift - 4)) + r / QB;
-    const float ks = checked_scale(c.k_scale[at], p.err), vs = checked_scale(c.v_scale[at], p.err);
-    const uint32_t kw = *reinterpret_cast<const uint32_t*>(c.k + pg * c.k_sp + r * c.k_st + kvh * c.k_sh + lane * 4);
-    const uint32_t vw = *reinterpret_cast<const uint32_t*>(c.v + pg * c.v_sp + r * c.v_st + kvh * c.v_sh + lane * 4);
-    const float2 k0 = unpack_e4m3(kw), k1 = unpack_e4m3(kw >> 16), v0 = unpack_e4m3(vw), v1 = unpack_e4m3(vw >> 16);
-    float s = q[0] * k0.x + q[1] * k0.y + q[2] * k1.x + q[3] * k1.y;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= p.scale * ks;
-    const float top = fmaxf(m, s), corr = m == top ? 1.f : expf(m - top), w = s == -INFINITY ? 0.f : expf(s - top);
-    m = top;
-    l *= corr;
-    part = part * corr + w;
-    if ((j & 127) == 127) {
-      l += part;
-      part = 0.f;
-    }
-    o[0] = o[0] * corr + w * v0.x * vs;
-    o[1] = o[1] * corr + w * v0.y * vs;
-    o[2] = o[2] * corr + w * v1.x * vs;
-    o[3] = o[3] * corr + w * v1.y * vs;
-  }
-  l += part;
-  for (int j = 0; j < 4; ++j) o[j] = l == 0.f ? 0.f : o[j] / l;
-  *reinterpret_cast<uint2*>(p.out + row * D + lane * 4) = make_uint2(act_pack2<FP16>(o[0], o[1]), act_pack2<FP16>(o[2], o[3]));
-  if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
-}
-
 }  // namespace
-
-size_t attention_quant_workspace_bytes(int t_total, int hq) {
-  return attention_workspace_bytes() + (size_t)t_total * hq * 400;
-}
-
-int launch_attention_quant(const AttentionParams& a, const KvQuantCache& c, bool fp16, void* workspace, cudaStream_t stream) {
-  (void)workspace;
-  const unsigned blocks = (unsigned)(((int64_t)a.t_total * a.hq + 7) / 8);
-  trace_begin("attention_quant", stream);
-  if (fp16) attention_quant_rows<true><<<blocks, 256, 0, stream>>>(a, c);
-  else attention_quant_rows<false><<<blocks, 256, 0, stream>>>(a, c);
-  trace_end(stream);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
-}
 
 int launch_kv_quant_append(KvQuantAppendParams p, bool fp16, cudaStream_t stream) {
   // Blocks begin at every token of a decode step, at every 16th of a prompt: a

@@ -105,9 +105,9 @@ class Case:
         empty = np.isneginf(want_lse)
         assert np.array_equal(empty, np.isneginf(lse)) and not out[empty].any()
         if self.dtype == FP16:
-            # 8-bit numbers times scales reach past fp16: what rounds past its largest number, 65504, is infinite
-            with np.errstate(invalid="ignore"):
-                past = np.isinf(out) & (np.sign(out) == np.sign(want)) & (np.abs(want) + tol >= 65520)
+            # 8-bit numbers times scales reach past fp16: where want +- tol reaches a number that rounds past the
+            # largest, 65504, an infinity of that sign is within it
+            past = (np.isposinf(out) & (want + tol >= 65520)) | (np.isneginf(out) & (want - tol <= -65520))
             out, want = np.where(past, 0, out), np.where(past, 0, want)
             assert (np.abs(want) - tol < 65520).all()
         off = np.abs(out - want) - tol
