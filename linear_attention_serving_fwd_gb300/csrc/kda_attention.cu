@@ -126,17 +126,52 @@ struct Smem {
 // Over an 8-bit cache: tiles of 16 KB, and the scales of the key tiles in flight.
 // A query tile takes two places of 16 KB (bf16) or three (fp16).
 constexpr int TILE8_BYTES = KT * D, BLOCKS8 = KT / KDA_KV_BLOCK;
+constexpr int SCALES = 32;  // key tiles whose scales fit
+// When a tile's copy begins, the fifth before it is done with: its values' place is
+// in use again.
+constexpr int IN_FLIGHT = 5;
 template <bool FP16>
 constexpr int Q_PARTS = FP16 ? 3 : 2;
 template <bool FP16>
 constexpr int W_PARTS = FP16 ? 3 : 2;
 template <bool FP16>
 constexpr int STAGES8 = FP16 ? 7 : 9;
+// Narrow blocks: few rows (single tokens, short windows) over an 8-bit cache.  A
+// row a lane would leave all but one of the SM's four schedulers idle, because a
+// warp reaches 32 lanes of tensor memory only.  So the keys are the lanes here:
+// S^T = K Q^T (128 keys x rows) and O^T = V^T P^T (128 dimensions x rows), with the
+// parts of the queries and of the weights side by side in the columns, and a
+// thread has one key and all rows.  The four softmax warpgroups take the key tiles
+// in turn, each with a reference, sums and an O^T of its own, and their results
+// are joined in shared memory.
+constexpr int NARROW_ROWS = 16;
+// In the queries' buffer: those of two narrow blocks, so that the next one's are
+// there when it begins, and behind them the weights.
+constexpr int NARROW_ROW_BYTES = NARROW_ROWS * D;  // a part of the queries
+template <bool FP16>
+constexpr int NARROW_Q = Q_PARTS<FP16> * NARROW_ROW_BYTES;
+template <bool FP16>
+constexpr int NARROW_P = 2 * NARROW_Q<FP16>;
+__device__ __forceinline__ bool is_narrow(int n_tok, int group) { return n_tok * group <= NARROW_ROWS; }
+__device__ __forceinline__ int octets(int n_tok, int group) { return n_tok * group <= 8 ? 1 : 2; }  // of rows
+__host__ __device__ constexpr int columns(int octets, int parts) { return (octets * parts + 1) / 2 * 16; }
+template <bool FP16>
+constexpr int NARROW_W = columns(NARROW_ROWS / 8, W_PARTS<FP16>) * KT;  // bytes of a group's weights
 struct QuantSmem : Smem {
   uint64_t full8[9], empty8[9];
-  float4 k_scale[MASKS][BLOCKS8 / 4];    // of each block of 16 keys
-  float4 v_log[MASKS][BLOCKS8 / 4];      // the scale of its values in powers of two,
-  float4 v_inverse[MASKS][BLOCKS8 / 4];  // and what takes it out of their weights' sum
+  // The scales of the key tiles to come, by the planning warp: a scale comes from
+  // memory behind a page number, and where the copies keep memory busy that takes
+  // 3 us and more, several tiles.
+  uint64_t scales_full[SCALES];
+  float4 k_scale[SCALES][BLOCKS8 / 4];    // of each block of 16 keys
+  float4 v_log[SCALES][BLOCKS8 / 4];      // the scale of its values in powers of two,
+  float4 v_inverse[SCALES][BLOCKS8 / 4];  // and what takes it out of their weights' sum
+  int held[SCALES];                       // the blocks that some row may see, a bit each
+  int copied;                             // the key tile that the copies have come to
+  // narrow blocks, by group
+  uint64_t narrow_s[4], narrow_p[4], narrow_q_full[2], narrow_q_empty[2];
+  float4 narrow_factor[4][NARROW_ROWS / 4], narrow_m[4][NARROW_ROWS / 4];
+  float narrow_top[4][4 * NARROW_ROWS];  // of each warp's keys
 };
 // What differs between the two caches.
 template <bool FP16, bool QUANT>
@@ -178,8 +213,8 @@ struct Params {
 // engine's boxes are what limits, single tokens over 4096 cached take 343 us
 // instead of 472; with pages of 64 and more the two are alike.
 
-// hardware barriers: a pair of warps that share rows (stream, quarter), a stream's eight warps
-constexpr int PAIR_BAR = 1, STREAM_BAR = 9;
+// hardware barriers: a pair of warps that share rows (stream, quarter), a stream's eight warps, a warpgroup
+constexpr int PAIR_BAR = 1, STREAM_BAR = 9, GROUP_BAR = 11;
 
 // --- waits ---------------------------------------------------------------------
 // A wait that expires (bounded as all waits are) marks the CTA: its other waits
@@ -224,12 +259,16 @@ __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, Smem& sm, u
   if (!try_wait(bar, parity)) wait_slow(bar, parity, sm, err);
 }
 __device__ __forceinline__ bool is_dead(const Smem& sm) { return *(const volatile int*)&sm.dead != 0; }
-__device__ __forceinline__ void wait_joined(Smem& sm, int count, unsigned* err) {
+__device__ __forceinline__ void store_release(int* at, int x) {
+  asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(at)), "r"(x) : "memory");
+}
+// until a counter in shared memory has come to ``count``
+__device__ __forceinline__ void wait_count(const int* counter, int count, Smem& sm, unsigned* err) {
   Patience patience;
   for (uint32_t i = 0;; ++i) {
-    int joined;
-    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(joined) : "r"(smem_u32(&sm.joined)) : "memory");
-    if (joined >= count || is_dead(sm)) break;
+    int now;
+    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(now) : "r"(smem_u32(counter)) : "memory");
+    if (now >= count || is_dead(sm)) break;
     __nanosleep(64);
     if (i == WAIT_CAP || patience.over(sm)) {
       *(volatile int*)&sm.dead = 1;
@@ -305,10 +344,10 @@ __device__ __forceinline__ void mma_f8_ts(uint32_t d, uint32_t a, uint64_t b_des
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n"
       "}\n" ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
-// Instruction descriptor of kind::f8f6f4 with fp32 accumulation; B is e4m3.
-constexpr uint32_t E4M3 = 0, E5M2 = 1;
-__host__ __device__ constexpr uint32_t idesc_f8(uint32_t M, uint32_t N, uint32_t a) {
-  return (1u << 4) | (a << 7) | (E4M3 << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
+// Instruction descriptor of kind::f8f6f4 with fp32 accumulation.
+constexpr uint32_t E4M3 = 0, E5M2 = 1, A_MN_MAJOR = 1u << 15, B_MN_MAJOR = 1u << 16;
+__host__ __device__ constexpr uint32_t idesc_f8(uint32_t M, uint32_t N, uint32_t a, uint32_t b) {
+  return (1u << 4) | (a << 7) | (b << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 __device__ __forceinline__ void tma_load5(void* dst, const CUtensorMap* map, int c1, int c2, int c3, int c4, uint64_t* bar) {
   asm volatile(
@@ -645,8 +684,11 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
   const int lane = threadIdx.x & 31;
   unsigned* err = p.a.err;
   uint32_t fills = 0, tiles = 0, q_count = 0;
+  uint32_t place = 0, parity = 0;  // in 8 bits: of the next fill
   int merges = 0;       // joined results before this item
   int rows_before = 0;  // rows of the last block whose results are joined
+  bool narrow_before = false;
+  uint32_t narrow_count = 0;
   for (uint32_t items = 0;; ++items) {
     const uint32_t slot = items % RING;
     wait(&sm.ring_full[slot], (items / RING) & 1, sm, err);
@@ -673,16 +715,50 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
     // Queries: their buffer is free only when the item before is through, so the
     // first keys and values go ahead of them while there is room.
     bool asked = false;
+    const bool narrow = QUANT && is_narrow(it.n_tok, p.group);
+    auto queries_free = [&]() {
+      const bool last = mbar_test_wait(&sm.q_empty, (q_count & 1) ^ 1);
+      if constexpr (QUANT) {
+        if (narrow) return last && mbar_test_wait(&static_cast<QuantSmem&>(sm).narrow_q_empty[narrow_count & 1], ((narrow_count >> 1) & 1) ^ 1);
+      }
+      return last;
+    };
     auto queries = [&]() {
       asked = true;
       const bool two = it.n_tok > p.tile_tok;
       warp_wait(&sm.q_empty, (q_count & 1) ^ 1, sm, err);
+      if constexpr (QUANT) {
+        if (narrow) {
+          QuantSmem& qs = static_cast<QuantSmem&>(sm);
+          const uint32_t place = narrow_count & 1;
+          warp_wait(&qs.narrow_q_empty[place], ((narrow_count >> 1) & 1) ^ 1, sm, err);
+          if (rows_before > MERGE_ROWS) wait_count(&sm.joined, merges, sm, err);
+          if (__any_sync(0xffffffffu, is_dead(sm))) return;
+          ++merges;
+          rows_before = 0;
+          narrow_before = true;
+          ++narrow_count;
+          constexpr int PARTS = Q_PARTS<FP16>;
+          const int rows = 8 * octets(it.n_tok, p.group);
+          if (lane == 0) mbar_arrive_expect_tx(&qs.narrow_q_full[place], PARTS * it.n_tok * p.group * 128u);
+          __syncwarp();
+          for (int x = lane; x < PARTS * it.n_tok; x += 32) {
+            const int i = x / PARTS, part = x % PARTS;
+            tma_load5(q_smem + place * NARROW_Q<FP16> + (part * rows + i * p.group) * 128, &maps.q1, 0, it.kvh, it.tok + i, part,
+                      &qs.narrow_q_full[place]);
+          }
+          __syncwarp();
+          return;
+        }
+      }
       // Blocks of one tile join their results in the second tile's place, or in
       // all of the buffer: the last such joining has to be over if it is in the
       // way.  (A count and no barrier: this warp does not see every joining.)
-      if (two || rows_before > MERGE_ROWS) wait_joined(sm, merges, err);
+      // A narrow one's weights lie in the way as well.
+      if (two || rows_before > MERGE_ROWS || narrow_before) wait_count(&sm.joined, merges, sm, err);
       if (__any_sync(0xffffffffu, is_dead(sm))) return;
       const bool joins = !two && it.i1 - it.i0 > 1;
+      narrow_before = false;
       merges += joins;
       if (joins) rows_before = it.n_tok * p.group;
       ++q_count;
@@ -721,68 +797,43 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
       __syncwarp();
     };
     if constexpr (QUANT) {
-      // Four key tiles at once, a lane a block of 16 keys: its page, then its
-      // scales, are fetched while the four before are copied.
+      // A tile's keys and values in one step, a lane a box of either: at half the
+      // bytes a tile, two steps took longer than the memory (1600 cycles a tile
+      // against 700 with pages of 64).  The page number is not looked at before the step
+      // that needs it.
       QuantSmem& qs = static_cast<QuantSmem&>(sm);
-      auto key_of = [&](int i) { return list_tile(it, i) * KT + (lane & 7) * KDA_KV_BLOCK; };
-      auto block_page = [&](int i) {  // i: the four's first; -1 for a block that no row sees
-        i += lane >> 3;
-        if (i >= it.i1) return -1;
-        const int key = key_of(i);
-        if (!((key < it.hi && key + KDA_KV_BLOCK > it.lo) || key < it.sink_hi)) return -1;
-        const int pg = table[key >> p.a.page_shift];
-        if (pg >= p.a.n_pages) set_error(err, ERR_INDEX);
-        return pg < 0 || pg >= p.a.n_pages ? -1 : pg;
+      const bool values = lane >= p.boxes, copies = lane < 2 * p.boxes;
+      const int my_box = values ? lane - p.boxes : lane;
+      const CUtensorMap* map = values ? &maps.v : &maps.k;
+      unsigned char* to = kv_smem + my_box * box * 128;
+      auto entry = [&](int i) {  // of the table; -1 for a box that no row sees
+        if (!copies || i >= it.i1) return -1;
+        const int key = list_tile(it, i) * KT + my_box * box;
+        return (key < it.hi && key + box > it.lo) || key < it.sink_hi ? table[key >> p.a.page_shift] : -1;
       };
-      auto block_scales = [&](int i, int pg) {
-        if (pg < 0) return make_float2(1.f, 1.f);
-        const int64_t at = (((int64_t)pg * p.a.hkv + it.kvh) << (p.a.page_shift - 4)) +
-                           ((key_of(i + (lane >> 3)) & (page - 1)) / KDA_KV_BLOCK);
-        return make_float2(p.c.k_scale[at], p.c.v_scale[at]);
-      };
-      int pages = block_page(it.i0), pages_next = -1;
-      float2 scales = make_float2(0.f, 0.f), scales_next = scales;
-      for (int i = it.i0; i < it.i1; ++i, ++tiles) {
-        const int sub = (i - it.i0) & 3;
-        if (sub == 0 && i > it.i0) {
-          pages = pages_next;
-          scales = scales_next;
+      int next = entry(it.i0);
+      for (int i = it.i0; i < it.i1; ++i, ++tiles, fills += 2) {
+        const int now = next;
+        next = entry(i + 1);
+        if (!asked && __any_sync(0xffffffffu, queries_free() || !mbar_test_wait(K::empty(sm, place), parity ^ 1))) queries();
+        const uint32_t second = place + 1 == K::stages ? 0 : place + 1, second_parity = second == 0 ? parity ^ 1 : parity;
+        if (!__all_sync(0xffffffffu, wait_or_stop(K::empty(sm, place), parity ^ 1, sm, err) &&
+                                         wait_or_stop(K::empty(sm, second), second_parity ^ 1, sm, err)))
+          goto out;
+        if (lane == 0) {
+          store_release(&qs.copied, (int)tiles);
+          mbar_arrive_expect_tx(K::full(sm, place), K::tile);
+          mbar_arrive_expect_tx(K::full(sm, second), K::tile);
         }
-        // the page of a box of 16 to 128 keys, wherever one of its blocks is seen
-        int box_page = pages;
-        for (int d = 1; d < 8 / p.boxes; d <<= 1) box_page = max(box_page, __shfl_xor_sync(0xffffffffu, box_page, d));
-        const int c_page = __shfl_sync(0xffffffffu, box_page < 0 ? p.a.n_pages : box_page, (sub * 8 + lane * (8 / p.boxes)) & 31);
-        const unsigned held = __ballot_sync(0xffffffffu, pages >= 0) >> (sub * 8) & 0xff;
-        const int row = (list_tile(it, i) * KT) & (page - 1) & ~(box - 1);
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv, ++fills) {
-          const uint32_t st = fills % K::stages;
-          const uint32_t parity = ((fills / K::stages) & 1) ^ 1;
-          if (!asked && __any_sync(0xffffffffu, mbar_test_wait(&sm.q_empty, (q_count & 1) ^ 1) ||
-                                                    !mbar_test_wait(K::empty(sm, st), parity)))
-            queries();
-          if (!__all_sync(0xffffffffu, wait_or_stop(K::empty(sm, st), parity, sm, err))) goto out;
-          // the copy's bytes are announced after it: the arrival that ends the phase comes with them
-          if (lane < p.boxes)
-            tma_load4(kv_smem + st * K::tile + lane * box * 128, kv == 0 ? &maps.k : &maps.v, 0, row, it.kvh, c_page, K::full(sm, st));
-          if (kv == 0) {
-            if (i == it.i0) scales = block_scales(i, pages);
-            if (lane >> 3 == sub) {
-              const float ks = in_range(scales.x), vs = in_range(scales.y);
-              if (ks != scales.x || vs != scales.y) set_error(err, ERR_RANGE);
-              const int place = tiles % MASKS, b = lane & 7;
-              reinterpret_cast<float*>(qs.k_scale[place])[b] = ks;
-              reinterpret_cast<float*>(qs.v_log[place])[b] = log2f(vs);
-              reinterpret_cast<float*>(qs.v_inverse[place])[b] = 1.f / vs;
-            }
-            if (lane == 0) *(volatile int*)&sm.page_mask[tiles % MASKS] = (int)held;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(K::full(sm, st), K::tile);
-          __syncwarp();
+        if (now >= p.a.n_pages) set_error(err, ERR_INDEX);
+        __syncwarp();
+        if (copies) {
+          const int row = (list_tile(it, i) * KT) & (page - 1) & ~(box - 1);
+          const uint32_t st = values ? second : place;
+          tma_load4(to + st * K::tile, map, 0, row, it.kvh, now < 0 || now > p.a.n_pages ? p.a.n_pages : now, K::full(sm, st));
         }
-        if (sub == 0) pages_next = block_page(i + 4);
-        if (sub == 2) scales_next = block_scales(i + 2, pages_next);
+        place = second + 1 == K::stages ? 0 : second + 1;
+        parity = place == 0 ? second_parity ^ 1 : second_parity;
       }
       if (!asked) queries();
       continue;
@@ -795,15 +846,13 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
       pg = page_of(i + 1);
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++fills) {
-        const uint32_t st = fills % STAGES;
-        const uint32_t parity = ((fills / STAGES) & 1) ^ 1;
-        if (!asked && __any_sync(0xffffffffu, mbar_test_wait(&sm.q_empty, (q_count & 1) ^ 1) ||
-                                                  !mbar_test_wait(&sm.kv_empty[st], parity)))
-          queries();
-        if (!__all_sync(0xffffffffu, wait_or_stop(&sm.kv_empty[st], parity, sm, err))) goto out;
+        const uint32_t st = fills % K::stages;
+        const uint32_t parity = ((fills / K::stages) & 1) ^ 1;
+        if (!asked && __any_sync(0xffffffffu, queries_free() || !mbar_test_wait(K::empty(sm, st), parity))) queries();
+        if (!__all_sync(0xffffffffu, wait_or_stop(K::empty(sm, st), parity, sm, err))) goto out;
         if (lane == 0) {
           if (kv == 0) *(volatile int*)&sm.page_mask[tiles % MASKS] = (int)held;
-          mbar_arrive_expect_tx(&sm.kv_full[st], TILE_BYTES);
+          mbar_arrive_expect_tx(K::full(sm, st), K::tile);
         }
         __syncwarp();
         if (p.joined) {  // a lane a box
@@ -823,6 +872,10 @@ out:
     for (uint32_t f = fills > K::stages ? fills - K::stages : 0; f < fills; ++f)
       mbar_wait_bounded(K::full(sm, f % K::stages), (f / K::stages) & 1, err);
     if (q_count > 0) mbar_wait_bounded(&sm.q_full, (q_count - 1) & 1, err);
+    if constexpr (QUANT) {
+      for (uint32_t c = narrow_count > 2 ? narrow_count - 2 : 0; c < narrow_count; ++c)
+        mbar_wait_bounded(&static_cast<QuantSmem&>(sm).narrow_q_full[c & 1], (c >> 1) & 1, err);
+    }
   }
 }
 
@@ -861,11 +914,13 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
   using K = Kind<FP16, QUANT>;
   using Stage = Stage<K::stages>;
   unsigned* err = p.a.err;
-  const uint32_t id_qk = QUANT ? idesc_f8(ROWS, KT, E4M3) : tc::idesc_f16(ROWS, KT, bf16);
-  const uint32_t id_pv = (QUANT ? idesc_f8(ROWS, D, E5M2) : tc::idesc_f16(ROWS, D, bf16)) | (1u << 16);
+  const uint32_t id_qk = QUANT ? idesc_f8(ROWS, KT, E4M3, E4M3) : tc::idesc_f16(ROWS, KT, bf16);
+  const uint32_t id_pv = (QUANT ? idesc_f8(ROWS, D, E5M2, E4M3) : tc::idesc_f16(ROWS, D, bf16)) | B_MN_MAJOR;
   const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * 128;
   Stage next;  // of list index i0 of the next item
   uint32_t q_parity = 0, p_parity = 0, o_parity = 1;
+  uint32_t narrow_parity = 0;  // of the two warpgroups' weights, a bit each
+  uint32_t narrow_blocks = 0;
   const uint64_t k_desc = smem_desc_rows(kv_addr, p.group_bytes, p.half_bytes, false);
   const uint64_t v_desc = smem_desc_rows(kv_addr, p.group_bytes, p.half_bytes, true);
   const uint32_t k_half = (uint32_t)p.half_bytes >> 4, v_step = (uint32_t)p.group_bytes >> 3;  // 16 keys: two groups
@@ -897,9 +952,100 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
     if (it.b < 0) break;
     if (it.i1 == it.i0) continue;
     const bool two = it.n_tok > p.tile_tok;
-    await(&sm.q_full, q_parity);
-    q_parity ^= 1;
+    const bool narrow = QUANT && is_narrow(it.n_tok, p.group);
+    if (!narrow) {
+      await(&sm.q_full, q_parity);
+      q_parity ^= 1;
+    }
     const uint64_t qd = tc::smem_desc_sw128(q_addr + (two ? s * K::q_tile : 0));
+    if constexpr (QUANT) {
+      if (narrow) {
+        // This stream's key tiles go to its two warpgroups in turn.  Scores are
+        // issued up to two tiles ahead of the weights' product, whichever is ready.
+        QuantSmem& qs = static_cast<QuantSmem&>(sm);
+        const int oct = octets(it.n_tok, p.group), n_tiles = it.i1 - it.i0;
+        const int mine = (n_tiles - odd + 1) >> 1;
+        const uint32_t n_qk = columns(oct, Q_PARTS<FP16>), n_pv = columns(oct, W_PARTS<FP16>);
+        const uint32_t id_s = idesc_f8(KT, n_qk, E4M3, E4M3), id_o = idesc_f8(D, n_pv, E4M3, E5M2) | A_MN_MAJOR | B_MN_MAJOR;
+        const uint32_t place = narrow_blocks & 1;
+        await(&qs.narrow_q_full[place], (narrow_blocks >> 1) & 1);
+        ++narrow_blocks;
+        const uint64_t q_desc = tc::smem_desc_sw128(q_addr + place * NARROW_Q<FP16>);
+        const uint64_t w_desc = tc::smem_desc(q_addr + NARROW_P<FP16> + s * 2 * NARROW_W<FP16>, 128, 2048);
+        int tile = 0, scored_n = 0, done = 0;  // key tiles passed, of them this stream's, of those finished
+        Stage at = next, v_at = next;
+        v_at.skip(1 + 2 * odd);
+        Patience patience;
+        while (done < mine || tile < n_tiles) {
+          bool moved = false;
+          if (done < scored_n && __all_sync(0xffffffffu, mbar_test_wait(&qs.narrow_p[s * 2 + (done & 1)], narrow_parity >> (done & 1) & 1))) {
+            const int g = done & 1;
+            narrow_parity ^= 1u << g;
+            if (done == 0) {
+              await(&sm.o_free[s], o_parity);
+              o_parity ^= 1;
+            }
+            await(K::full(sm, v_at.at), v_at.parity);
+            tc::fence_after_sync();
+            if (elect_one()) {
+              const uint64_t vd = v_desc + v_at.at * (K::tile >> 4);
+#pragma unroll
+              for (int j = 0; j < KT / 32; ++j)
+                mma_f8(t_o + g * 64, vd + j * 2 * v_step, w_desc + g * (NARROW_W<FP16> >> 4) + j * (512 >> 4), id_o,
+                       (j > 0 || done > 1) ? 1u : 0u);
+              tc::mma_commit(K::empty(sm, v_at.at));
+            }
+            __syncwarp();
+            v_at.skip(4);
+            ++done;
+            moved = true;
+          }
+          if (tile < n_tiles && scored_n < done + 2 && __all_sync(0xffffffffu, mbar_test_wait(K::full(sm, at.at), at.parity))) {
+            Stage v = at;
+            v.skip(1);
+            if ((tile & 1) == odd) {
+              tc::fence_after_sync();
+              const int g = scored_n & 1;
+              if (elect_one()) {
+                const uint64_t kd = k_desc + at.at * (K::tile >> 4);
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) mma_f8(t_s + g * 64, kd + j * 2, q_desc + j * 2, id_s, j > 0 ? 1u : 0u);
+                tc::mma_commit(&qs.narrow_s[s * 2 + g]);
+                tc::mma_commit(K::empty(sm, at.at));
+                if (scored_n + 1 == mine) tc::mma_commit(&qs.narrow_q_empty[place]);
+              }
+              ++scored_n;
+            } else {
+              // the other stream's: see its fills
+              await(K::full(sm, v.at), v.parity);
+              if (elect_one()) {
+                mbar_arrive(K::empty(sm, at.at));
+                mbar_arrive(K::empty(sm, v.at));
+              }
+            }
+            __syncwarp();
+            at.skip(2);
+            ++tile;
+            moved = true;
+          }
+          if (moved) {
+            patience.t0 = 0;
+          } else if (__any_sync(0xffffffffu, is_dead(sm) || patience.over(sm))) {
+            *(volatile int*)&sm.dead = 1;
+            set_error(err, ERR_TIMEOUT);
+            break;
+          }
+        }
+        if (elect_one()) {
+          if (mine > 0) tc::mma_commit(&sm.o_full[s]);
+          else mbar_arrive(&qs.narrow_q_empty[place]);
+        }
+        __syncwarp();
+        next.skip((2 * n_tiles) % K::stages);
+        next.parity ^= (2 * n_tiles / K::stages) & 1;
+        continue;
+      }
+    }
     int last = it.i1 - 1;  // this stream's last tile
     if (two) {
       while (last >= it.i0 && !active(act, last)) --last;
@@ -1016,12 +1162,63 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
 }
 
 // --- the planning warp -----------------------------------------------------------------
+// The scales of an item's key tiles, four tiles at once, a lane a block of 16 keys;
+// the pages of the next four and then their scales are under way meanwhile.
+// ``tiles``: key tiles before the item's.
+__device__ __forceinline__ void fetch_scales(const Params& p, QuantSmem& sm, const Item& it, uint32_t tiles) {
+  const int lane = threadIdx.x & 31, b = lane & 7;
+  unsigned* err = p.a.err;
+  const int32_t* table = p.a.table + (int64_t)it.b * p.a.table_stride;
+  auto page_of = [&](int i) {  // -1 for a block that no row sees
+    if (i >= it.i1) return -1;
+    const int key = list_tile(it, i) * KT + b * KDA_KV_BLOCK;
+    if (!((key < it.hi && key + KDA_KV_BLOCK > it.lo) || key < it.sink_hi)) return -1;
+    const int pg = table[key >> p.a.page_shift];
+    return pg >= p.a.n_pages ? -1 : pg;  // reported by the copies
+  };
+  auto scales_of = [&](int i, int pg) {
+    if (pg < 0) return make_float2(1.f, 1.f);
+    const int row = (list_tile(it, i) * KT + b * KDA_KV_BLOCK) & ((1 << p.a.page_shift) - 1);
+    const int64_t at = (((int64_t)pg * p.a.hkv + it.kvh) << (p.a.page_shift - 4)) + row / KDA_KV_BLOCK;
+    return make_float2(p.c.k_scale[at], p.c.v_scale[at]);
+  };
+  // pages of the four tiles from i on, of the next four and of those after; scales of the first and second
+  int i = it.i0 + (lane >> 3);
+  int pg[3] = {page_of(i), page_of(i + 4), page_of(i + 8)};
+  float2 x[2] = {scales_of(i, pg[0]), scales_of(i + 4, pg[1])};
+  for (int from = it.i0; from < it.i1; from += 4, i += 4) {
+    const int n = min(4, it.i1 - from);  // tiles of these four
+    const uint32_t first = tiles + (from - it.i0);
+    const float2 after = scales_of(i + 8, pg[2]);
+    const int pages = pg[0];
+    pg[0] = pg[1];
+    pg[1] = pg[2];
+    pg[2] = page_of(i + 12);
+    wait_count(&sm.copied, (int)(first + n - 1) - (SCALES - IN_FLIGHT), sm, err);
+    const float ks = in_range(x[0].x), vs = in_range(x[0].y);
+    if (ks != x[0].x || vs != x[0].y) set_error(err, ERR_RANGE);
+    const unsigned held = __ballot_sync(0xffffffffu, pages >= 0);
+    if ((lane >> 3) < n) {
+      const uint32_t place = (first + (lane >> 3)) % SCALES;
+      reinterpret_cast<float*>(sm.k_scale[place])[b] = ks;
+      reinterpret_cast<float*>(sm.v_log[place])[b] = log2f(vs);
+      reinterpret_cast<float*>(sm.v_inverse[place])[b] = 1.f / vs;
+      if (b == 0) sm.held[place] = (held >> (lane & 24)) & 0xff;
+    }
+    __syncwarp();
+    if (lane < n) mbar_arrive(&sm.scales_full[(first + lane) % SCALES]);
+    x[0] = x[1];
+    x[1] = after;
+  }
+}
+
+template <bool QUANT>
 __device__ __forceinline__ void plan_role(const Params& p, Smem& sm, int cta, long long piece) {
   const int lane = threadIdx.x & 31;
   unsigned* err = p.a.err;
   const long long total = sm.total, all = total * p.a.hkv;
   const long long u0 = cta * piece, u1 = min(all, u0 + piece);
-  uint32_t items = 0;
+  uint32_t items = 0, key_tiles = 0;
   int turn = 0;
   bool ok = true;
   auto post = [&](const Item& it) {
@@ -1065,6 +1262,10 @@ __device__ __forceinline__ void plan_role(const Params& p, Smem& sm, int cta, lo
         tile_range(p, it, 0);
         tile_range(p, it, 1);
         post(it);
+        if constexpr (QUANT) {
+          if (ok) fetch_scales(p, static_cast<QuantSmem&>(sm), it, key_tiles);
+          key_tiles += it.i1 - it.i0;
+        }
       };
       for (int k0 = 0; ok && k0 < blocks && at < u1; k0 += 32) {
         // 32 blocks at once, unless the request has but one
@@ -1248,6 +1449,23 @@ __device__ __forceinline__ void join_rows(const Params& p, Smem& sm, int s, cons
   }
 }
 
+// Counts a tile's part, whose results the stream has stored; true with the last one.
+__device__ __forceinline__ bool last_part(const Params& p, Smem& sm, int s, const Item& it, int tile, int bar) {
+  named_bar_sync(bar, 256);
+  if ((threadIdx.x & 255) == 0) {
+    __threadfence();  // for all of the stream's stores, which the barrier put before it
+    unsigned* counter = &p.counters[it.first * 2 + tile];
+    const bool last = atomicAdd(counter, 1u) + 1 == (unsigned)it.parts;
+    if (last) {
+      *counter = 0;
+      __threadfence();
+    }
+    sm.last[s] = last;
+  }
+  named_bar_sync(bar, 256);
+  return sm.last[s];
+}
+
 // Joins a tile's parts, by the stream's warpgroups that finished the last of
 // them.  Many rows: a lane takes a quarter of its row, so that each part's loads
 // are many.  Few: a sixteenth, so that all warps have some, and several parts'
@@ -1266,9 +1484,325 @@ __device__ __forceinline__ void join_parts(const Params& p, Smem& sm, int s, con
   if (bad) mend_rows<FP16, QUANT>(p, sm, s, warp >> 2, quarter, PAIR_BAR + s * 4 + quarter, it, tile, bad);
 }
 
+__device__ __forceinline__ void tmem_ld8_async(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_regs8(uint32_t (&r)[8]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
+}
+
+// A narrow block by one of the stream's warpgroups: thread r has key r of its tiles
+// and dimension r of the results, which go to shared memory; the leading stream
+// joins them.  The counters are those of the softmax role.
+template <bool FP16, int OCT>
+__device__ __forceinline__ void narrow_block(const Params& p, QuantSmem& sm, const Item& it, unsigned char* q_smem,
+                                          unsigned char* kv_smem, uint32_t tmem, uint32_t tiles, uint32_t fills,
+                                          uint32_t s_count, uint32_t o_count, uint32_t merges) {
+  using K = Kind<FP16, true>;
+  constexpr int RP = OCT * 8;
+  unsigned* err = p.a.err;
+  const int s = threadIdx.x >> 8, half = (threadIdx.x >> 7) & 1, g = s * 2 + half;
+  const int r = threadIdx.x & 127, lane = r & 31, quarter = r >> 5, bar = GROUP_BAR + g;
+  const uint32_t lane_base = tmem + ((uint32_t)(r & 96) << 16);
+  const uint32_t t_s = lane_base + s * 128 + half * 64, t_o = lane_base + 256 + s * 128 + half * 64;
+  const int i0 = it.i0, i1 = it.i1, kv = it.kv, odd = it.lead ^ s, n_rows = it.n_tok * p.group;
+  float* factor = reinterpret_cast<float*>(sm.narrow_factor[g]);
+  float* ref = reinterpret_cast<float*>(sm.narrow_m[g]);  // the rows' references, in powers of two
+  unsigned char* weights = q_smem + NARROW_P<FP16> + g * NARROW_W<FP16> + r * 16;
+  // what row ``lane`` sees
+  const int pos = it.pos + (lane < n_rows ? lane / p.group : 0);
+  const int row_hi = max(0, min(pos + 1, kv)), row_lo = p.a.window ? max(0, pos + 1 - p.a.window) : 0;
+  const int row_sink = min(p.a.sinks, row_hi);
+  const bool real = lane < n_rows;
+  const int hi_min = __reduce_min_sync(0xffffffffu, real ? row_hi : 0x7fffffff);
+  const int lo_max = __reduce_max_sync(0xffffffffu, real ? row_lo : 0);
+  const int sink_min = __reduce_min_sync(0xffffffffu, real ? row_sink : 0x7fffffff);
+  if (r < RP) {
+    factor[r] = real ? p.q_scale[(int64_t)(it.tok + r / p.group) * p.a.hq + it.kvh * p.group + r % p.group] : 1.f;
+    ref[r] = -CUDART_INF_F;
+  }
+  named_bar_sync(bar, 128);
+  float l[RP];
+#pragma unroll
+  for (int k = 0; k < RP; ++k) l[k] = 0.f;
+  bool stepped = false;
+#pragma unroll 1
+  for (int i = i0 + odd + 2 * half; i < i1; i += 4) {
+    const int first_key = list_tile(it, i) * KT, key = first_key + r, place = (tiles + i - i0) % SCALES;
+    // what the key brings, before the scores are there
+    warp_wait(&sm.scales_full[place], ((tiles + i - i0) / SCALES) & 1, sm, err);
+    const float ks = reinterpret_cast<const float*>(sm.k_scale[place])[r >> 4];
+    const float lv = reinterpret_cast<const float*>(sm.v_log[place])[r >> 4];
+    const float iv = reinterpret_cast<const float*>(sm.v_inverse[place])[r >> 4];
+    const int held = sm.held[place];
+    const bool clear = held == (1 << BLOCKS8) - 1 && first_key + KT <= hi_min && (first_key >= lo_max || first_key + KT <= sink_min);
+    // Weights are 2^(a score + b).  Of 8 rows a and b wait in registers, of 16 (no
+    // room) they are formed where they are used.
+    bool begun = true;  // every row has a reference
+    auto terms = [&](int k, float2& a, float2& b) {
+      const float2 f = *reinterpret_cast<const float2*>(factor + k), m = *reinterpret_cast<const float2*>(ref + k);
+      a = make_float2(row_factor(f.x, ks), row_factor(f.y, ks));
+      b = make_float2(K::weight_exp - (m.x == -CUDART_INF_F ? 0.f : m.x) + lv,
+                      K::weight_exp - (m.y == -CUDART_INF_F ? 0.f : m.y) + lv);
+      begun = begun && (k >= n_rows || m.x != -CUDART_INF_F) && (k + 1 >= n_rows || m.y != -CUDART_INF_F);
+    };
+    float2 a8[4], b8[4];
+    if constexpr (OCT == 1) {
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) terms(k, a8[k / 2], b8[k / 2]);
+    }
+    warp_wait(&sm.narrow_s[g], s_count & 1, sm, err);
+    ++s_count;
+    tc::fence_after_sync();
+    float x[RP];
+#pragma unroll
+    for (int o = 0; o < OCT; ++o) {
+      uint32_t y[Q_PARTS<FP16>][8];
+#pragma unroll
+      for (int part = 0; part < Q_PARTS<FP16>; ++part) tmem_ld8_async(t_s + part * RP + o * 8, y[part]);
+      tc::tmem_wait_ld();
+#pragma unroll
+      for (int part = 0; part < Q_PARTS<FP16>; ++part) tmem_regs8(y[part]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x[o * 8 + k] = __uint_as_float(y[0][k]);
+#pragma unroll
+        for (int part = 1; part < Q_PARTS<FP16>; ++part) x[o * 8 + k] += __uint_as_float(y[part][k]);
+      }
+    }
+    if (!clear) {
+      const bool there = (held >> (r >> 4)) & 1;
+#pragma unroll
+      for (int k = 0; k < RP; ++k) {
+        const int hi = __shfl_sync(0xffffffffu, row_hi, k), lo = __shfl_sync(0xffffffffu, row_lo, k);
+        const int sink = __shfl_sync(0xffffffffu, row_sink, k);
+        if (!there || key >= hi || (key < lo && key >= sink)) x[k] = -CUDART_INF_F;
+      }
+      if (first_key + KT > kv) {
+        // the rows past the cached tokens hold whatever was there
+        const uint32_t f = fills + 2 * (i - i0) + 1;
+        wait(K::full(sm, f % K::stages), (f / K::stages) & 1, sm, err);
+        if (key >= kv) {
+          int4* v = reinterpret_cast<int4*>(kv_smem + (f % K::stages) * K::tile + r * 128);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[c] = make_int4(0, 0, 0, 0);
+        }
+        __syncwarp();
+      }
+    }
+    uint32_t w[RP / 2];
+    float sum[RP];
+    auto weigh = [&]() {
+      bool fits = true;
+#pragma unroll
+      for (int k = 0; k < RP; k += 2) {
+        float2 a, b;
+        if constexpr (OCT == 1) {
+          a = a8[k / 2];
+          b = b8[k / 2];
+        } else {
+          terms(k, a, b);
+        }
+        const float2 e = ffma2(make_float2(x[k], x[k + 1]), a, b);
+        // rows past the block hold anything: no weight
+        sum[k] = k < n_rows ? ex2(e.x) : 0.f;
+        sum[k + 1] = k + 1 < n_rows ? ex2(e.y) : 0.f;
+        fits = fits && sum[k] <= LIMIT && sum[k + 1] <= LIMIT;
+        w[k / 2] = act_pack2<true>(sum[k], sum[k + 1]);
+      }
+      return fits;
+    };
+    const bool fits = weigh();
+    if (named_bar_or(bar, 128, !begun || !fits)) {
+      // the reference moves to each row's largest score so far
+      float* share = sm.narrow_top[g];
+#pragma unroll
+      for (int k = 0; k < RP; ++k) {
+        const float y = fmaf(x[k], row_factor(factor[k], ks), lv);
+        // in the order of whole numbers; NaN has no say
+        const int bits = __float_as_int(y == y ? y : -CUDART_INF_F), top = __reduce_max_sync(0xffffffffu, bits ^ ((bits >> 31) & 0x7fffffff));
+        if (lane == 0) share[quarter * NARROW_ROWS + k] = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
+      }
+      named_bar_sync(bar, 128);
+      float corr[RP], m_mine = -CUDART_INF_F;
+#pragma unroll
+      for (int k = 0; k < RP; ++k) {
+        const float m = ref[k];
+        float m_new = m;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) m_new = fmaxf(m_new, share[q * NARROW_ROWS + k]);
+        corr[k] = m_new == -CUDART_INF_F ? 1.f : ex2(m - m_new);
+        l[k] *= corr[k];
+        if (r == k) m_mine = m_new;
+      }
+      if (stepped) {
+#pragma unroll 1
+        for (int part = 0; part < W_PARTS<FP16>; ++part) {
+#pragma unroll
+          for (int o = 0; o < OCT; ++o) {
+            uint32_t y[8];
+            tmem_ld8_async(t_o + part * RP + o * 8, y);
+            tc::tmem_wait_ld();
+            tmem_regs8(y);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * corr[o * 8 + k]);
+            tmem_st8(t_o + part * RP + o * 8, y);
+          }
+        }
+        tmem_wait_st();
+      }
+      named_bar_sync(bar, 128);  // all have read the references
+      if (r < RP) ref[r] = m_mine;
+      named_bar_sync(bar, 128);
+      if constexpr (OCT == 1) {
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) terms(k, a8[k / 2], b8[k / 2]);
+      }
+      weigh();
+    }
+#pragma unroll
+    for (int k = 0; k < RP; ++k) l[k] += sum[k] * iv;
+    // key r's weights of all rows, part after part: 16 bytes a line, 128 lines to 16 columns
+#pragma unroll
+    for (int part = 0; part < W_PARTS<FP16>; ++part) {
+#pragma unroll
+      for (int o = 0; o < OCT; ++o) {
+        uint32_t y[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t t[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t& h = w[o * 4 + j * 2 + k];
+            t[k] = h + 0x00800080u;
+            if (part + 1 < W_PARTS<FP16>) {
+              const uint32_t top = t[k] & 0xff00ff00u;
+              const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&top));
+              h = *reinterpret_cast<const uint32_t*>(&rest);
+            }
+          }
+          y[j] = __byte_perm(t[0], t[1], 0x7531);
+        }
+        const int column = part * RP + o * 8;
+        *reinterpret_cast<uint2*>(weights + (column >> 4) * 2048 + (column & 8)) = make_uint2(y[0], y[1]);
+      }
+    }
+    fence_proxy_async_smem();
+    stepped = true;
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.narrow_p[g]);
+  }
+  // results: O^T and the sums of each warp's keys
+  float* merge = reinterpret_cast<float*>(q_smem + K::q_tile) + g * NARROW_ROWS * D;
+  float* share = sm.share[s][half];
+  warp_wait(&sm.merge_free, (merges & 1) ^ 1, sm, err);  // the last joined results have been read
+  if (i0 + odd < i1) {
+    warp_wait(&sm.o_full[s], o_count & 1, sm, err);
+    tc::fence_after_sync();
+    if (stepped) {
+#pragma unroll
+      for (int o = 0; o < OCT; ++o) {
+        uint32_t y[W_PARTS<FP16>][8];
+#pragma unroll
+        for (int part = 0; part < W_PARTS<FP16>; ++part) tmem_ld8_async(t_o + part * RP + o * 8, y[part]);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int part = 0; part < W_PARTS<FP16>; ++part) tmem_regs8(y[part]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float sum = __uint_as_float(y[0][k]);
+#pragma unroll
+          for (int part = 1; part < W_PARTS<FP16>; ++part) sum += __uint_as_float(y[part][k]);
+          merge[(o * 8 + k) * D + r] = sum;
+        }
+      }
+    }
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.o_free[s]);
+  }
+#pragma unroll
+  for (int k = 0; k < RP; ++k) {
+    const float sum = warp_sum(l[k]);
+    if (lane == 0) share[quarter * NARROW_ROWS + k] = sum;
+  }
+  if (r < RP) share[4 * NARROW_ROWS + r] = ref[r];
+  __syncwarp();
+}
+
+// The leading stream's eight warps join the four groups' results of a narrow block.
+template <bool FP16>
+__device__ __forceinline__ void join_groups(const Params& p, QuantSmem& sm, const Item& it, unsigned char* q_smem) {
+  using K = Kind<FP16, true>;
+  const int s = threadIdx.x >> 8, t = threadIdx.x & 255, n_rows = it.n_tok * p.group;
+  const float* merge = reinterpret_cast<const float*>(q_smem + K::q_tile);
+  if (t < 4) sm.poisoned[s][0][t] = 0;
+  named_bar_sync(STREAM_BAR + s, 256);
+  const int c = t & 31;  // 4 dimensions
+#pragma unroll 1
+  for (int row = t >> 5; row < n_rows; row += 8) {
+    float m[4], l[4], top = -CUDART_INF_F;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      l[g] = 0.f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) l[g] += sm.share[g >> 1][g & 1][q * NARROW_ROWS + row];
+      const float ref = sm.share[g >> 1][g & 1][4 * NARROW_ROWS + row];
+      m[g] = l[g] == 0.f ? -CUDART_INF_F : ref == -CUDART_INF_F ? 0.f : ref;
+      top = fmaxf(top, m[g]);
+    }
+    float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      if (m[g] == -CUDART_INF_F) continue;
+      const float w = ex2(m[g] - top);
+      const float4 x = *reinterpret_cast<const float4*>(merge + (g * NARROW_ROWS + row) * D + c * 4);
+      sum += l[g] * w;
+      o[0] += x.x * w;
+      o[1] += x.y * w;
+      o[2] += x.z * w;
+      o[3] += x.w * w;
+    }
+    const int tok = it.tok + row / p.group, head = it.kvh * p.group + row % p.group;
+    if (it.parts == 1) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      float poison = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        o[j] *= inv;
+        poison += o[j] * 0.f;
+      }
+      *reinterpret_cast<uint2*>(p.a.out + ((int64_t)tok * p.a.hq + head) * D + c * 4) =
+          make_uint2(act_pack2<FP16>(o[0], o[1]), act_pack2<FP16>(o[2], o[3]));
+      if (p.a.lse && c == 0)
+        p.a.lse[(int64_t)tok * p.a.hq + head] = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum) - K::weight_exp) * LN2;
+      if (poison != 0.f && sum == sum) atomicOr(&sm.poisoned[s][0][0], 1u << row);
+    } else {
+      const size_t part_row = (((size_t)blockIdx.x * 2 + (it.part == 0 ? 1 : 0)) * 2) * ROWS + row;
+      __stcg(p.part_o + part_piece(part_row, c), make_float4(o[0], o[1], o[2], o[3]));
+      if (c == 0) __stcg(&p.part_ml[part_row], make_float2(top, sum));
+    }
+  }
+  __syncwarp();
+}
+
+// What the softmax warps count.
+struct Counts {
+  uint32_t items = 0, fills = 0, tiles = 0, s_count = 0, o_count = 0, merges = 0, q_reads = 0, narrow_count = 0;
+};
+
+// Items up to the end, or (true) up to a narrow one.
 template <bool FP16, bool QUANT>
-__device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned char* q_smem, unsigned char* kv_smem,
-                                             uint32_t tmem) {
+__device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigned char* q_smem, unsigned char* kv_smem,
+                                              uint32_t tmem, Counts& n) {
   using K = Kind<FP16, QUANT>;
   unsigned* err = p.a.err;
   const int s = threadIdx.x >> 8, half = (threadIdx.x >> 7) & 1;  // stream; half of the tile's keys, and of the dimensions
@@ -1280,13 +1814,16 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
   float sl = p.a.scale * LOG2E;
   const int all_held = QUANT ? (1 << BLOCKS8) - 1 : (1 << p.boxes) - 1;
   const int box_shift = p.a.page_shift < 7 ? p.a.page_shift : 7;
-  uint32_t fills = 0, tiles = 0, s_count = 0, o_count = 0, merges = 0, q_reads = 0;
-  for (uint32_t items = 0;; ++items) {
+  uint32_t &fills = n.fills, &tiles = n.tiles, &s_count = n.s_count, &o_count = n.o_count, &merges = n.merges, &q_reads = n.q_reads;
+  for (uint32_t& items = n.items;; ++items) {
     const uint32_t slot = items % RING;
     wait(&sm.ring_full[slot], (items / RING) & 1, sm, err);
     if (named_bar_or(bar, 256, is_dead(sm))) break;
     const Item& it = sm.ring[slot];
     if (it.b < 0) break;
+    if constexpr (QUANT) {
+      if (is_narrow(it.n_tok, p.group) && it.i1 > it.i0) return true;
+    }
     const bool two = it.n_tok > p.tile_tok;
     const int tile = two ? s : 0, i0 = it.i0, i1 = it.i1, kv = it.kv, odd = it.lead ^ s;
     const int tb = tile * p.tile_tok + row_tok;
@@ -1334,7 +1871,15 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
         __syncwarp();
       }
       if (any_row) {
-        const int held = *(volatile int*)&sm.page_mask[(tiles + i - i0) % MASKS];
+        int held;
+        if constexpr (QUANT) {
+          QuantSmem& qs = static_cast<QuantSmem&>(sm);
+          const uint32_t t = tiles + i - i0;
+          warp_wait(&qs.scales_full[t % SCALES], (t / SCALES) & 1, sm, err);
+          held = *(volatile int*)&qs.held[t % SCALES];
+        } else {
+          held = *(volatile int*)&sm.page_mask[(tiles + i - i0) % MASKS];
+        }
         if (!clear || held != all_held) {
           // hidden scores become -inf where they are
 #pragma unroll 1
@@ -1375,32 +1920,30 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
               // The values' scale is part of the score here, so that a weight is what
               // their number is multiplied by, and is taken out of the row's sum.
               const QuantSmem& qs = static_cast<const QuantSmem&>(sm);
-              const int place = (tiles + i - i0) % MASKS;
+              const int place = (tiles + i - i0) % SCALES;
               const float ref = K::weight_exp - (m == -CUDART_INF_F ? 0.f : m);
               total = 0.f;
               sum[0].x = 0.f;
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                load(c);
-                const float2 ks = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(&qs.k_scale[place][half]) + c * 2);
-                const float2 lv = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(&qs.v_log[place][half]) + c * 2);
-                const float2 iv = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(&qs.v_inverse[place][half]) + c * 2);
+              for (int b = 0; b < 4; ++b) {
+                uint32_t z[16];
+                tc::tmem_ld16_async(t_s + b * 16, z);
+                const float a = row_factor(sl, reinterpret_cast<const float*>(&qs.k_scale[place][half])[b]);
+                const float r0 = ref + reinterpret_cast<const float*>(&qs.v_log[place][half])[b];
+                const float2 a2 = make_float2(a, a), r2 = make_float2(r0, r0);
+                float2 block = make_float2(0.f, 0.f);
+                tc::tmem_wait_ld();
+                tc::tmem_regs(z);
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                  const float a = row_factor(sl, b ? ks.y : ks.x), r0 = ref + (b ? lv.y : lv.x);
-                  const float2 a2 = make_float2(a, a), r2 = make_float2(r0, r0);
-                  float2 block = make_float2(0.f, 0.f);
-#pragma unroll
-                  for (int j = b * 8; j < b * 8 + 8; ++j) {
-                    const float2 e = ffma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), a2, r2);
-                    const float2 y = make_float2(ex2(e.x), ex2(e.y));
-                    block = fadd2(block, y);
-                    w[c][j] = act_pack2<true>(y.x, y.y);
-                  }
-                  const float t = block.x + block.y;
-                  total += t;
-                  sum[0].x += t * (b ? iv.y : iv.x);
+                for (int j = 0; j < 8; ++j) {
+                  const float2 e = ffma2(make_float2(__uint_as_float(z[2 * j]), __uint_as_float(z[2 * j + 1])), a2, r2);
+                  const float2 y = make_float2(ex2(e.x), ex2(e.y));
+                  block = fadd2(block, y);
+                  w[b >> 1][(b & 1) * 8 + j] = act_pack2<true>(y.x, y.y);
                 }
+                const float t = block.x + block.y;
+                total += t;
+                sum[0].x += t * reinterpret_cast<const float*>(&qs.v_inverse[place][half])[b];
               }
             } else {
             const float ref = WEIGHT_EXP<FP16> - (m == -CUDART_INF_F ? 0.f : m * sl);
@@ -1430,7 +1973,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
             load(c);
             if constexpr (QUANT) {
               const QuantSmem& qs = static_cast<const QuantSmem&>(sm);
-              const int place = (tiles + i - i0) % MASKS;
+              const int place = (tiles + i - i0) % SCALES;
 #pragma unroll
               for (int b = 0; b < 2; ++b) {
                 const float ks = reinterpret_cast<const float*>(&qs.k_scale[place][half])[c * 2 + b];
@@ -1611,7 +2154,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
       named_bar_sync(bar, 256);
       if ((threadIdx.x & 255) == 0) {
         mbar_arrive(&sm.merge_free);
-        asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(&sm.joined)), "r"((int)merges) : "memory");
+        store_release(&sm.joined, (int)merges);
       }
     }
     if (whole_pair) {
@@ -1632,24 +2175,79 @@ __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned
       if (bad) mend_rows<FP16, QUANT>(p, sm, s, half, quarter, pair, it, tile, bad);
     } else {
       if (half == 0 && valid) __stcg(&p.part_ml[part_row], make_float2(m2, l));
-      named_bar_sync(bar, 256);
-      if ((threadIdx.x & 255) == 0) {
-        __threadfence();  // for all of the stream's stores, which the barrier put before it
-        unsigned* counter = &p.counters[it.first * 2 + tile];
-        const bool last = atomicAdd(counter, 1u) + 1 == (unsigned)it.parts;
-        if (last) {
-          *counter = 0;
-          __threadfence();
-        }
-        sm.last[s] = last;
-      }
-      named_bar_sync(bar, 256);
-      if (sm.last[s]) {
+      if (last_part(p, sm, s, it, tile, bar)) {
         join_parts<FP16, QUANT>(p, sm, s, it, tile, min(p.tile_tok, it.n_tok - tile * p.tile_tok) * p.group);
       }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.ring_empty[slot]);
+  }
+  return false;
+}
+
+// Out of line, so that the narrow blocks' calls cost the loop above no registers.
+template <bool FP16>
+__device__ __forceinline__ bool wide_items(const Params& p, QuantSmem& sm, unsigned char* q_smem, unsigned char* kv_smem, uint32_t tmem,
+                                        Counts& n) {
+  Counts c = n;  // in registers
+  const bool narrow = softmax_items<FP16, true>(p, sm, q_smem, kv_smem, tmem, c);
+  n = c;
+  return narrow;
+}
+
+// A narrow block by all softmax warps.
+template <bool FP16>
+__device__ __forceinline__ void narrow_item(const Params& p, QuantSmem& sm, const Item& it, unsigned char* q_smem,
+                                         unsigned char* kv_smem, uint32_t tmem, Counts& n) {
+  unsigned* err = p.a.err;
+  const int s = threadIdx.x >> 8, half = (threadIdx.x >> 7) & 1, lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
+  const int bar = STREAM_BAR + s, odd = it.lead ^ s, n_tiles = it.i1 - it.i0;
+  if (octets(it.n_tok, p.group) == 1)
+    narrow_block<FP16, 1>(p, sm, it, q_smem, kv_smem, tmem, n.tiles, n.fills, n.narrow_count, n.o_count, n.merges);
+  else
+    narrow_block<FP16, 2>(p, sm, it, q_smem, kv_smem, tmem, n.tiles, n.fills, n.narrow_count, n.o_count, n.merges);
+  n.narrow_count += (n_tiles - odd - 2 * half + 3) >> 2;
+  if (n_tiles > odd) ++n.o_count;
+  n.fills += 2 * n_tiles;
+  n.tiles += n_tiles;
+  if (odd) {
+    ++n.merges;
+    if (lane == 0) mbar_arrive(&sm.merge_full);
+    return;
+  }
+  warp_wait(&sm.merge_full, n.merges & 1, sm, err);
+  ++n.merges;
+  join_groups<FP16>(p, sm, it, q_smem);
+  // queries and weights may land where the results were
+  fence_proxy_async_smem();
+  named_bar_sync(bar, 256);
+  if ((threadIdx.x & 255) == 0) {
+    mbar_arrive(&sm.merge_free);
+    store_release(&sm.joined, (int)n.merges);
+  }
+  if (it.parts == 1) {
+    const unsigned bad = sm.poisoned[s][0][0];
+    if (bad && quarter == 0) mend_rows<FP16, true>(p, sm, s, half, quarter, PAIR_BAR + s * 4, it, 0, bad);
+  } else if (last_part(p, sm, s, it, 0, bar)) {
+    join_parts<FP16, true>(p, sm, s, it, 0, it.n_tok * p.group);
+  }
+}
+
+template <bool FP16, bool QUANT>
+__device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned char* q_smem, unsigned char* kv_smem,
+                                             uint32_t tmem) {
+  Counts n;
+  if constexpr (QUANT) {
+    QuantSmem& qs = static_cast<QuantSmem&>(sm);
+    const int lane = threadIdx.x & 31;
+    while (wide_items<FP16>(p, qs, q_smem, kv_smem, tmem, n)) {
+      narrow_item<FP16>(p, qs, sm.ring[n.items % RING], q_smem, kv_smem, tmem, n);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.ring_empty[n.items % RING]);
+      ++n.items;
+    }
+  } else {
+    softmax_items<FP16, QUANT>(p, sm, q_smem, kv_smem, tmem, n);
   }
 }
 
@@ -1684,6 +2282,18 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&sm.o_full[s], 1);
       mbar_init(&sm.o_free[s], 8);
     }
+    if constexpr (QUANT) {
+      for (int g = 0; g < 4; ++g) {
+        mbar_init(&sm.narrow_s[g], 1);
+        mbar_init(&sm.narrow_p[g], 4);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sm.narrow_q_full[i], 1);
+        mbar_init(&sm.narrow_q_empty[i], 2);  // both streams
+      }
+      for (int i = 0; i < SCALES; ++i) mbar_init(&sm.scales_full[i], 1);
+      sm.copied = 0;
+    }
     sm.dead = sm.beat = 0;
     sm.joined = 0;
     fence_mbar_init();
@@ -1705,7 +2315,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp >= MMA_WARP) {
     mma_role<FP16, QUANT>(p, sm, warp - MMA_WARP, smem_u32(q_smem), smem_u32(kv_smem), tmem, FP16 ? 0u : 1u);
   } else if (warp == PLAN_WARP) {
-    plan_role(p, sm, blockIdx.x, piece);
+    plan_role<QUANT>(p, sm, blockIdx.x, piece);
   }
   __syncwarp();
   tc::fence_before_sync();
@@ -1842,7 +2452,7 @@ bool encode8(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, int rank, 
                                  (cuuint64_t)(n4 > 1 ? s4 : D)};
   const cuuint32_t box[5] = {D, b1, b2, b3, 1}, step[5] = {1, 1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, step,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
