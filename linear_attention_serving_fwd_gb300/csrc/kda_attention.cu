@@ -77,6 +77,8 @@ constexpr int LOAD_WARP = 16, PLAN_WARP = 17, MMA_WARP = 18;  // MMA_WARP + 1: t
 // prompts of 2048 tokens 246 -> 193 us, a window of 1024 over 8001 tokens 114 ->
 // 83 us, 128 single tokens 393 -> 369 us; 6 and 2, or 4 and 1, are 1 to 5 % behind.
 constexpr int LEAD_TWO = 4, LEAD_ONE = 2;
+// Over an 8-bit cache, where blocks differ more: what a key tile and the lead count.
+constexpr int COST_NARROW8 = 2, COST_ONE8 = 3, LEAD_NARROW8 = 6, LEAD_ONE8 = 6, LEAD_TWO8 = 16;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // The running reference follows the row's maximum only when 64 weights have
 // come to sum to more: until then weights above one stand, and the accumulator
@@ -193,6 +195,7 @@ struct Kind {
 struct Params {
   AttentionParams a;
   KvQuantCache c;          // the 8-bit cache
+  int cost_two;            // of a key tile of a block of two tiles
   const float* q_scale;    // of the rows of its queries' parts, [t_total, hq], with scale and log2 e
   int group, tile_tok;     // G, tokens per query tile
   int n_cta;
@@ -627,15 +630,27 @@ __device__ __forceinline__ int block_tiles(const Params& p, int n, int kv, int k
 }
 // Its length on the line: the key tiles, and before them what a block costs by
 // itself (queries, pipeline fill, results), in key tiles.
-__device__ __forceinline__ int block_lead(const Params& p, const Item& it) { return it.n_tok > p.tile_tok ? LEAD_TWO : LEAD_ONE; }
+template <bool QUANT>
+__device__ __forceinline__ int block_lead(const Params& p, const Item& it) {
+  if constexpr (QUANT) return it.n_tok > p.tile_tok ? LEAD_TWO8 : is_narrow(it.n_tok, p.group) ? LEAD_NARROW8 : LEAD_ONE8;
+  return it.n_tok > p.tile_tok ? LEAD_TWO : LEAD_ONE;
+}
+// What a key tile of it counts.
+template <bool QUANT>
+__device__ __forceinline__ int tile_cost(const Params& p, const Item& it) {
+  if constexpr (QUANT) return it.n_tok > p.tile_tok ? p.cost_two : is_narrow(it.n_tok, p.group) ? COST_NARROW8 : COST_ONE8;
+  return 1;
+}
+template <bool QUANT>
 __device__ __forceinline__ int block_cost(const Params& p, int n, int kv, int k) {
   Item it;
   const int tiles = max(1, block_tiles(p, n, kv, k, it));
-  return tiles + block_lead(p, it);
+  return tiles * tile_cost<QUANT>(p, it) + block_lead<QUANT>(p, it);
 }
 __device__ __forceinline__ int n_blocks(const Params& p, int n) { return (n + 2 * p.tile_tok - 1) / (2 * p.tile_tok); }
 
 // Sum of the costs of a request's blocks; the lanes of a warp share long ones.
+template <bool QUANT>
 __device__ __forceinline__ long long request_cost(const Params& p, int b, bool valid, bool report) {
   const int lane = threadIdx.x & 31;
   int t0 = 0, n = 0, kv = 0;
@@ -643,7 +658,7 @@ __device__ __forceinline__ long long request_cost(const Params& p, int b, bool v
   const int blocks = n_blocks(p, n);
   long long cost = 0;
   if (blocks <= 4)
-    for (int k = 0; k < blocks; ++k) cost += block_cost(p, n, kv, k);
+    for (int k = 0; k < blocks; ++k) cost += block_cost<QUANT>(p, n, kv, k);
   unsigned big = __ballot_sync(0xffffffffu, blocks > 4);
   while (big) {
     const int src = __ffs(big) - 1;
@@ -651,7 +666,7 @@ __device__ __forceinline__ long long request_cost(const Params& p, int b, bool v
     const int n_s = __shfl_sync(0xffffffffu, n, src), kv_s = __shfl_sync(0xffffffffu, kv, src);
     const int blocks_s = __shfl_sync(0xffffffffu, blocks, src);
     long long sum = 0;
-    for (int k = lane; k < blocks_s; k += 32) sum += block_cost(p, n_s, kv_s, k);
+    for (int k = lane; k < blocks_s; k += 32) sum += block_cost<QUANT>(p, n_s, kv_s, k);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
     if (lane == src) cost = sum;
@@ -725,6 +740,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
     };
     auto queries = [&]() {
       asked = true;
+      if constexpr (QUANT) griddep_wait();  // at once after the first time
       const bool two = it.n_tok > p.tile_tok;
       warp_wait(&sm.q_empty, (q_count & 1) ^ 1, sm, err);
       if constexpr (QUANT) {
@@ -1245,15 +1261,17 @@ __device__ __forceinline__ void plan_role(const Params& p, Smem& sm, int cta, lo
       auto emit = [&](int k, long long s) {
         Item it;
         const int tiles = block_tiles(p, n, kv, k, it);
-        s += block_lead(p, it);
-        const long long e = s + max(1, tiles);
+        const int each = tile_cost<QUANT>(p, it);
+        s += block_lead<QUANT>(p, it);
+        const long long e = s + (long long)max(1, tiles) * each;
         if (s >= u1 || e <= u0) return;
         it.b = b;
         it.kvh = h;
         it.tok = t0 + k * 2 * p.tile_tok;
         it.kv = kv;
-        it.i0 = (int)max(0LL, u0 - s);
-        it.i1 = (int)min((long long)tiles, u1 - s);
+        // a tile belongs to the piece in which it begins
+        it.i0 = u0 <= s ? 0 : (int)quotient(u0 - s + each - 1, each);
+        it.i1 = u1 >= e ? tiles : min(tiles, (int)quotient(u1 - s + each - 1, each));
         it.first = (int)quotient(s, piece);
         it.parts = (int)quotient(e - 1, piece) - it.first + 1;
         it.part = cta - it.first;
@@ -1269,7 +1287,7 @@ __device__ __forceinline__ void plan_role(const Params& p, Smem& sm, int cta, lo
       };
       for (int k0 = 0; ok && k0 < blocks && at < u1; k0 += 32) {
         // 32 blocks at once, unless the request has but one
-        long long upto = k0 + lane < blocks ? block_cost(p, n, kv, k0 + lane) : 0;
+        long long upto = k0 + lane < blocks ? block_cost<QUANT>(p, n, kv, k0 + lane) : 0;
         const long long mine = upto;
         if (blocks > 1) {
 #pragma unroll 1
@@ -1301,6 +1319,7 @@ __device__ __forceinline__ void plan_role(const Params& p, Smem& sm, int cta, lo
 // Costs of all requests: the line's length, and the request in which this CTA's
 // piece begins.  By the softmax warps, while the others set the CTA up; all
 // meet at the barrier inside.
+template <bool QUANT>
 __device__ __forceinline__ long long measure_line(const Params& p, Smem& sm, int cta) {
   constexpr int COUNTERS = SOFTMAX_WARPS * 32;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -1308,7 +1327,7 @@ __device__ __forceinline__ long long measure_line(const Params& p, Smem& sm, int
   const int each = (p.a.n_req + COUNTERS - 1) / COUNTERS;
   long long cost = 0, upto = 0;
   if (counts) {
-    for (int j = 0; j < each; ++j) cost += request_cost(p, t * each + j, t * each + j < p.a.n_req, cta == 0);
+    for (int j = 0; j < each; ++j) cost += request_cost<QUANT>(p, t * each + j, t * each + j < p.a.n_req, cta == 0);
     upto = cost;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -1341,7 +1360,7 @@ __device__ __forceinline__ long long measure_line(const Params& p, Smem& sm, int
     } else if (__any_sync(0xffffffffu, mine)) {
       bool found = false;
       for (int j = 0; j < each; ++j) {
-        const long long c = request_cost(p, t * each + j, t * each + j < p.a.n_req, false);
+        const long long c = request_cost<QUANT>(p, t * each + j, t * each + j < p.a.n_req, false);
         if (mine && !found && w0 < before + c) {
           found = true;
           sm.start_b = t * each + j;
@@ -2237,6 +2256,7 @@ template <bool FP16, bool QUANT>
 __device__ __forceinline__ void softmax_role(const Params& p, Smem& sm, unsigned char* q_smem, unsigned char* kv_smem,
                                              uint32_t tmem) {
   Counts n;
+  if constexpr (QUANT) griddep_wait();  // the rows' factors
   if constexpr (QUANT) {
     QuantSmem& qs = static_cast<QuantSmem&>(sm);
     const int lane = threadIdx.x & 31;
@@ -2304,8 +2324,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   // the set-up above overlaps the end of the kernel before; what it wrote is read below
   griddep_launch_dependents();
-  griddep_wait();
-  const long long piece = measure_line(p, sm, blockIdx.x);
+  // In 8 bits the kernel before is the queries' split, which lets this one begin
+  // when what came before it is done: only those who take its results wait for it.
+  if constexpr (!QUANT) griddep_wait();
+  const long long piece = measure_line<QUANT>(p, sm, blockIdx.x);
   __syncthreads();
   const uint32_t tmem = sm.tmem;
   if (warp < SOFTMAX_WARPS) {
@@ -2337,8 +2359,10 @@ static_assert(SMEM_BYTES8<false> <= 232448 && SMEM_BYTES8<true> <= 232448, "shar
 // 1.5 (bf16) or 2 times... bytes of the queries once.
 template <bool FP16>
 __global__ void __launch_bounds__(256) split_queries_kernel(AttentionParams p, uint8_t* parts, float* factors) {
-  griddep_launch_dependents();
+  // In this order: the attention kernel may begin once all of this grid is past the
+  // wait, and so after everything before this call.
   griddep_wait();
+  griddep_launch_dependents();
   const int64_t i = blockIdx.x * 256ll + threadIdx.x, row = i >> 4, rows = (int64_t)p.t_total * p.hq;
   const int c = (int)(i & 15) * 8;
   if (row >= rows) return;  // 16 lanes alike
@@ -2537,6 +2561,8 @@ int launch_attention_quant(const AttentionParams& a, const KvQuantCache& c, bool
   Params p = {};
   plan_call(p, a, workspace);
   p.c = c;
+  p.cost_two = fp16 ? 7 : 6;
+  p.min_piece *= COST_NARROW8;
   const int page = 1 << a.page_shift, box = page < KT ? page : KT, parts = fp16 ? Q_PARTS<true> : Q_PARTS<false>;
   p.group_bytes = 1024;
   p.half_bytes = 16;  // a row is whole: not used
