@@ -51,7 +51,7 @@ __device__ __forceinline__ uint32_t max_halves(uint32_t m, uint32_t w) { return 
 // head of k or of v of those blocks: lane l holds 8 dimensions of the rows of
 // one parity, so that a load or store of the warp is two whole rows.
 template <bool FP16>
-__global__ void __launch_bounds__(256) kv_quant_append_kernel(KvQuantAppendParams p) {
+__global__ void __launch_bounds__(256, 4) kv_quant_append_kernel(KvQuantAppendParams p) {
   constexpr uint32_t LARGEST = FP16 ? 0x7bffu : 0x7f7fu;  // finite
   const int lane = threadIdx.x & 31, piece = lane & 15, odd = lane >> 4;
   const int64_t unit = blockIdx.x * 8ll + (threadIdx.x >> 5);
@@ -120,21 +120,6 @@ __global__ void __launch_bounds__(256) kv_quant_append_kernel(KvQuantAppendParam
     const bool kept = r0 > 0 && was >= need && was <= power(MOST);
     const float now = kept ? was : need, inv = kept ? 1.f / was : power(-exponent(unpack16<FP16>(m).x));
     uint8_t* out = cache + pg * c_sp + (int64_t)row * c_st + piece * 8;
-    if (r0 > 0 && !kept) {
-      const float ratio = was * inv;
-#pragma unroll 1
-      for (int i = odd - r0; i < 0; i += 2) {
-        uint2* at = reinterpret_cast<uint2*>(out + i * c_st);
-        const uint2 w = *at;
-        uint32_t y[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 v = unpack_e4m3((k < 2 ? w.x : w.y) >> (k & 1) * 16);
-          y[k] = pack_e4m3(v.x * ratio, v.y * ratio);
-        }
-        *at = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
-      }
-    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int i = 2 * j + odd;
@@ -146,6 +131,24 @@ __global__ void __launch_bounds__(256) kv_quant_append_kernel(KvQuantAppendParam
         y[k] = pack_e4m3(v.x * inv, v.y * inv);
       }
       if (i < n) *reinterpret_cast<uint2*>(out + i * c_st) = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
+    }
+    if (r0 > 0 && !kept) {  // all earlier rows at once: one after another took 5 us
+      const float ratio = was * inv;
+      uint2 old[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (2 * j + odd < r0) old[j] = *reinterpret_cast<const uint2*>(out + (2 * j + odd - r0) * c_st);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = unpack_e4m3((k < 2 ? old[j].x : old[j].y) >> (k & 1) * 16);
+          y[k] = pack_e4m3(v.x * ratio, v.y * ratio);
+        }
+        if (2 * j + odd < r0)
+          *reinterpret_cast<uint2*>(out + (2 * j + odd - r0) * c_st) = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
+      }
     }
     if (lane == 0 && !kept) *scale = now;
   }

@@ -63,6 +63,13 @@ class Rope:
         self._ref = ctypes.byref(r)
 
 
+def _out(y, x, name, dtype, index):
+    """(pointer, token stride, head stride) of the output y of x."""
+    if y is not x and y.shape != x.shape:
+        raise ValueError(f"{name}_out must have {name}'s shape.")
+    return _rows(y, f"{name}_out", dtype, index)[2:]
+
+
 def kda_rope(rope: Rope, q, k=None, *, positions=None, cu_seqlens=None, kv_lens=None, q_out=None, k_out=None, stream=None):
     """Turn q [T, Hq, 128] and k [T, Hkv, 128] (bf16 or fp16; k may be None) by
     the positions of their tokens: ``positions`` [T], or, from ``cu_seqlens``
@@ -79,37 +86,36 @@ def kda_rope(rope: Rope, q, k=None, *, positions=None, cu_seqlens=None, kv_lens=
     handle, dtype = _stream(None, index), q.dtype
     if dtype not in _DTYPES:
         raise TypeError(f"q must be torch.bfloat16 or torch.float16 (got {dtype}).")
-    args, out = [], []
-    tokens = None
-    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            if y is not None:
-                raise ValueError(f"{name}_out without {name}.")
-            args += [None, 0, 0, 0, None, 0, 0]
-            out.append(None)
-            continue
-        t, h, ptr, st, sh = _rows(x, name, dtype, index)
-        if tokens is not None and t != tokens:
+    t, hq, qp, qt, qh = _rows(q, "q", dtype, index)
+    if q_out is None:
+        q_out = torch.empty((t, hq, 128), dtype=dtype, device=q.device)
+        out = q_out.data_ptr(), hq * 128, 128
+    else:
+        out = _out(q_out, q, "q", dtype, index)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k.")
+        hk, kp, kt, kh, k_args = 0, None, 0, 0, (None, 0, 0)
+    else:
+        tk, hk, kp, kt, kh = _rows(k, "k", dtype, index)
+        if tk != t:
             raise ValueError("q and k must have the same number of tokens.")
-        tokens = t
-        if y is None:
-            y = torch.empty((t, h, 128), dtype=dtype, device=x.device)
-        elif y is not x and y.shape != x.shape:
-            raise ValueError(f"{name}_out must have {name}'s shape.")
-        _, _, y_ptr, y_st, y_sh = _rows(y, f"{name}_out", dtype, index, h)
-        args += [ptr, st, sh, h, y_ptr, y_st, y_sh]
-        out.append(y)
+        if k_out is None:
+            k_out = torch.empty((t, hk, 128), dtype=dtype, device=k.device)
+            k_args = k_out.data_ptr(), hk * 128, 128
+        else:
+            k_args = _out(k_out, k, "k", dtype, index)
     n = 0
     if positions is not None:
         if cu_seqlens is not None or kv_lens is not None:
             raise ValueError("positions, or cu_seqlens and kv_lens, not both.")
-        where = (_int32(positions, "positions", index, tokens), None, None)
+        where = (_int32(positions, "positions", index, t), None, None)
     elif cu_seqlens is None or kv_lens is None:
         raise ValueError("positions, or cu_seqlens and kv_lens, are needed.")
     else:
         n = kv_lens.numel()
         where = (None, _int32(cu_seqlens, "cu_seqlens", index, n + 1), _int32(kv_lens, "kv_lens", index))
-    rc = _native.lib().kda_rope(rope._ref, _DTYPES[dtype], *args, tokens, *where, n, handle)
+    rc = _native.lib().kda_rope(rope._ref, _DTYPES[dtype], qp, qt, qh, hq, *out, kp, kt, kh, hk, *k_args, t, *where, n, handle)
     if rc:
         _native.check(rc)
-    return out[0], out[1]
+    return q_out, k_out
