@@ -143,9 +143,10 @@ constexpr int STAGES8 = FP16 ? 7 : 9;
 // warp reaches 32 lanes of tensor memory only.  So the keys are the lanes here:
 // S^T = K Q^T (128 keys x rows) and O^T = V^T P^T (128 dimensions x rows), with the
 // parts of the queries and of the weights side by side in the columns, and a
-// thread has one key and all rows.  The four softmax warpgroups take the key tiles
-// in turn, each with a reference, sums and an O^T of its own, and their results
-// are joined in shared memory.
+// thread has one key and all rows.  The streams take such blocks in turn, so that
+// one begins while the other ends; a stream's two warpgroups take its key tiles in
+// turn, each with a reference, sums and an O^T of its own, and their results are
+// joined in shared memory.
 constexpr int NARROW_ROWS = 16;
 // In the queries' buffer: those of two narrow blocks, so that the next one's are
 // there when it begins, and behind them the weights.
@@ -174,6 +175,7 @@ struct QuantSmem : Smem {
   uint64_t narrow_s[4], narrow_p[4], narrow_q_full[2], narrow_q_empty[2];
   float4 narrow_factor[4][NARROW_ROWS / 4], narrow_m[4][NARROW_ROWS / 4];
   float narrow_top[4][4 * NARROW_ROWS];  // of each warp's keys
+  int narrow_done[2];                    // blocks of each stream
 };
 // What differs between the two caches.
 template <bool FP16, bool QUANT>
@@ -315,6 +317,18 @@ __device__ __forceinline__ void tma_load5(void* dst, const CUtensorMap* map, int
   asm volatile(
       "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], [%5];"
       ::"r"(smem_u32(dst)), "l"(map), "r"(0), "r"(c3), "r"(c4), "r"(smem_u32(bar)) : "memory");
+}
+// of what no one reads again
+__device__ __forceinline__ void tma_load4_once(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint64_t* bar,
+                                               uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6], %7;" ::"r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)), "l"(policy) : "memory");
+}
+__device__ __forceinline__ uint64_t evict_first() {
+  uint64_t policy;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
 }
 __device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
   asm volatile(
@@ -702,8 +716,8 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
   uint32_t place = 0, parity = 0;  // in 8 bits: of the next fill
   int merges = 0;       // joined results before this item
   int rows_before = 0;  // rows of the last block whose results are joined
-  bool narrow_before = false;
   uint32_t narrow_count = 0;
+  int narrow_of[2] = {0, 0};  // by stream
   for (uint32_t items = 0;; ++items) {
     const uint32_t slot = items % RING;
     wait(&sm.ring_full[slot], (items / RING) & 1, sm, err);
@@ -750,10 +764,9 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
           warp_wait(&qs.narrow_q_empty[place], ((narrow_count >> 1) & 1) ^ 1, sm, err);
           if (rows_before > MERGE_ROWS) wait_count(&sm.joined, merges, sm, err);
           if (__any_sync(0xffffffffu, is_dead(sm))) return;
-          ++merges;
           rows_before = 0;
-          narrow_before = true;
           ++narrow_count;
+          ++narrow_of[it.lead];
           constexpr int PARTS = Q_PARTS<FP16>;
           const int rows = 8 * octets(it.n_tok, p.group);
           if (lane == 0) mbar_arrive_expect_tx(&qs.narrow_q_full[place], PARTS * it.n_tok * p.group * 128u);
@@ -770,11 +783,13 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
       // Blocks of one tile join their results in the second tile's place, or in
       // all of the buffer: the last such joining has to be over if it is in the
       // way.  (A count and no barrier: this warp does not see every joining.)
-      // A narrow one's weights lie in the way as well.
-      if (two || rows_before > MERGE_ROWS || narrow_before) wait_count(&sm.joined, merges, sm, err);
+      if (two || rows_before > MERGE_ROWS) wait_count(&sm.joined, merges, sm, err);
+      if constexpr (QUANT) {  // narrow blocks' weights and results lie in the way as well
+        wait_count(&static_cast<QuantSmem&>(sm).narrow_done[0], narrow_of[0], sm, err);
+        wait_count(&static_cast<QuantSmem&>(sm).narrow_done[1], narrow_of[1], sm, err);
+      }
       if (__any_sync(0xffffffffu, is_dead(sm))) return;
       const bool joins = !two && it.i1 - it.i0 > 1;
-      narrow_before = false;
       merges += joins;
       if (joins) rows_before = it.n_tok * p.group;
       ++q_count;
@@ -822,6 +837,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
       const int my_box = values ? lane - p.boxes : lane;
       const CUtensorMap* map = values ? &maps.v : &maps.k;
       unsigned char* to = kv_smem + my_box * box * 128;
+      const uint64_t policy = evict_first();  // a narrow block is all who read its keys: 391 -> 375 us on 256 requests
       auto entry = [&](int i) {  // of the table; -1 for a box that no row sees
         if (!copies || i >= it.i1) return -1;
         const int key = list_tile(it, i) * KT + my_box * box;
@@ -846,7 +862,9 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
         if (copies) {
           const int row = (list_tile(it, i) * KT) & (page - 1) & ~(box - 1);
           const uint32_t st = values ? second : place;
-          tma_load4(to + st * K::tile, map, 0, row, it.kvh, now < 0 || now > p.a.n_pages ? p.a.n_pages : now, K::full(sm, st));
+          const int pg = now < 0 || now > p.a.n_pages ? p.a.n_pages : now;
+          if (narrow) tma_load4_once(to + st * K::tile, map, 0, row, it.kvh, pg, K::full(sm, st), policy);
+          else tma_load4(to + st * K::tile, map, 0, row, it.kvh, pg, K::full(sm, st));
         }
         place = second + 1 == K::stages ? 0 : second + 1;
         parity = place == 0 ? second_parity ^ 1 : second_parity;
@@ -976,21 +994,22 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
     const uint64_t qd = tc::smem_desc_sw128(q_addr + (two ? s * K::q_tile : 0));
     if constexpr (QUANT) {
       if (narrow) {
-        // This stream's key tiles go to its two warpgroups in turn.  Scores are
-        // issued up to two tiles ahead of the weights' product, whichever is ready.
+        // The key tiles go to the two warpgroups of the block's stream in turn; the
+        // other stream sees their copies alone.  Scores are issued up to two tiles
+        // ahead of the weights' product, whichever is ready.
         QuantSmem& qs = static_cast<QuantSmem&>(sm);
         const int oct = octets(it.n_tok, p.group), n_tiles = it.i1 - it.i0;
-        const int mine = (n_tiles - odd + 1) >> 1;
+        const int mine = odd ? 0 : n_tiles;
         const uint32_t n_qk = columns(oct, Q_PARTS<FP16>), n_pv = columns(oct, W_PARTS<FP16>);
         const uint32_t id_s = idesc_f8(KT, n_qk, E4M3, E4M3), id_o = idesc_f8(D, n_pv, E4M3, E5M2) | A_MN_MAJOR | B_MN_MAJOR;
         const uint32_t place = narrow_blocks & 1;
-        await(&qs.narrow_q_full[place], (narrow_blocks >> 1) & 1);
+        if (!odd) await(&qs.narrow_q_full[place], (narrow_blocks >> 1) & 1);
         ++narrow_blocks;
         const uint64_t q_desc = tc::smem_desc_sw128(q_addr + place * NARROW_Q<FP16>);
         const uint64_t w_desc = tc::smem_desc(q_addr + NARROW_P<FP16> + s * 2 * NARROW_W<FP16>, 128, 2048);
-        int tile = 0, scored_n = 0, done = 0;  // key tiles passed, of them this stream's, of those finished
+        int tile = 0, scored_n = 0, done = 0;  // key tiles passed, scored, finished
         Stage at = next, v_at = next;
-        v_at.skip(1 + 2 * odd);
+        v_at.skip(1);
         Patience patience;
         while (done < mine || tile < n_tiles) {
           bool moved = false;
@@ -1012,14 +1031,14 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
               tc::mma_commit(K::empty(sm, v_at.at));
             }
             __syncwarp();
-            v_at.skip(4);
+            v_at.skip(2);
             ++done;
             moved = true;
           }
           if (tile < n_tiles && scored_n < done + 2 && __all_sync(0xffffffffu, mbar_test_wait(K::full(sm, at.at), at.parity))) {
             Stage v = at;
             v.skip(1);
-            if ((tile & 1) == odd) {
+            if (!odd) {
               tc::fence_after_sync();
               const int g = scored_n & 1;
               if (elect_one()) {
@@ -1032,7 +1051,6 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
               }
               ++scored_n;
             } else {
-              // the other stream's: see its fills
               await(K::full(sm, v.at), v.parity);
               if (elect_one()) {
                 mbar_arrive(K::empty(sm, at.at));
@@ -1531,7 +1549,7 @@ __device__ __forceinline__ void narrow_block(const Params& p, QuantSmem& sm, con
   const int r = threadIdx.x & 127, lane = r & 31, quarter = r >> 5, bar = GROUP_BAR + g;
   const uint32_t lane_base = tmem + ((uint32_t)(r & 96) << 16);
   const uint32_t t_s = lane_base + s * 128 + half * 64, t_o = lane_base + 256 + s * 128 + half * 64;
-  const int i0 = it.i0, i1 = it.i1, kv = it.kv, odd = it.lead ^ s, n_rows = it.n_tok * p.group;
+  const int i0 = it.i0, i1 = it.i1, kv = it.kv, n_rows = it.n_tok * p.group;
   float* factor = reinterpret_cast<float*>(sm.narrow_factor[g]);
   float* ref = reinterpret_cast<float*>(sm.narrow_m[g]);  // the rows' references, in powers of two
   unsigned char* weights = q_smem + NARROW_P<FP16> + g * NARROW_W<FP16> + r * 16;
@@ -1553,7 +1571,7 @@ __device__ __forceinline__ void narrow_block(const Params& p, QuantSmem& sm, con
   for (int k = 0; k < RP; ++k) l[k] = 0.f;
   bool stepped = false;
 #pragma unroll 1
-  for (int i = i0 + odd + 2 * half; i < i1; i += 4) {
+  for (int i = i0 + half; i < i1; i += 2) {
     const int first_key = list_tile(it, i) * KT, key = first_key + r, place = (tiles + i - i0) % SCALES;
     // what the key brings, before the scores are there
     warp_wait(&sm.scales_full[place], ((tiles + i - i0) / SCALES) & 1, sm, err);
@@ -1723,31 +1741,29 @@ __device__ __forceinline__ void narrow_block(const Params& p, QuantSmem& sm, con
   float* merge = reinterpret_cast<float*>(q_smem + K::q_tile) + g * NARROW_ROWS * D;
   float* share = sm.share[s][half];
   warp_wait(&sm.merge_free, (merges & 1) ^ 1, sm, err);  // the last joined results have been read
-  if (i0 + odd < i1) {
-    warp_wait(&sm.o_full[s], o_count & 1, sm, err);
-    tc::fence_after_sync();
-    if (stepped) {
+  warp_wait(&sm.o_full[s], o_count & 1, sm, err);
+  tc::fence_after_sync();
+  if (stepped) {
 #pragma unroll
-      for (int o = 0; o < OCT; ++o) {
-        uint32_t y[W_PARTS<FP16>][8];
+    for (int o = 0; o < OCT; ++o) {
+      uint32_t y[W_PARTS<FP16>][8];
 #pragma unroll
-        for (int part = 0; part < W_PARTS<FP16>; ++part) tmem_ld8_async(t_o + part * RP + o * 8, y[part]);
-        tc::tmem_wait_ld();
+      for (int part = 0; part < W_PARTS<FP16>; ++part) tmem_ld8_async(t_o + part * RP + o * 8, y[part]);
+      tc::tmem_wait_ld();
 #pragma unroll
-        for (int part = 0; part < W_PARTS<FP16>; ++part) tmem_regs8(y[part]);
+      for (int part = 0; part < W_PARTS<FP16>; ++part) tmem_regs8(y[part]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float sum = __uint_as_float(y[0][k]);
+      for (int k = 0; k < 8; ++k) {
+        float sum = __uint_as_float(y[0][k]);
 #pragma unroll
-          for (int part = 1; part < W_PARTS<FP16>; ++part) sum += __uint_as_float(y[part][k]);
-          merge[(o * 8 + k) * D + r] = sum;
-        }
+        for (int part = 1; part < W_PARTS<FP16>; ++part) sum += __uint_as_float(y[part][k]);
+        merge[(o * 8 + k) * D + r] = sum;
       }
     }
-    tc::fence_before_sync();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.o_free[s]);
   }
+  tc::fence_before_sync();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sm.o_free[s]);
 #pragma unroll
   for (int k = 0; k < RP; ++k) {
     const float sum = warp_sum(l[k]);
@@ -1757,7 +1773,7 @@ __device__ __forceinline__ void narrow_block(const Params& p, QuantSmem& sm, con
   __syncwarp();
 }
 
-// The leading stream's eight warps join the four groups' results of a narrow block.
+// A stream's eight warps join its two warpgroups' results of a narrow block.
 template <bool FP16>
 __device__ __forceinline__ void join_groups(const Params& p, QuantSmem& sm, const Item& it, unsigned char* q_smem) {
   using K = Kind<FP16, true>;
@@ -1768,22 +1784,22 @@ __device__ __forceinline__ void join_groups(const Params& p, QuantSmem& sm, cons
   const int c = t & 31;  // 4 dimensions
 #pragma unroll 1
   for (int row = t >> 5; row < n_rows; row += 8) {
-    float m[4], l[4], top = -CUDART_INF_F;
+    float m[2], l[2], top = -CUDART_INF_F;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < 2; ++g) {
       l[g] = 0.f;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) l[g] += sm.share[g >> 1][g & 1][q * NARROW_ROWS + row];
-      const float ref = sm.share[g >> 1][g & 1][4 * NARROW_ROWS + row];
+      for (int q = 0; q < 4; ++q) l[g] += sm.share[s][g][q * NARROW_ROWS + row];
+      const float ref = sm.share[s][g][4 * NARROW_ROWS + row];
       m[g] = l[g] == 0.f ? -CUDART_INF_F : ref == -CUDART_INF_F ? 0.f : ref;
       top = fmaxf(top, m[g]);
     }
     float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < 2; ++g) {
       if (m[g] == -CUDART_INF_F) continue;
       const float w = ex2(m[g] - top);
-      const float4 x = *reinterpret_cast<const float4*>(merge + (g * NARROW_ROWS + row) * D + c * 4);
+      const float4 x = *reinterpret_cast<const float4*>(merge + ((s * 2 + g) * NARROW_ROWS + row) * D + c * 4);
       sum += l[g] * w;
       o[0] += x.x * w;
       o[1] += x.y * w;
@@ -2214,42 +2230,33 @@ __device__ __forceinline__ bool wide_items(const Params& p, QuantSmem& sm, unsig
   return narrow;
 }
 
-// A narrow block by all softmax warps.
+// A narrow block: by its stream's warps, the others pass it.
 template <bool FP16>
 __device__ __forceinline__ void narrow_item(const Params& p, QuantSmem& sm, const Item& it, unsigned char* q_smem,
-                                         unsigned char* kv_smem, uint32_t tmem, Counts& n) {
-  unsigned* err = p.a.err;
-  const int s = threadIdx.x >> 8, half = (threadIdx.x >> 7) & 1, lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
-  const int bar = STREAM_BAR + s, odd = it.lead ^ s, n_tiles = it.i1 - it.i0;
-  if (octets(it.n_tok, p.group) == 1)
-    narrow_block<FP16, 1>(p, sm, it, q_smem, kv_smem, tmem, n.tiles, n.fills, n.narrow_count, n.o_count, n.merges);
-  else
-    narrow_block<FP16, 2>(p, sm, it, q_smem, kv_smem, tmem, n.tiles, n.fills, n.narrow_count, n.o_count, n.merges);
-  n.narrow_count += (n_tiles - odd - 2 * half + 3) >> 2;
-  if (n_tiles > odd) ++n.o_count;
+                                            unsigned char* kv_smem, uint32_t tmem, Counts& n) {
+  const int s = threadIdx.x >> 8, half = (threadIdx.x >> 7) & 1, quarter = (threadIdx.x >> 5) & 3;
+  const int bar = STREAM_BAR + s, n_tiles = it.i1 - it.i0;
+  if (it.lead == s) {
+    if (octets(it.n_tok, p.group) == 1)
+      narrow_block<FP16, 1>(p, sm, it, q_smem, kv_smem, tmem, n.tiles, n.fills, n.narrow_count, n.o_count, n.merges);
+    else
+      narrow_block<FP16, 2>(p, sm, it, q_smem, kv_smem, tmem, n.tiles, n.fills, n.narrow_count, n.o_count, n.merges);
+    n.narrow_count += (n_tiles - half + 1) >> 1;
+    ++n.o_count;
+    join_groups<FP16>(p, sm, it, q_smem);
+    // queries may land where the results were
+    fence_proxy_async_smem();
+    named_bar_sync(bar, 256);
+    if ((threadIdx.x & 255) == 0) store_release(&sm.narrow_done[s], sm.narrow_done[s] + 1);
+    if (it.parts == 1) {
+      const unsigned bad = sm.poisoned[s][0][0];
+      if (bad && quarter == 0) mend_rows<FP16, true>(p, sm, s, half, quarter, PAIR_BAR + s * 4, it, 0, bad);
+    } else if (last_part(p, sm, s, it, 0, bar)) {
+      join_parts<FP16, true>(p, sm, s, it, 0, it.n_tok * p.group);
+    }
+  }
   n.fills += 2 * n_tiles;
   n.tiles += n_tiles;
-  if (odd) {
-    ++n.merges;
-    if (lane == 0) mbar_arrive(&sm.merge_full);
-    return;
-  }
-  warp_wait(&sm.merge_full, n.merges & 1, sm, err);
-  ++n.merges;
-  join_groups<FP16>(p, sm, it, q_smem);
-  // queries and weights may land where the results were
-  fence_proxy_async_smem();
-  named_bar_sync(bar, 256);
-  if ((threadIdx.x & 255) == 0) {
-    mbar_arrive(&sm.merge_free);
-    store_release(&sm.joined, (int)n.merges);
-  }
-  if (it.parts == 1) {
-    const unsigned bad = sm.poisoned[s][0][0];
-    if (bad && quarter == 0) mend_rows<FP16, true>(p, sm, s, half, quarter, PAIR_BAR + s * 4, it, 0, bad);
-  } else if (last_part(p, sm, s, it, 0, bar)) {
-    join_parts<FP16, true>(p, sm, s, it, 0, it.n_tok * p.group);
-  }
 }
 
 template <bool FP16, bool QUANT>
@@ -2312,7 +2319,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(&sm.narrow_q_empty[i], 2);  // both streams
       }
       for (int i = 0; i < SCALES; ++i) mbar_init(&sm.scales_full[i], 1);
-      sm.copied = 0;
+      sm.copied = sm.narrow_done[0] = sm.narrow_done[1] = 0;
     }
     sm.dead = sm.beat = 0;
     sm.joined = 0;
