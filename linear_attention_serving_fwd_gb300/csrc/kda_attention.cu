@@ -1883,6 +1883,16 @@ __device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigne
       if (two && !active(it.act[s], i)) continue;
       const int first_key = list_tile(it, i) * KT, key = first_key + half * 64;
       const bool clear = first_key <= clear_hi && (first_key >= clear_lo || first_key <= clear_sink);
+      int held = 0;
+      const uint32_t scales = QUANT ? (tiles + i - i0) % SCALES : 0;
+      if constexpr (QUANT) {
+        if (any_row) {
+          QuantSmem& qs = static_cast<QuantSmem&>(sm);
+          warp_wait(&qs.scales_full[scales], ((tiles + i - i0) / SCALES) & 1, sm, err);
+          held = *(volatile int*)&qs.held[scales];
+        }
+      }
+      auto scale_of = [&](const float4 (&of)[SCALES][BLOCKS8 / 4], int b) { return reinterpret_cast<const float*>(&of[scales][half])[b]; };
       warp_wait(&sm.s_full[s], s_count & 1, sm, err);
       ++s_count;
       tc::fence_after_sync();
@@ -1906,15 +1916,7 @@ __device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigne
         __syncwarp();
       }
       if (any_row) {
-        int held;
-        if constexpr (QUANT) {
-          QuantSmem& qs = static_cast<QuantSmem&>(sm);
-          const uint32_t t = tiles + i - i0;
-          warp_wait(&qs.scales_full[t % SCALES], (t / SCALES) & 1, sm, err);
-          held = *(volatile int*)&qs.held[t % SCALES];
-        } else {
-          held = *(volatile int*)&sm.page_mask[(tiles + i - i0) % MASKS];
-        }
+        if constexpr (!QUANT) held = *(volatile int*)&sm.page_mask[(tiles + i - i0) % MASKS];
         if (!clear || held != all_held) {
           // hidden scores become -inf where they are
 #pragma unroll 1
@@ -1955,30 +1957,29 @@ __device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigne
               // The values' scale is part of the score here, so that a weight is what
               // their number is multiplied by, and is taken out of the row's sum.
               const QuantSmem& qs = static_cast<const QuantSmem&>(sm);
-              const int place = (tiles + i - i0) % SCALES;
               const float ref = K::weight_exp - (m == -CUDART_INF_F ? 0.f : m);
               total = 0.f;
               sum[0].x = 0.f;
+              uint32_t z[2][16];  // a block's scores, and the next one's on their way
+              tc::tmem_ld16_async(t_s, z[0]);
 #pragma unroll
               for (int b = 0; b < 4; ++b) {
-                uint32_t z[16];
-                tc::tmem_ld16_async(t_s + b * 16, z);
-                const float a = row_factor(sl, reinterpret_cast<const float*>(&qs.k_scale[place][half])[b]);
-                const float r0 = ref + reinterpret_cast<const float*>(&qs.v_log[place][half])[b];
+                const float a = row_factor(sl, scale_of(qs.k_scale, b)), r0 = ref + scale_of(qs.v_log, b);
                 const float2 a2 = make_float2(a, a), r2 = make_float2(r0, r0);
                 float2 block = make_float2(0.f, 0.f);
                 tc::tmem_wait_ld();
-                tc::tmem_regs(z);
+                tc::tmem_regs(z[b & 1]);
+                if (b < 3) tc::tmem_ld16_async(t_s + (b + 1) * 16, z[(b + 1) & 1]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                  const float2 e = ffma2(make_float2(__uint_as_float(z[2 * j]), __uint_as_float(z[2 * j + 1])), a2, r2);
+                  const float2 e = ffma2(make_float2(__uint_as_float(z[b & 1][2 * j]), __uint_as_float(z[b & 1][2 * j + 1])), a2, r2);
                   const float2 y = make_float2(ex2(e.x), ex2(e.y));
                   block = fadd2(block, y);
                   w[b >> 1][(b & 1) * 8 + j] = act_pack2<true>(y.x, y.y);
                 }
                 const float t = block.x + block.y;
                 total += t;
-                sum[0].x += t * reinterpret_cast<const float*>(&qs.v_inverse[place][half])[b];
+                sum[0].x += t * scale_of(qs.v_inverse, b);
               }
             } else {
             const float ref = WEIGHT_EXP<FP16> - (m == -CUDART_INF_F ? 0.f : m * sl);
@@ -2008,16 +2009,13 @@ __device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigne
             load(c);
             if constexpr (QUANT) {
               const QuantSmem& qs = static_cast<const QuantSmem&>(sm);
-              const int place = (tiles + i - i0) % SCALES;
 #pragma unroll
               for (int b = 0; b < 2; ++b) {
-                const float ks = reinterpret_cast<const float*>(&qs.k_scale[place][half])[c * 2 + b];
-                const float lv = reinterpret_cast<const float*>(&qs.v_log[place][half])[c * 2 + b];
                 float top = -CUDART_INF_F;
 #pragma unroll
                 for (int j = b * 16; j < b * 16 + 16; j += 2)
                   top = max3(top, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-                m_new = fmaxf(m_new, fmaf(top, row_factor(sl, ks), lv));
+                m_new = fmaxf(m_new, fmaf(top, row_factor(sl, scale_of(qs.k_scale, c * 2 + b)), scale_of(qs.v_log, c * 2 + b)));
               }
             } else {
             float top[2] = {m_new, m_new};
