@@ -12,8 +12,9 @@ other sizes and must give the same logits up to rounding.
 Per step: kda_kv_extend takes pages for the step's tokens and lays them out;
 in every layer the tokens are projected, and run through kda_chunk_fwd (prompt
 chunks) or kda_decode (single tokens) on the request's state row, or written
-with kda_kv_append and run through kda_paged_attention.  A rejected draft is
-undone by kda_kv_truncate on the key/value side; on the recurrent side the
+with kda_kv_append and run through kda_paged_attention; with ``rope`` their
+queries and keys are turned by kda_rope first, with ``quantized`` the cache
+holds them in 8 bits.  A rejected draft is undone by kda_kv_truncate on the key/value side; on the recurrent side the
 step is run from a copy of the states (kda_verify and kda_commit do that
 without the copy).
 """
@@ -33,28 +34,30 @@ D = 128  # head dimension
 
 class HybridModel:
     """Layers 0 .. n - 1; every fourth is softmax attention (``window`` > 0: of
-    a sliding window with ``sinks`` first tokens that stay), the others KDA."""
+    a sliding window with ``sinks`` first tokens that stay; ``rope``: a
+    kda.Rope; ``quantized``: a cache in 8 bits), the others KDA."""
 
     def __init__(self, n_layers=4, heads=8, kv_heads=2, vocab=512, window=0, sinks=0, requests=8, pages=64,
-                 page_size=64, columns=16, seed=0):
+                 page_size=64, columns=16, seed=0, rope=None, quantized=False):
         g = torch.Generator(device="cuda").manual_seed(seed)
         w = lambda *s: (torch.randn(*s, generator=g, device="cuda") * s[0] ** -0.5).bfloat16()  # noqa: E731
         self.heads, self.kv_heads, self.hidden = heads, kv_heads, heads * D
-        self.window, self.sinks = window, sinks
+        self.window, self.sinks, self.rope = window, sinks, rope
         self.embed, self.head = w(vocab, self.hidden) * vocab ** 0.5, w(self.hidden, vocab)
         self.layers = []
         for i in range(n_layers):
             if i % 4 == 3:
-                kv = torch.zeros(2, pages, page_size, kv_heads, D, dtype=torch.bfloat16, device="cuda")
                 self.layers.append(dict(kind="attention", qkv=w(self.hidden, (heads + 2 * kv_heads) * D),
-                                        out=w(self.hidden, self.hidden), cache=kda.KvCache(kv[0], kv[1])))
+                                        out=w(self.hidden, self.hidden),
+                                        cache=kda.KvCache.empty(pages, page_size, kv_heads, quantized=quantized)))
             else:
                 self.layers.append(dict(
                     kind="kda", proj=w(self.hidden, 4 * self.hidden + heads), out=w(self.hidden, self.hidden),
                     A_log=torch.zeros(heads, device="cuda"), dt_bias=torch.zeros(heads, D, device="cuda"),
                     states=torch.zeros(requests, heads, D, D, device="cuda")))
         self.pages = kda.KvPages.empty(requests, columns, pages, page_size)
-        self.workspace = kda.paged_attention_workspace()
+        # of a step's tokens, where the cache is in 8 bits
+        self.workspace = kda.paged_attention_workspace(tokens=2048 if quantized else 0, heads=heads)
         self.rows = torch.arange(requests, dtype=torch.int32, device="cuda")
 
     def step(self, tokens, new_lens):
@@ -74,6 +77,8 @@ class HybridModel:
     def _attention(self, layer, y, cu, slots, kv_lens):
         qkv = (y @ layer["qkv"]).view(-1, self.heads + 2 * self.kv_heads, D)
         q, k, v = qkv.split((self.heads, self.kv_heads, self.kv_heads), 1)
+        if self.rope is not None:
+            kda.kda_rope(self.rope, q, k, cu_seqlens=cu, kv_lens=kv_lens, q_out=q, k_out=k)
         kda.kda_kv_append(layer["cache"], k, v, slots)
         return kda.kda_paged_attention(layer["cache"], q, cu, kv_lens, self.pages.block_table, window=self.window,
                                        sinks=self.sinks, workspace=self.workspace)[0]
@@ -137,6 +142,13 @@ def main():
         print(f"window {window}, {sinks} sinks: prompts in chunks of 128 against whole prompts, logits differ by "
               f"{worst:.2e} (relative norm); {free} of 64 pages free at the end; device status {status}")
         assert worst < 5e-2 and free == 64 and status == 0
+    rope = kda.Rope(kda.rope_frequencies(D, 5e5, factor=4.0, original_context=256))
+    wide = serve(HybridModel(rope=rope), texts, 256)
+    model = HybridModel(rope=rope, quantized=True)
+    narrow = serve(model, texts, 256)
+    apart = max(float((a - b).float().norm() / a.float().norm()) for a, b in zip(wide, narrow))
+    assert int(model.pages.free_count) == 64 and kda.kda_device_status() == 0
+    print(f"rotary positions, the cache in 8 bits against 16: logits differ by {apart:.2e} (relative norm)")
 
 
 if __name__ == "__main__":

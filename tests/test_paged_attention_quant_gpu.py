@@ -278,6 +278,15 @@ def test_rows_before_the_cache_begins():
     Case([300], [1], 4, 2, 64, FP16, seed=12).check(window=7, sinks=2)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("heads", [(1, 1), (4, 2), (3, 3), (6, 1)])
+def test_blocks_without_keys(heads, dtype):
+    """Whole blocks before position 0, of one tile and of two, wherever the cuts of
+    the line of work fall in them, among blocks that have keys."""
+    for extra in range(4):
+        Case([300 + 37 * extra, 2, 70 + extra, 129], [1, 0, extra, 400], *heads, 16, dtype, seed=extra).check()
+
+
 @pytest.mark.parametrize("page", [16, 64])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (90, 3)])
 @pytest.mark.parametrize("dtype", [BF16, FP16])
