@@ -2364,58 +2364,66 @@ static_assert(SMEM_BYTES8<false> <= 232448 && SMEM_BYTES8<true> <= 232448, "shar
 // left to the nearest e4m3 (4 significant bits).  Two parts are a bf16 number,
 // three an fp16 one, down to 2^-17 of the row's largest.  16 lanes a row.  Bound by
 // memory (256 bytes in, 256 or 384 out a row): 11,000 tokens of 32 heads 27 us.
+constexpr int SPLIT_ROWS = 4;  // that a thread has under way
 template <bool FP16>
 __global__ void __launch_bounds__(256) split_queries_kernel(AttentionParams p, uint8_t* parts, float* factors) {
   // In this order: the attention kernel may begin once all of this grid is past the
   // wait, and so after everything before this call.
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t i = blockIdx.x * 256ll + threadIdx.x, row = i >> 4, rows = (int64_t)p.t_total * p.hq;
-  const int c = (int)(i & 15) * 8;
-  if (row >= rows) return;  // 16 lanes alike
-  const int64_t tok = row / p.hq;
-  const int head = (int)(row % p.hq);
-  const uint4 raw = *reinterpret_cast<const uint4*>(p.q + tok * p.q_st + head * p.q_sh + c);
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  float x[8], top = 0.f;
-  bool finite = true;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 v = act_f2<FP16>(reinterpret_cast<const __nv_bfloat16*>(&w[k]));
-    x[2 * k] = v.x;
-    x[2 * k + 1] = v.y;
-  }
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    top = fmaxf(top, fabsf(x[k]));
-    finite = finite && fabsf(x[k]) < CUDART_INF_F;
-  }
+  const int64_t rows = (int64_t)p.t_total * p.hq, first = blockIdx.x * (16ll * SPLIT_ROWS) + (threadIdx.x >> 4);
+  const int c = (threadIdx.x & 15) * 8;
   const unsigned group = 0xffffu << (threadIdx.x & 16);
+  uint4 raw[SPLIT_ROWS];
 #pragma unroll
-  for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(group, top, d));
-  finite = __all_sync(group, finite);
-  const int e = max(-110, (__float_as_int(top) >> 23) - 127 - 7);  // of the row's power of two (0 and what is not finite: any)
-  const float down = __int_as_float((127 - (finite ? e : 0)) << 23);
-#pragma unroll
-  for (int part = 0; part < Q_PARTS<FP16>; ++part) {
-    uint32_t y[2];
-#pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      float a = part == 0 ? x[k] * down : x[k], b = part == 0 ? x[k + 1] * down : x[k + 1];
-      uint16_t two;
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(b), "f"(a));
-      uint32_t h;
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-      const float2 taken = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      x[k] = a - taken.x;
-      x[k + 1] = b - taken.y;
-      if (!finite) two = 0x7f7f;
-      if (k & 2) y[k >> 2] |= (uint32_t)two << 16;
-      else y[k >> 2] = two;
-    }
-    *reinterpret_cast<uint2*>(parts + ((int64_t)part * rows + row) * D + c) = make_uint2(y[0], y[1]);
+  for (int i = 0; i < SPLIT_ROWS; ++i) {
+    const int64_t row = first + i * 16, tok = row / p.hq;
+    if (row < rows) raw[i] = *reinterpret_cast<const uint4*>(p.q + tok * p.q_st + (row - tok * p.hq) * p.q_sh + c);
   }
-  if (c == 0) factors[row] = p.scale * LOG2E * __int_as_float((127 + (finite ? e : 0)) << 23);
+#pragma unroll
+  for (int i = 0; i < SPLIT_ROWS; ++i) {
+    const int64_t row = first + i * 16;
+    if (row >= rows) return;  // 16 lanes alike
+    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+    float x[8], top = 0.f;
+    bool finite = true;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 v = act_f2<FP16>(reinterpret_cast<const __nv_bfloat16*>(&w[k]));
+      x[2 * k] = v.x;
+      x[2 * k + 1] = v.y;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      top = fmaxf(top, fabsf(x[k]));
+      finite = finite && fabsf(x[k]) < CUDART_INF_F;
+    }
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(group, top, d));
+    finite = __all_sync(group, finite);
+    const int e = max(-110, (__float_as_int(top) >> 23) - 127 - 7);  // of the row's power of two (0 and what is not finite: any)
+    const float down = __int_as_float((127 - (finite ? e : 0)) << 23);
+#pragma unroll
+    for (int part = 0; part < Q_PARTS<FP16>; ++part) {
+      uint32_t y[2];
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) {
+        const float a = part == 0 ? x[k] * down : x[k], b = part == 0 ? x[k + 1] * down : x[k + 1];
+        uint16_t two;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(b), "f"(a));
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+        const float2 taken = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        x[k] = a - taken.x;
+        x[k + 1] = b - taken.y;
+        if (!finite) two = 0x7f7f;
+        if (k & 2) y[k >> 2] |= (uint32_t)two << 16;
+        else y[k >> 2] = two;
+      }
+      *reinterpret_cast<uint2*>(parts + ((int64_t)part * rows + row) * D + c) = make_uint2(y[0], y[1]);
+    }
+    if (c == 0) factors[row] = p.scale * LOG2E * __int_as_float((127 + (finite ? e : 0)) << 23);
+  }
 }
 
 int sm_count() {
@@ -2588,7 +2596,7 @@ int launch_attention_quant(const AttentionParams& a, const KvQuantCache& c, bool
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)((rows + 15) / 16));
+  cfg.gridDim = dim3((unsigned)((rows + 16 * SPLIT_ROWS - 1) / (16 * SPLIT_ROWS)));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = attr;
