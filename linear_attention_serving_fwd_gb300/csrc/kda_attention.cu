@@ -50,6 +50,27 @@
 // double the second product.  It takes the outputs' error against 64 bits from
 // 1.7e-3 (their own rounding) to 1.8e-3 of their norm in bf16, from 2.1e-4 to
 // 2.2e-4 in fp16.  Sums take the weights before they are rounded.
+//
+// The cache in 8 bits.  k_j = 2^e q_j with e4m3 numbers q_j and a scale for each 16
+// keys of a head, v_j likewise.  Its tiles (16 KB) go to the tensor cores as they
+// are, as operands of 8 bits, twice as many of which are multiplied at once; what
+// they are multiplied by is a sum of 8-bit numbers.
+// - A query row is a power of two times two e4m3 numbers (bf16: exact) or three
+//   (fp16), a kernel of its own: split_queries_kernel.
+// - The keys' scale and the row's are a factor of the score.  The values' is part
+//   of it: p_j = 2^(a s_j + log2 v_scale - m) is what the tensor cores take, and
+//   p_j / v_scale what the row's sum takes.
+// - A weight is formed in fp16 and taken as two e5m2 numbers (bf16: 2^-7 of it is
+//   left at most) or three (fp16: 2^-11).  e5m2 has fp16's exponents: thousands of weights
+//   2^-18 of the largest keep their bits, where two e4m3 numbers lost 9 % of
+//   them.  Outputs are 1.9e-3 to 2.1e-3 (bf16) and 2.2e-4 to 2.3e-4 (fp16) of their norm
+//   off 64 bits, 1.6e-3 and 2.0e-4 of it their own rounding.
+// So prompt chunks take as many tensor cycles as over 16 bits (fp16: half as many
+// again), and more work on the weights: 8192 tokens over 16384 of 32 heads 2.06 to
+// 2.10 ms (1335 to 1310 TFLOP/s), issue slots 63 % and tensor cores 53 % busy.
+// Single tokens read half the bytes: see NARROW_ROWS.  256 requests over 2.2 GB
+// 372 us, 5.9 TB/s; copies alone take 350 to 377 us by the chip (rows of 128 bytes, 1 KB
+// apart; 256-byte rows run at 6.9 TB/s in the same ring).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math_constants.h>
@@ -77,7 +98,9 @@ constexpr int LOAD_WARP = 16, PLAN_WARP = 17, MMA_WARP = 18;  // MMA_WARP + 1: t
 // prompts of 2048 tokens 246 -> 193 us, a window of 1024 over 8001 tokens 114 ->
 // 83 us, 128 single tokens 393 -> 369 us; 6 and 2, or 4 and 1, are 1 to 5 % behind.
 constexpr int LEAD_TWO = 4, LEAD_ONE = 2;
-// Over an 8-bit cache, where blocks differ more: what a key tile and the lead count.
+// Over an 8-bit cache, where blocks differ more: what a key tile and the lead count
+// (cost_two: a key tile of a block of two tiles).  A mixed batch of 64 requests takes
+// 221 us with 1 for all tiles, 158 so; a third more or less of any moves it by 2 %.
 constexpr int COST_NARROW8 = 2, COST_ONE8 = 3, LEAD_NARROW8 = 6, LEAD_ONE8 = 6, LEAD_TWO8 = 16;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // The running reference follows the row's maximum only when 64 weights have
@@ -146,7 +169,8 @@ constexpr int STAGES8 = FP16 ? 7 : 9;
 // thread has one key and all rows.  The streams take such blocks in turn, so that
 // one begins while the other ends; a stream's two warpgroups take its key tiles in
 // turn, each with a reference, sums and an O^T of its own, and their results are
-// joined in shared memory.
+// joined in shared memory.  256 single tokens of four heads a key head: 530 us with
+// a row a lane, 372 so, the tensor cores 4 % busy.
 constexpr int NARROW_ROWS = 16;
 // In the queries' buffer: those of two narrow blocks, so that the next one's are
 // there when it begins, and behind them the weights.

