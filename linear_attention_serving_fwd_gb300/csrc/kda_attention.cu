@@ -66,8 +66,11 @@
 //   them.  Outputs are 1.9e-3 to 2.1e-3 (bf16) and 2.2e-4 to 2.3e-4 (fp16) of their norm
 //   off 64 bits, 1.6e-3 and 2.0e-4 of it their own rounding.
 // So prompt chunks take as many tensor cycles as over 16 bits (fp16: half as many
-// again), and more work on the weights: 8192 tokens over 16384 of 32 heads 2.06 to
-// 2.10 ms (1335 to 1310 TFLOP/s), issue slots 63 % and tensor cores 53 % busy.
+// again), and more work on the weights, which is what bounds them: a key tile takes
+// a stream 1,100 cycles for the exponentials, 150 to agree on the reference and 1,400 for
+// the parts and what is around them, and the scores are always there.  8192 tokens
+// over 16384 of 32 heads 2.05 to 2.10 ms (1345 to 1310 TFLOP/s), issue slots 63 %
+// and tensor cores 53 % busy.
 // Single tokens read half the bytes: see NARROW_ROWS.  256 requests over 2.2 GB
 // 372 us, 5.9 TB/s; copies alone take 350 to 377 us by the chip (rows of 128 bytes, 1 KB
 // apart; 256-byte rows run at 6.9 TB/s in the same ring).
@@ -153,7 +156,7 @@ struct Smem {
 constexpr int TILE8_BYTES = KT * D, BLOCKS8 = KT / KDA_KV_BLOCK;
 constexpr int SCALES = 32;  // key tiles whose scales fit
 // When a tile's copy begins, the fifth before it is done with: its values' place is
-// in use again.
+// in use again (with nine places; with seven the fourth).
 constexpr int IN_FLIGHT = 5;
 template <bool FP16>
 constexpr int Q_PARTS = FP16 ? 3 : 2;
@@ -185,7 +188,7 @@ __host__ __device__ constexpr int columns(int octets, int parts) { return (octet
 template <bool FP16>
 constexpr int NARROW_W = columns(NARROW_ROWS / 8, W_PARTS<FP16>) * KT;  // bytes of a group's weights
 struct QuantSmem : Smem {
-  uint64_t full8[9], empty8[9];
+  uint64_t full8[STAGES8<false>], empty8[STAGES8<false>];
   // The scales of the key tiles to come, by the planning warp: a scale comes from
   // memory behind a page number, and where the copies keep memory busy that takes
   // 3 us and more, several tiles.
@@ -893,33 +896,32 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
         place = second + 1 == K::stages ? 0 : second + 1;
         parity = place == 0 ? second_parity ^ 1 : second_parity;
       }
-      if (!asked) queries();
-      continue;
-    }
-    // keys and values
-    for (int i = it.i0; i < it.i1; ++i, ++tiles) {
-      const int row = (list_tile(it, i) * KT) & (page - 1) & ~(box - 1);
-      const int c_page = __shfl_sync(0xffffffffu, pg < 0 ? p.a.n_pages : pg, p.joined ? lane : lane >> 1);
-      const unsigned held = __ballot_sync(0xffffffffu, pg >= 0);
-      pg = page_of(i + 1);
+    } else {
+      // keys and values
+      for (int i = it.i0; i < it.i1; ++i, ++tiles) {
+        const int row = (list_tile(it, i) * KT) & (page - 1) & ~(box - 1);
+        const int c_page = __shfl_sync(0xffffffffu, pg < 0 ? p.a.n_pages : pg, p.joined ? lane : lane >> 1);
+        const unsigned held = __ballot_sync(0xffffffffu, pg >= 0);
+        pg = page_of(i + 1);
 #pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv, ++fills) {
-        const uint32_t st = fills % K::stages;
-        const uint32_t parity = ((fills / K::stages) & 1) ^ 1;
-        if (!asked && __any_sync(0xffffffffu, queries_free() || !mbar_test_wait(K::empty(sm, st), parity))) queries();
-        if (!__all_sync(0xffffffffu, wait_or_stop(K::empty(sm, st), parity, sm, err))) goto out;
-        if (lane == 0) {
-          if (kv == 0) *(volatile int*)&sm.page_mask[tiles % MASKS] = (int)held;
-          mbar_arrive_expect_tx(K::full(sm, st), K::tile);
+        for (int kv = 0; kv < 2; ++kv, ++fills) {
+          const uint32_t st = fills % K::stages;
+          const uint32_t parity = ((fills / K::stages) & 1) ^ 1;
+          if (!asked && __any_sync(0xffffffffu, queries_free() || !mbar_test_wait(K::empty(sm, st), parity))) queries();
+          if (!__all_sync(0xffffffffu, wait_or_stop(K::empty(sm, st), parity, sm, err))) goto out;
+          if (lane == 0) {
+            if (kv == 0) *(volatile int*)&sm.page_mask[tiles % MASKS] = (int)held;
+            mbar_arrive_expect_tx(K::full(sm, st), K::tile);
+          }
+          __syncwarp();
+          if (p.joined) {  // a lane a box
+            if (lane < p.boxes)
+              tma_load5(kv_smem + st * TILE_BYTES + lane * box * 256, kv == 0 ? &maps.k : &maps.v,
+                        c_page * p.page_groups + (row >> 3), c_page * p.page_outer + it.kvh, &sm.kv_full[st]);
+          } else if (lane < 2 * p.boxes)  // page, half
+            tma_load4(kv_smem + st * TILE_BYTES + (lane & 1) * HALF_BYTES + (lane >> 1) * box * 128, kv == 0 ? &maps.k : &maps.v,
+                      (lane & 1) * 64, row, it.kvh, c_page, &sm.kv_full[st]);
         }
-        __syncwarp();
-        if (p.joined) {  // a lane a box
-          if (lane < p.boxes)
-            tma_load5(kv_smem + st * TILE_BYTES + lane * box * 256, kv == 0 ? &maps.k : &maps.v,
-                      c_page * p.page_groups + (row >> 3), c_page * p.page_outer + it.kvh, &sm.kv_full[st]);
-        } else if (lane < 2 * p.boxes)  // page, half
-          tma_load4(kv_smem + st * TILE_BYTES + (lane & 1) * HALF_BYTES + (lane >> 1) * box * 128, kv == 0 ? &maps.k : &maps.v,
-                    (lane & 1) * 64, row, it.kvh, c_page, &sm.kv_full[st]);
       }
     }
     if (!asked) queries();
@@ -1425,7 +1427,23 @@ __device__ __forceinline__ float row_factor(float sl, float ks) { return fmaxf(s
 // half of fp16 with its exponents, so that small weights keep their relative
 // precision.  Each part takes what is left to its nearest 3 significant bits (half
 // up, in fp16's bits): of an fp16 weight two parts leave at most 2^-7 of it, three 2^-11.
-// Four keys to a column, 16 columns to a part, w[c] are 32 keys two by two.
+// The next part of four weights, two by two in h, which keeps what is left of them
+// where more parts follow.
+template <bool MORE>
+__device__ __forceinline__ uint32_t next_part(uint32_t (&h)[2]) {
+  uint32_t r[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    r[k] = h[k] + 0x00800080u;
+    if constexpr (MORE) {
+      const uint32_t top = r[k] & 0xff00ff00u;
+      const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&h[k]), *reinterpret_cast<const __half2*>(&top));
+      h[k] = *reinterpret_cast<const uint32_t*>(&rest);
+    }
+  }
+  return __byte_perm(r[0], r[1], 0x7531);
+}
+// Four keys to a column, 16 columns to a part; w[c] are 32 keys two by two.
 template <int PARTS>
 __device__ __forceinline__ void store_parts(uint32_t t_s, uint32_t (&w)[2][16]) {
 #pragma unroll
@@ -1433,18 +1451,10 @@ __device__ __forceinline__ void store_parts(uint32_t t_s, uint32_t (&w)[2][16]) 
     uint32_t y[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      uint32_t r[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t& h = w[i >> 3][(i & 7) * 2 + k];
-        r[k] = h + 0x00800080u;
-        if (part + 1 < PARTS) {
-          const uint32_t top = r[k] & 0xff00ff00u;
-          const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&top));
-          h = *reinterpret_cast<const uint32_t*>(&rest);
-        }
-      }
-      y[i] = __byte_perm(r[0], r[1], 0x7531);
+      uint32_t h[2] = {w[i >> 3][(i & 7) * 2], w[i >> 3][(i & 7) * 2 + 1]};
+      y[i] = part + 1 < PARTS ? next_part<true>(h) : next_part<false>(h);
+      w[i >> 3][(i & 7) * 2] = h[0];
+      w[i >> 3][(i & 7) * 2 + 1] = h[1];
     }
     tmem_st16(t_s + part * 16, y);
   }
@@ -1739,18 +1749,10 @@ __device__ __forceinline__ void narrow_block(const Params& p, QuantSmem& sm, con
         uint32_t y[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          uint32_t t[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t& h = w[o * 4 + j * 2 + k];
-            t[k] = h + 0x00800080u;
-            if (part + 1 < W_PARTS<FP16>) {
-              const uint32_t top = t[k] & 0xff00ff00u;
-              const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&top));
-              h = *reinterpret_cast<const uint32_t*>(&rest);
-            }
-          }
-          y[j] = __byte_perm(t[0], t[1], 0x7531);
+          uint32_t h[2] = {w[o * 4 + j * 2], w[o * 4 + j * 2 + 1]};
+          y[j] = part + 1 < W_PARTS<FP16> ? next_part<true>(h) : next_part<false>(h);
+          w[o * 4 + j * 2] = h[0];
+          w[o * 4 + j * 2 + 1] = h[1];
         }
         const int column = part * RP + o * 8;
         *reinterpret_cast<uint2*>(weights + (column >> 4) * 2048 + (column & 8)) = make_uint2(y[0], y[1]);
@@ -2382,6 +2384,10 @@ static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 template <bool FP16>
 constexpr size_t SMEM_BYTES8 = 2 * Kind<FP16, true>::q_tile + STAGES8<FP16> * TILE8_BYTES + sizeof(QuantSmem);
 static_assert(SMEM_BYTES8<false> <= 232448 && SMEM_BYTES8<true> <= 232448, "shared memory of one CTA");
+static_assert(NARROW_P<false> + 4 * NARROW_W<false> <= Kind<false, true>::q_tile &&
+                  NARROW_P<true> + 4 * NARROW_W<true> <= Kind<true, true>::q_tile,
+              "narrow blocks' queries and weights in the first tile's place");
+static_assert(4 * NARROW_ROWS * D * 4 <= Kind<false, true>::q_tile, "their results in the second one's");
 
 // The queries of a call in 8-bit parts, [part][token][head][128], and each row's
 // factor: a row is taken to [2^7, 2^8) by a power of two, and every part what is

@@ -96,7 +96,6 @@ struct RopeParams {
   const int32_t* kv_lens;
   int n_req;
   int tokens;                 // of a CTA
-  unsigned* err;
 };
 
 int launch_kv_extend(const KvPagesParams& p, cudaStream_t stream);

@@ -417,8 +417,6 @@ int kda_rope(const kda_rotation* rotation, int32_t dtype, const void* q, int64_t
   p.turns = reinterpret_cast<const unsigned long long*>(rotation->turns);
   p.amplitude = rotation->amplitude;
   p.positions = positions; p.cu_seqlens = cu_seqlens; p.kv_lens = kv_lens; p.n_req = n_req;
-  p.err = kda::device_error_word();
-  if (!p.err) return fail(KDA_ERR_CUDA, "cannot resolve the device error word.");
   if (kda::launch_rope(p, rotation->interleaved != 0, dtype == KDA_DTYPE_FP16, static_cast<cudaStream_t>(stream)) != 0)
     return cuda_fail("kda_rope launch");
   return ok();

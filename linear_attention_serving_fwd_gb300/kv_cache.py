@@ -22,6 +22,7 @@ from . import _native
 
 D = 128
 BLOCK = 16  # rows of a page that share a scale in an 8-bit cache
+ZEROED = 4096  # bytes of an attention workspace that are zero before its first call
 _DTYPES = {torch.bfloat16: _native.KDA_DTYPE_BF16, torch.float16: _native.KDA_DTYPE_FP16}
 
 
@@ -261,8 +262,10 @@ def paged_attention_workspace(device=None, *, tokens: int = 0, heads: int = 0) -
     with torch.cuda.device(device):  # the size goes by the current device
         if tokens:
             n = int(_native.lib().kda_paged_attention_quant_workspace_bytes(tokens, heads))
-        else:
-            n = int(_native.lib().kda_paged_attention_workspace_bytes())
+            workspace = torch.empty(n, dtype=torch.uint8, device=device)
+            workspace[:ZEROED].zero_()  # the rest grows with the tokens
+            return workspace
+        n = int(_native.lib().kda_paged_attention_workspace_bytes())
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
