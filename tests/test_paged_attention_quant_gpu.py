@@ -458,6 +458,22 @@ def test_one_workspace_for_calls_of_all_shapes_and_both_caches():
     assert not ws[:4096].any()
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_a_workspace_holds_anything_past_its_first_bytes(dtype):
+    """Blocks cut in parts, some of them without keys, over a workspace whose rest is all ones (a
+    NaN in each of its types): the same bits as over zeros."""
+    cases = [Case([1], [9000], 4, 1, 64, dtype, seed=24), Case([300, 2, 70, 129], [1, 0, 1, 400], 3, 3, 16, dtype, seed=25),
+             Case([700, 1, 300], [2900, 2000, 100], 2, 2, 64, dtype, seed=26)]
+    for c in cases:
+        zeros = kda.paged_attention_workspace(tokens=1001, heads=9)
+        zeros.zero_()
+        ones = torch.full_like(zeros, 255)
+        ones[:4096] = 0
+        want, got = c.run(workspace=zeros), c.run(workspace=ones)
+        c.check(result=got)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_other_stream_and_graph():
     c = Case([1, 2, 150], [800, 700, 300], 4, 2, 64, seed=24)
     want = c.run()
