@@ -52,25 +52,31 @@
 // 2.2e-4 in fp16.  Sums take the weights before they are rounded.
 //
 // The cache in 8 bits.  k_j = 2^e q_j with e4m3 numbers q_j and a scale for each 16
-// keys of a head, v_j likewise.  Its tiles (16 KB) go to the tensor cores as they
-// are, as operands of 8 bits, twice as many of which are multiplied at once; what
-// they are multiplied by is a sum of 8-bit numbers.
-// - A query row is a power of two times two e4m3 numbers (bf16: exact) or three
-//   (fp16), a kernel of its own: split_queries_kernel.
+// keys of a head, v_j likewise; tiles of 16 KB.
+// - The keys go to the tensor cores as they are, as operands of 8 bits, twice as many
+//   of which are multiplied at once; a query row is a power of two times the sum of
+//   two e4m3 numbers (bf16: exact) or three (fp16), by a kernel of its own,
+//   split_queries_kernel.
 // - The keys' scale and the row's are a factor of the score.  The values' is part
 //   of it: p_j = 2^(a s_j + log2 v_scale - m) is what the tensor cores take, and
 //   p_j / v_scale what the row's sum takes.
-// - A weight is formed in fp16 and taken as two e5m2 numbers (bf16: 2^-7 of it is
-//   left at most) or three (fp16: 2^-11).  e5m2 has fp16's exponents: thousands of weights
-//   2^-18 of the largest keep their bits, where two e4m3 numbers lost 9 % of
-//   them.  Outputs are 1.9e-3 to 2.1e-3 (bf16) and 2.2e-4 to 2.3e-4 (fp16) of their norm
-//   off 64 bits, 1.6e-3 and 2.0e-4 of it their own rounding.
-// So prompt chunks take as many tensor cycles as over 16 bits (fp16: half as many
-// again), and more work on the weights, which is what bounds them: a key tile takes
-// a stream 1,100 cycles for the exponentials, 150 to agree on the reference and 1,400 for
-// the parts and what is around them, and the scores are always there.  8192 tokens
-// over 16384 of 32 heads 2.05 to 2.10 ms (1345 to 1310 TFLOP/s), issue slots 63 %
-// and tensor cores 53 % busy.
+// - The weights are fp16, and so are the values once the softmax warps have widened
+//   them (exactly), a sixteenth of a tile each, while they wait for its scores: 30
+//   instructions a thread.  The values as they are, with weights as sums of two or
+//   three 8-bit numbers, took 160 and more of them, between the scores and
+//   the product (8192 tokens over 16384 2.06 -> 1.95 ms); widened by the issuing warps,
+//   2.65 ms.
+// - In narrow blocks (see NARROW_ROWS) weights are few and the values many: there a
+//   weight is formed in fp16 and taken as two e5m2 numbers (bf16: 2^-7 of it is left at
+//   most) or three (fp16: 2^-11).  e5m2 has fp16's exponents: thousands of weights
+//   2^-18 of the largest keep their bits, where two e4m3 numbers lost 9 % of them.
+// Outputs are off 64 bits by 1.6e-3 of their norm (bf16) and 2.1e-4 (fp16), all but their
+// own rounding (1.6e-3, 2.0e-4); those of narrow blocks by 2.1e-3 and 2.3e-4.
+// So prompt chunks take as many tensor cycles as over 16 bits (fp16: a quarter more),
+// and are bound by the same chain of scores, weights and product, with the values' part
+// in it: of a key tile's 3,300 cycles a stream spends 1,400 on weights, 200 on their
+// store and the rest on the next scores, during which it widens values.  8192 tokens over
+// 16384 of 32 heads 1.95 to 1.99 ms (1410 to 1380 TFLOP/s).
 // Single tokens read half the bytes: see NARROW_ROWS.  256 requests over 2.2 GB
 // 372 us, 5.9 TB/s; copies alone take 350 to 377 us by the chip (rows of 128 bytes, 1 KB
 // apart; 256-byte rows run at 6.9 TB/s in the same ring).
@@ -155,13 +161,14 @@ struct Smem {
 // A query tile takes two places of 16 KB (bf16) or three (fp16).
 constexpr int TILE8_BYTES = KT * D, BLOCKS8 = KT / KDA_KV_BLOCK;
 constexpr int SCALES = 32;  // key tiles whose scales fit
-// When a tile's copy begins, the fifth before it is done with: its values' place is
-// in use again (with nine places; with seven the fourth).
+// When a tile's copy begins, the fifth before it is done with: its first place was the
+// values' of that one, where tiles take two of nine places each (of seven: of the
+// fourth), and a later one's where they take three.
 constexpr int IN_FLIGHT = 5;
 template <bool FP16>
 constexpr int Q_PARTS = FP16 ? 3 : 2;
 template <bool FP16>
-constexpr int W_PARTS = FP16 ? 3 : 2;
+constexpr int W_PARTS = FP16 ? 3 : 2;  // narrow blocks
 template <bool FP16>
 constexpr int STAGES8 = FP16 ? 7 : 9;
 // Narrow blocks: few rows (single tokens, short windows) over an 8-bit cache.  A
@@ -189,6 +196,7 @@ template <bool FP16>
 constexpr int NARROW_W = columns(NARROW_ROWS / 8, W_PARTS<FP16>) * KT;  // bytes of a group's weights
 struct QuantSmem : Smem {
   uint64_t full8[STAGES8<false>], empty8[STAGES8<false>];
+  uint64_t wide_full[STAGES8<false>];  // the values copied to this place are there in fp16
   // The scales of the key tiles to come, by the planning warp: a scale comes from
   // memory behind a page number, and where the copies keep memory busy that takes
   // 3 us and more, several tiles.
@@ -379,14 +387,6 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a_desc, uint64_t b_d
       "setp.ne.u32 p, %4, 0;\n"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
       "}\n" ::"r"(d), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
-}
-__device__ __forceinline__ void mma_f8_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n"
-      ".reg .pred p;\n"
-      "setp.ne.u32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n"
-      "}\n" ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 // Instruction descriptor of kind::f8f6f4 with fp32 accumulation.
 constexpr uint32_t E4M3 = 0, E5M2 = 1, A_MN_MAJOR = 1u << 15, B_MN_MAJOR = 1u << 16;
@@ -855,6 +855,9 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
       __syncwarp();
     };
     if constexpr (QUANT) {
+      // Places of the ring: a narrow block's tile takes one for the keys and one for the
+      // values; another's, whose values are widened to two places, one for the keys
+      // and two, the second of which their copy goes to.
       // A tile's keys and values in one step, a lane a box of either: at half the
       // bytes a tile, two steps took longer than the memory (1600 cycles a tile
       // against 700 with pages of 64).  The page number is not looked at before the step
@@ -870,32 +873,40 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
         const int key = list_tile(it, i) * KT + my_box * box;
         return (key < it.hi && key + box > it.lo) || key < it.sink_hi ? table[key >> p.a.page_shift] : -1;
       };
-      int next = entry(it.i0);
-      for (int i = it.i0; i < it.i1; ++i, ++tiles, fills += 2) {
-        const int now = next;
-        next = entry(i + 1);
-        if (!asked && __any_sync(0xffffffffu, queries_free() || !mbar_test_wait(K::empty(sm, place), parity ^ 1))) queries();
-        const uint32_t second = place + 1 == K::stages ? 0 : place + 1, second_parity = second == 0 ? parity ^ 1 : parity;
-        if (!__all_sync(0xffffffffu, wait_or_stop(K::empty(sm, place), parity ^ 1, sm, err) &&
-                                         wait_or_stop(K::empty(sm, second), second_parity ^ 1, sm, err)))
-          goto out;
-        if (lane == 0) {
-          store_release(&qs.copied, (int)tiles);
-          mbar_arrive_expect_tx(K::full(sm, place), K::tile);
-          mbar_arrive_expect_tx(K::full(sm, second), K::tile);
+      auto copy = [&](auto wide) {  // false: the CTA is marked
+        int next = entry(it.i0);
+        for (int i = it.i0; i < it.i1; ++i, ++tiles, fills += wide ? 3 : 2) {
+          const int now = next;
+          next = entry(i + 1);
+          if (!asked && __any_sync(0xffffffffu, queries_free() || !mbar_test_wait(K::empty(sm, place), parity ^ 1))) queries();
+          const uint32_t middle = place + 1 == K::stages ? 0 : place + 1, middle_parity = middle == 0 ? parity ^ 1 : parity;
+          const uint32_t second = !wide ? middle : middle + 1 == K::stages ? 0 : middle + 1;
+          const uint32_t second_parity = wide && second == 0 ? middle_parity ^ 1 : middle_parity;
+          if (!__all_sync(0xffffffffu, wait_or_stop(K::empty(sm, place), parity ^ 1, sm, err) &&
+                                           (!wide || wait_or_stop(K::empty(sm, middle), middle_parity ^ 1, sm, err)) &&
+                                           wait_or_stop(K::empty(sm, second), second_parity ^ 1, sm, err)))
+            return false;
+          if (lane == 0) {
+            store_release(&qs.copied, (int)tiles);
+            mbar_arrive_expect_tx(K::full(sm, place), K::tile);
+            if (wide) mbar_arrive(K::full(sm, middle));  // a fill without a copy, before the one that is waited for
+            mbar_arrive_expect_tx(K::full(sm, second), K::tile);
+          }
+          if (now >= p.a.n_pages) set_error(err, ERR_INDEX);
+          __syncwarp();
+          if (copies) {
+            const int row = (list_tile(it, i) * KT) & (page - 1) & ~(box - 1);
+            const uint32_t st = values ? second : place;
+            const int pg = now < 0 || now > p.a.n_pages ? p.a.n_pages : now;
+            if (wide) tma_load4(to + st * K::tile, map, 0, row, it.kvh, pg, K::full(sm, st));
+            else tma_load4_once(to + st * K::tile, map, 0, row, it.kvh, pg, K::full(sm, st), policy);
+          }
+          place = second + 1 == K::stages ? 0 : second + 1;
+          parity = place == 0 ? second_parity ^ 1 : second_parity;
         }
-        if (now >= p.a.n_pages) set_error(err, ERR_INDEX);
-        __syncwarp();
-        if (copies) {
-          const int row = (list_tile(it, i) * KT) & (page - 1) & ~(box - 1);
-          const uint32_t st = values ? second : place;
-          const int pg = now < 0 || now > p.a.n_pages ? p.a.n_pages : now;
-          if (narrow) tma_load4_once(to + st * K::tile, map, 0, row, it.kvh, pg, K::full(sm, st), policy);
-          else tma_load4(to + st * K::tile, map, 0, row, it.kvh, pg, K::full(sm, st));
-        }
-        place = second + 1 == K::stages ? 0 : second + 1;
-        parity = place == 0 ? second_parity ^ 1 : second_parity;
-      }
+        return true;
+      };
+      if (!(narrow ? copy(std::false_type()) : copy(std::true_type()))) goto out;
     } else {
       // keys and values
       for (int i = it.i0; i < it.i1; ++i, ++tiles) {
@@ -969,14 +980,14 @@ struct Stage {
 };
 
 template <bool FP16, bool QUANT>
-__device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint32_t q_addr, uint32_t kv_addr, uint32_t tmem,
+__device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint32_t q_addr, unsigned char* kv_smem, uint32_t tmem,
                                          uint32_t bf16) {
   using K = Kind<FP16, QUANT>;
   using Stage = Stage<K::stages>;
   unsigned* err = p.a.err;
   const uint32_t id_qk = QUANT ? idesc_f8(ROWS, KT, E4M3, E4M3) : tc::idesc_f16(ROWS, KT, bf16);
-  const uint32_t id_pv = (QUANT ? idesc_f8(ROWS, D, E5M2, E4M3) : tc::idesc_f16(ROWS, D, bf16)) | B_MN_MAJOR;
-  const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * 128;
+  const uint32_t id_pv = tc::idesc_f16(ROWS, D, QUANT ? 0u : bf16) | B_MN_MAJOR;
+  const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * 128, kv_addr = smem_u32(kv_smem);
   Stage next;  // of list index i0 of the next item
   uint32_t q_parity = 0, p_parity = 0, o_parity = 1;
   uint32_t narrow_parity = 0;  // of the two warpgroups' weights, a bit each
@@ -984,6 +995,9 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
   const uint64_t k_desc = smem_desc_rows(kv_addr, p.group_bytes, p.half_bytes, false);
   const uint64_t v_desc = smem_desc_rows(kv_addr, p.group_bytes, p.half_bytes, true);
   const uint32_t k_half = (uint32_t)p.half_bytes >> 4, v_step = (uint32_t)p.group_bytes >> 3;  // 16 keys: two groups
+  constexpr int PLACES = QUANT ? 3 : 2;  // of a key tile in the ring
+  const uint64_t wide_desc = smem_desc_rows(kv_addr, 1024, TILE8_BYTES, true);
+  uint32_t wide_parity = 0;  // a bit a place
   auto await = [&](uint64_t* bar, uint32_t parity) { warp_wait(bar, parity, sm, err); };
   // In blocks of two tiles the streams take turns at the tensor cores, key tile
   // by key tile: a product of one and its next scores go in a row.  Left to mix,
@@ -1139,16 +1153,22 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
       }
       __syncwarp();
     };
-    for (int i = it.i0; i < it.i1; ++i, st.skip(2)) {
+    for (int i = it.i0; i < it.i1; ++i, st.skip(PLACES)) {
       Stage sv = st;
-      sv.skip(1);
+      sv.skip(PLACES - 1);
+      const uint32_t middle = st.at + 1 == K::stages ? 0 : st.at + 1;  // in 8 bits, for half of the wide values
       if (two ? !active(act, i) : ((i - it.i0) & 1) != odd) {
         // hidden from every row, or the other stream's: both streams see every
         // fill, so that none is two fills behind (a wait tells odd from even)
         await(K::full(sm, st.at), st.parity);
         await(K::full(sm, sv.at), sv.parity);
+        if constexpr (QUANT) {
+          await(&static_cast<QuantSmem&>(sm).wide_full[sv.at], (wide_parity >> sv.at) & 1);
+          wide_parity ^= 1u << sv.at;
+        }
         if (elect_one()) {
           mbar_arrive(K::empty(sm, st.at));
+          if constexpr (QUANT) mbar_arrive(K::empty(sm, middle));
           mbar_arrive(K::empty(sm, sv.at));
         }
         __syncwarp();
@@ -1174,27 +1194,33 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
         await(&sm.o_free[s], o_parity);
         o_parity ^= 1;
       }
-      const uint64_t vd = v_desc + sv.at * (K::tile >> 4);
       if (two) {
         await(&sm.turn[s], turn);
         turn ^= 1;
       }
       await(&sm.p_full[s], p_parity);
       p_parity ^= 1;
+      if constexpr (QUANT) {
+        await(&static_cast<QuantSmem&>(sm).wide_full[sv.at], (wide_parity >> sv.at) & 1);
+        wide_parity ^= 1u << sv.at;
+      }
       tc::fence_after_sync();
       if (elect_one()) {
-        if constexpr (QUANT) {
+        // 16 keys: two 8-row groups of V
+        if (!QUANT || sv.at > 0) {
+          const uint64_t vd = QUANT ? wide_desc + middle * (K::tile >> 4) : v_desc + sv.at * (K::tile >> 4);
+          const uint32_t step = QUANT ? 2 * 1024 >> 4 : v_step;
 #pragma unroll
-          for (int j = 0; j < KT / 32; ++j)  // 32 keys: four 8-row groups of V, 8 columns of each part of the weights
+          for (int j = 0; j < KT / 16; ++j)
+            mma_f16_ts(t_o, t_s + (j >> 2) * 64 + (j & 3) * 8, vd + j * step, id_pv, (j > 0 || !first) ? 1u : 0u);
+        } else {  // the halves at the ring's two ends
 #pragma unroll
-            for (int part = 0; part < W_PARTS<FP16>; ++part)
-              mma_f8_ts(t_o, t_s + (j >> 1) * 64 + part * 16 + (j & 1) * 8, vd + j * 2 * v_step, id_pv,
-                        (j > 0 || part > 0 || !first) ? 1u : 0u);
-        } else {
-#pragma unroll
-          for (int j = 0; j < KT / 16; ++j)  // 16 keys: two 8-row groups of V
-            mma_f16_ts(t_o, t_s + (j >> 2) * 64 + (j & 3) * 8, vd + j * v_step, id_pv, (j > 0 || !first) ? 1u : 0u);
+          for (int j = 0; j < 2 * (KT / 16); ++j)
+            mma_f16_ts(t_o + (j & 1) * 64, t_s + (j >> 3) * 64 + (j >> 1 & 3) * 8,
+                       wide_desc + (j & 1 ? 0 : middle) * (K::tile >> 4) + (j >> 1) * (2 * 1024 >> 4),
+                       tc::idesc_f16(ROWS, D / 2, 0) | B_MN_MAJOR, (j > 1 || !first) ? 1u : 0u);
         }
+        if constexpr (QUANT) tc::mma_commit(K::empty(sm, middle));
         tc::mma_commit(K::empty(sm, sv.at));
       }
       __syncwarp();
@@ -1443,21 +1469,37 @@ __device__ __forceinline__ uint32_t next_part(uint32_t (&h)[2]) {
   }
   return __byte_perm(r[0], r[1], 0x7531);
 }
-// Four keys to a column, 16 columns to a part; w[c] are 32 keys two by two.
-template <int PARTS>
-__device__ __forceinline__ void store_parts(uint32_t t_s, uint32_t (&w)[2][16]) {
+
+// Eight rows of an 8-bit values' tile, from row ``from`` on, to fp16, zeros from row
+// ``end`` on: dimensions 0 - 63 of a row to the place before, 64 - 127 to where the
+// row was (each 128 bytes, swizzled alike).  By one warp, 8 lanes a row.
+__device__ __forceinline__ void widen_values(unsigned char* kv_smem, uint32_t at, uint32_t places, int from, int end) {
+  const int lane = threadIdx.x & 31, j = lane & 7;
+  unsigned char* raw = kv_smem + at * TILE8_BYTES;
+  unsigned char* to = j < 4 ? kv_smem + (at == 0 ? places - 1 : at - 1) * TILE8_BYTES : raw;
+  uint4 x[2];
 #pragma unroll
-  for (int part = 0; part < PARTS; ++part) {
-    uint32_t y[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      uint32_t h[2] = {w[i >> 3][(i & 7) * 2], w[i >> 3][(i & 7) * 2 + 1]};
-      y[i] = part + 1 < PARTS ? next_part<true>(h) : next_part<false>(h);
-      w[i >> 3][(i & 7) * 2] = h[0];
-      w[i >> 3][(i & 7) * 2 + 1] = h[1];
-    }
-    tmem_st16(t_s + part * 16, y);
+  for (int i = 0; i < 2; ++i) {
+    const int r = from + 4 * i + (lane >> 3);
+    x[i] = *reinterpret_cast<const uint4*>(raw + r * 128 + ((j ^ (r & 7)) << 4));
+    if (r >= end) x[i] = make_uint4(0, 0, 0, 0);
   }
+  __syncwarp();  // a row's lanes have read it
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = from + 4 * i + (lane >> 3);
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    uint32_t h[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[k]) : "h"((uint16_t)(w[k >> 1] >> (k & 1) * 16)));
+    // lanes j and j + 4 take their two pieces in opposite orders: no bank conflicts
+    const int c = 2 * (j & 3), second = j >> 2;
+    const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
+    *reinterpret_cast<uint4*>(to + r * 128 + (((c + second) ^ (r & 7)) << 4)) = second ? b : a;
+    *reinterpret_cast<uint4*>(to + r * 128 + (((c + 1 - second) ^ (r & 7)) << 4)) = second ? a : b;
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
 }
 
 // --- a softmax warpgroup -----------------------------------------------------------------
@@ -1906,9 +1948,21 @@ __device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigne
     // the last joined results have been read (where they are, and what was told
     // with them, is written anew)
     warp_wait(&sm.merge_free, (merges & 1) ^ 1, sm, err);
-    for (int i = two ? i0 : i0 + odd; i < i1; i += two ? 1 : 2) {
-      if (two && !active(it.act[s], i)) continue;
+    // over 8 bits the streams' warps share every tile's values
+    for (int i = QUANT || two ? i0 : i0 + odd; i < i1; i += QUANT || two ? 1 : 2) {
       const int first_key = list_tile(it, i) * KT, key = first_key + half * 64;
+      if constexpr (QUANT) {
+        // Each takes eight rows to fp16 (a tile's places: keys, half of the wide
+        // values, values), while its scores are on their way.
+        const uint32_t f = fills + 3 * (i - i0) + 2, at = f % K::stages;
+        // These warps do not see narrow blocks' copies, and a wait tells odd fills from
+        // even: until the ring has gone round, the copy has to have begun.
+        if (i - i0 < 3) wait_count(&static_cast<QuantSmem&>(sm).copied, (int)(tiles + i - i0), sm, err);
+        warp_wait(K::full(sm, at), (f / K::stages) & 1, sm, err);
+        widen_values(kv_smem, at, K::stages, (threadIdx.x >> 5) * 8, kv - first_key);
+        if (lane == 0) mbar_arrive(&static_cast<QuantSmem&>(sm).wide_full[at]);
+      }
+      if (two ? !active(it.act[s], i) : QUANT && ((i - i0) & 1) != odd) continue;
       const bool clear = first_key <= clear_hi && (first_key >= clear_lo || first_key <= clear_sink);
       int held = 0;
       const uint32_t scales = QUANT ? (tiles + i - i0) % SCALES : 0;
@@ -1923,22 +1977,17 @@ __device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigne
       warp_wait(&sm.s_full[s], s_count & 1, sm, err);
       ++s_count;
       tc::fence_after_sync();
-      if (key + 64 > kv) {
+      if (!QUANT && key + 64 > kv) {
         // the rows past the cached tokens hold whatever was there: zeros there
         // keep the products finite
         const uint32_t f = fills + 2 * (i - i0) + 1;
         wait(K::full(sm, f % K::stages), (f / K::stages) & 1, sm, err);
         const int from = max(0, kv - key);
         unsigned char* v = kv_smem + (f % K::stages) * K::tile;
-        if constexpr (QUANT) {
-          for (int c = r; c < (64 - from) * 8; c += 128)
-            *reinterpret_cast<int4*>(v + (half * 64 + from) * 128 + c * 16) = make_int4(0, 0, 0, 0);
-        } else {
-          for (int c = r; c < (64 - from) * 16; c += 128) {
-            const int row = half * 64 + from + (c >> 4);
-            *reinterpret_cast<int4*>(v + (row >> 3) * p.group_bytes + ((c >> 3) & 1) * p.half_bytes + (row & 7) * 128 + (c & 7) * 16) =
-                make_int4(0, 0, 0, 0);
-          }
+        for (int c = r; c < (64 - from) * 16; c += 128) {
+          const int row = half * 64 + from + (c >> 4);
+          *reinterpret_cast<int4*>(v + (row >> 3) * p.group_bytes + ((c >> 3) & 1) * p.half_bytes + (row & 7) * 128 + (c & 7) * 16) =
+              make_int4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -2076,12 +2125,8 @@ __device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigne
         }
         l += sum[0].x;
         // they take the place of the first 32 of this half's columns of S
-        if constexpr (QUANT) {
-          store_parts<W_PARTS<FP16>>(t_s, w);
-        } else {
-          tmem_st16(t_s, w[0]);
-          tmem_st16(t_s + 16, w[1]);
-        }
+        tmem_st16(t_s, w[0]);
+        tmem_st16(t_s + 16, w[1]);
         tmem_wait_st();
       }
       stepped = true;
@@ -2089,7 +2134,7 @@ __device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigne
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.p_full[s]);
     }
-    fills += 2 * (i1 - i0);
+    fills += (QUANT ? 3 : 2) * (i1 - i0);
     tiles += i1 - i0;
     if (stepped) {
       // The row's sum goes where the maximum was: the other half may have yet to
@@ -2246,7 +2291,7 @@ __device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigne
   return false;
 }
 
-// Out of line, so that the narrow blocks' calls cost the loop above no registers.
+// With a copy of the counts, so that the narrow blocks' calls cost the loop above no registers.
 template <bool FP16>
 __device__ __forceinline__ bool wide_items(const Params& p, QuantSmem& sm, unsigned char* q_smem, unsigned char* kv_smem, uint32_t tmem,
                                         Counts& n) {
@@ -2345,6 +2390,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(&sm.narrow_q_empty[i], 2);  // both streams
       }
       for (int i = 0; i < SCALES; ++i) mbar_init(&sm.scales_full[i], 1);
+      for (int i = 0; i < K::stages; ++i) mbar_init(&sm.wide_full[i], SOFTMAX_WARPS);
       sm.copied = sm.narrow_done[0] = sm.narrow_done[1] = 0;
     }
     sm.dead = sm.beat = 0;
@@ -2368,7 +2414,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp == LOAD_WARP) {
     load_role<FP16, QUANT>(p, maps, sm, q_smem, kv_smem);
   } else if (warp >= MMA_WARP) {
-    mma_role<FP16, QUANT>(p, sm, warp - MMA_WARP, smem_u32(q_smem), smem_u32(kv_smem), tmem, FP16 ? 0u : 1u);
+    mma_role<FP16, QUANT>(p, sm, warp - MMA_WARP, smem_u32(q_smem), kv_smem, tmem, FP16 ? 0u : 1u);
   } else if (warp == PLAN_WARP) {
     plan_role<QUANT>(p, sm, blockIdx.x, piece);
   }
@@ -2606,7 +2652,7 @@ int launch_attention_quant(const AttentionParams& a, const KvQuantCache& c, bool
   Params p = {};
   plan_call(p, a, workspace);
   p.c = c;
-  p.cost_two = fp16 ? 8 : 6;
+  p.cost_two = fp16 ? 6 : 6;
   p.min_piece *= COST_NARROW8;
   const int page = 1 << a.page_shift, box = page < KT ? page : KT, parts = fp16 ? Q_PARTS<true> : Q_PARTS<false>;
   p.group_bytes = 1024;
