@@ -1472,31 +1472,25 @@ __device__ __forceinline__ uint32_t next_part(uint32_t (&h)[2]) {
 
 // Eight rows of an 8-bit values' tile, from row ``from`` on, to fp16, zeros from row
 // ``end`` on: dimensions 0 - 63 of a row to the place before, 64 - 127 to where the
-// row was (each 128 bytes, swizzled alike).  By one warp, 8 lanes a row.
+// row was (each 128 bytes, swizzled alike).  By one warp, 4 lanes a row; 8 lanes side
+// by side have the same piece of all rows, which the swizzle spreads over the banks.
 __device__ __forceinline__ void widen_values(unsigned char* kv_smem, uint32_t at, uint32_t places, int from, int end) {
-  const int lane = threadIdx.x & 31, j = lane & 7;
-  unsigned char* raw = kv_smem + at * TILE8_BYTES;
-  unsigned char* to = j < 4 ? kv_smem + (at == 0 ? places - 1 : at - 1) * TILE8_BYTES : raw;
-  uint4 x[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = from + 4 * i + (lane >> 3);
-    x[i] = *reinterpret_cast<const uint4*>(raw + r * 128 + ((j ^ (r & 7)) << 4));
-    if (r >= end) x[i] = make_uint4(0, 0, 0, 0);
-  }
+  const int lane = threadIdx.x & 31, row = lane & 7, j = lane >> 3;
+  const uint32_t first = from * 128 + row * 128, c = (j ^ row) << 4, to = (2 * j ^ row) << 4;
+  unsigned char* upper = kv_smem + at * TILE8_BYTES + first;
+  unsigned char* lower = kv_smem + (at == 0 ? places - 1 : at - 1) * TILE8_BYTES + first;
+  uint4 x[2] = {*reinterpret_cast<const uint4*>(upper + c), *reinterpret_cast<const uint4*>(upper + (c ^ 64))};
+  if (from + row >= end) x[0] = x[1] = make_uint4(0, 0, 0, 0);
   __syncwarp();  // a row's lanes have read it
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int r = from + 4 * i + (lane >> 3);
     const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
     uint32_t h[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[k]) : "h"((uint16_t)(w[k >> 1] >> (k & 1) * 16)));
-    // lanes j and j + 4 take their two pieces in opposite orders: no bank conflicts
-    const int c = 2 * (j & 3), second = j >> 2;
-    const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
-    *reinterpret_cast<uint4*>(to + r * 128 + (((c + second) ^ (r & 7)) << 4)) = second ? b : a;
-    *reinterpret_cast<uint4*>(to + r * 128 + (((c + 1 - second) ^ (r & 7)) << 4)) = second ? a : b;
+    unsigned char* row_at = i == 0 ? lower : upper;
+    *reinterpret_cast<uint4*>(row_at + to) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(row_at + (to ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
   }
   fence_proxy_async_smem();
   __syncwarp();

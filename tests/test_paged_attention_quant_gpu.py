@@ -575,6 +575,19 @@ def test_many_blocks_of_one_tile(rows, dtype):
         assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("kv,page", [(700, 16), (3000, 64), (6100, 128)])
+def test_small_blocks_with_long_caches_before_large_ones(kv, page, dtype):
+    """Blocks of few rows go to one stream; the other comes to the next block, with many
+    rows, long before its keys and values do."""
+    c = Case([1, 40, 2, 90] * 12, [kv, 300, kv + 90, 95] * 12, 4, 2, page, dtype, seed=page)
+    first = c.run()
+    c.check(result=first)
+    for _ in range(10):
+        again = c.run()
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
 # --- a serving step: turned, written, attended to, read back --------------------------
 
 @pytest.mark.parametrize("dtype", [BF16, FP16])
