@@ -201,6 +201,7 @@ struct QuantSmem : Smem {
   // memory behind a page number, and where the copies keep memory busy that takes
   // 3 us and more, several tiles.
   uint64_t scales_full[SCALES];
+  int4 clear[SOFTMAX_WARPS];              // bounds of the key tiles that a warp's rows see whole: no registers left for them
   float4 k_scale[SCALES][BLOCKS8 / 4];    // of each block of 16 keys
   float4 v_log[SCALES][BLOCKS8 / 4];      // the scale of its values in powers of two,
   float4 v_inverse[SCALES][BLOCKS8 / 4];  // and what takes it out of their weights' sum
@@ -1894,7 +1895,13 @@ __device__ __forceinline__ void join_groups(const Params& p, QuantSmem& sm, cons
 
 // What the softmax warps count.
 struct Counts {
-  uint32_t items = 0, fills = 0, tiles = 0, s_count = 0, o_count = 0, merges = 0, q_reads = 0, narrow_count = 0;
+  uint32_t items = 0, fills = 0, tiles = 0;
+  // In one register, as there are none to spare (prompts over 8 bits 330 -> 325 us):
+  // parities of the scores, outputs, readings of the queries and narrow tiles seen, and
+  // the number of joined results.
+  uint32_t seen = 0;
+  static constexpr uint32_t S = 1, O = 2, Q = 4, NARROW = 8, MERGE = 16;
+  __device__ __forceinline__ uint32_t parity(uint32_t of) const { return (seen & of) != 0; }
 };
 
 // Items up to the end, or (true) up to a narrow one.
@@ -1912,7 +1919,7 @@ __device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigne
   float sl = p.a.scale * LOG2E;
   const int all_held = QUANT ? (1 << BLOCKS8) - 1 : (1 << p.boxes) - 1;
   const int box_shift = p.a.page_shift < 7 ? p.a.page_shift : 7;
-  uint32_t &fills = n.fills, &tiles = n.tiles, &s_count = n.s_count, &o_count = n.o_count, &merges = n.merges, &q_reads = n.q_reads;
+  uint32_t &fills = n.fills, &tiles = n.tiles;
   for (uint32_t& items = n.items;; ++items) {
     const uint32_t slot = items % RING;
     wait(&sm.ring_full[slot], (items / RING) & 1, sm, err);
@@ -1937,11 +1944,15 @@ __device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigne
     // key tiles that every row of the warp sees whole: up to clear_hi, from
     // clear_lo on or below clear_sink
     const int clear_hi = hi_min - 64 - half * 64, clear_lo = lo_max - half * 64, clear_sink = sink_min - 64 - half * 64;
+    if constexpr (QUANT) {
+      if (lane == 0) static_cast<QuantSmem&>(sm).clear[threadIdx.x >> 5] = make_int4(clear_hi, clear_lo, clear_sink, 0);
+      __syncwarp();
+    }
     float m = -CUDART_INF_F, l = 0.f;  // m is the row's (in 8 bits: in powers of two), l this half's
     bool stepped = false;
     // the last joined results have been read (where they are, and what was told
     // with them, is written anew)
-    warp_wait(&sm.merge_free, (merges & 1) ^ 1, sm, err);
+    warp_wait(&sm.merge_free, n.parity(Counts::MERGE) ^ 1, sm, err);
     // over 8 bits the streams' warps share every tile's values
     for (int i = QUANT || two ? i0 : i0 + odd; i < i1; i += QUANT || two ? 1 : 2) {
       const int first_key = list_tile(it, i) * KT, key = first_key + half * 64;
@@ -1957,7 +1968,13 @@ __device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigne
         if (lane == 0) mbar_arrive(&static_cast<QuantSmem&>(sm).wide_full[at]);
       }
       if (two ? !active(it.act[s], i) : QUANT && ((i - i0) & 1) != odd) continue;
-      const bool clear = first_key <= clear_hi && (first_key >= clear_lo || first_key <= clear_sink);
+      bool clear;
+      if constexpr (QUANT) {
+        const int4 c = static_cast<QuantSmem&>(sm).clear[threadIdx.x >> 5];
+        clear = first_key <= c.x && (first_key >= c.y || first_key <= c.z);
+      } else {
+        clear = first_key <= clear_hi && (first_key >= clear_lo || first_key <= clear_sink);
+      }
       int held = 0;
       const uint32_t scales = QUANT ? (tiles + i - i0) % SCALES : 0;
       if constexpr (QUANT) {
@@ -1968,8 +1985,8 @@ __device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigne
         }
       }
       auto scale_of = [&](const float4 (&of)[SCALES][BLOCKS8 / 4], int b) { return reinterpret_cast<const float*>(&of[scales][half])[b]; };
-      warp_wait(&sm.s_full[s], s_count & 1, sm, err);
-      ++s_count;
+      warp_wait(&sm.s_full[s], n.parity(Counts::S), sm, err);
+      n.seen ^= Counts::S;
       tc::fence_after_sync();
       if (!QUANT && key + 64 > kv) {
         // the rows past the cached tokens hold whatever was there: zeros there
@@ -2138,8 +2155,8 @@ __device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigne
       sm.share[s][half][r] = l;
       named_bar_sync(pair, 64);
       l += sm.share[s][half ^ 1][r];
-      warp_wait(&sm.o_full[s], o_count & 1, sm, err);
-      ++o_count;
+      warp_wait(&sm.o_full[s], n.parity(Counts::O), sm, err);
+      n.seen ^= Counts::O;
       tc::fence_after_sync();
     }
     // m2: the reference in powers of two, -inf where the row has seen nothing, and
@@ -2151,10 +2168,10 @@ __device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigne
     if (!two && odd) {
       if (merged) {
         if (merge == q_smem) {
-          warp_wait(&sm.q_read, q_reads & 1, sm, err);
-          ++q_reads;
+          warp_wait(&sm.q_read, n.parity(Counts::Q), sm, err);
+          n.seen ^= Counts::Q;
         }
-        ++merges;
+        n.seen += Counts::MERGE;
         // rows of 512 bytes, their 16-byte pieces rotated by the row: no bank conflicts
 #pragma unroll 1
         for (int c = 0; c < 4 && any_row; ++c) {
@@ -2186,9 +2203,9 @@ __device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigne
     }
     float w0 = 1.f, w1 = 0.f;
     if (merged) {
-      warp_wait(&sm.merge_full, merges & 1, sm, err);
-      ++merges;
-      if (merge == q_smem) ++q_reads;  // over: the other stream has waited for it
+      warp_wait(&sm.merge_full, n.parity(Counts::MERGE), sm, err);
+      n.seen += Counts::MERGE;
+      if (merge == q_smem) n.seen ^= Counts::Q;  // over: the other stream has waited for it
       const float2 other = make_float2(sm.share[s ^ 1][0][r], sm.share[s ^ 1][1][r]);
       const float top = fmaxf(m2, other.x);
       if (top == -CUDART_INF_F) {
@@ -2254,7 +2271,7 @@ __device__ __forceinline__ bool softmax_items(const Params& p, Smem& sm, unsigne
       named_bar_sync(bar, 256);
       if ((threadIdx.x & 255) == 0) {
         mbar_arrive(&sm.merge_free);
-        store_release(&sm.joined, (int)merges);
+        store_release(&sm.joined, (int)(n.seen / Counts::MERGE));
       }
     }
     if (whole_pair) {
@@ -2303,11 +2320,13 @@ __device__ __forceinline__ void narrow_item(const Params& p, QuantSmem& sm, cons
   const int bar = STREAM_BAR + s, n_tiles = it.i1 - it.i0;
   if (it.lead == s) {
     if (octets(it.n_tok, p.group) == 1)
-      narrow_block<FP16, 1>(p, sm, it, q_smem, kv_smem, tmem, n.tiles, n.fills, n.narrow_count, n.o_count, n.merges);
+      narrow_block<FP16, 1>(p, sm, it, q_smem, kv_smem, tmem, n.tiles, n.fills, n.parity(Counts::NARROW), n.parity(Counts::O),
+                            n.parity(Counts::MERGE));
     else
-      narrow_block<FP16, 2>(p, sm, it, q_smem, kv_smem, tmem, n.tiles, n.fills, n.narrow_count, n.o_count, n.merges);
-    n.narrow_count += (n_tiles - half + 1) >> 1;
-    ++n.o_count;
+      narrow_block<FP16, 2>(p, sm, it, q_smem, kv_smem, tmem, n.tiles, n.fills, n.parity(Counts::NARROW), n.parity(Counts::O),
+                            n.parity(Counts::MERGE));
+    if ((n_tiles - half + 1) >> 1 & 1) n.seen ^= Counts::NARROW;
+    n.seen ^= Counts::O;
     join_groups<FP16>(p, sm, it, q_smem);
     // queries may land where the results were
     fence_proxy_async_smem();
