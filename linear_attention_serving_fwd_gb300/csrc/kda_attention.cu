@@ -76,7 +76,7 @@
 // and are bound by the same chain of scores, weights and product, with the values' part
 // in it: of a key tile's 3,300 cycles a stream spends 1,400 on weights, 200 on their
 // store and the rest on the next scores, during which it widens values.  8192 tokens over
-// 16384 of 32 heads 1.95 to 1.99 ms (1410 to 1380 TFLOP/s).
+// 16384 of 32 heads 1.93 to 1.99 ms (1425 to 1380 TFLOP/s).
 // Single tokens read half the bytes: see NARROW_ROWS.  256 requests over 2.2 GB
 // 372 us, 5.9 TB/s; copies alone take 350 to 377 us by the chip (rows of 128 bytes, 1 KB
 // apart; 256-byte rows run at 6.9 TB/s in the same ring).
@@ -108,9 +108,10 @@ constexpr int LOAD_WARP = 16, PLAN_WARP = 17, MMA_WARP = 18;  // MMA_WARP + 1: t
 // 83 us, 128 single tokens 393 -> 369 us; 6 and 2, or 4 and 1, are 1 to 5 % behind.
 constexpr int LEAD_TWO = 4, LEAD_ONE = 2;
 // Over an 8-bit cache, where blocks differ more: what a key tile and the lead count
-// (cost_two: a key tile of a block of two tiles).  A mixed batch of 64 requests takes
-// 221 us with 1 for all tiles, 158 so; a third more or less of any moves it by 2 %.
-constexpr int COST_NARROW8 = 2, COST_ONE8 = 3, LEAD_NARROW8 = 6, LEAD_ONE8 = 6, LEAD_TWO8 = 16;
+// (COST_TWO8: a key tile of a block of two tiles).  A mixed batch of 64 requests took
+// 221 us with 1 for all tiles, 158 with such counts; a third more or less of any moves
+// it, or prompts of 97 to 4096 tokens (322 us), by 2 %.
+constexpr int COST_TWO8 = 6, COST_NARROW8 = 2, COST_ONE8 = 3, LEAD_NARROW8 = 6, LEAD_ONE8 = 5, LEAD_TWO8 = 12;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // The running reference follows the row's maximum only when 64 weights have
 // come to sum to more: until then weights above one stand, and the accumulator
@@ -233,7 +234,6 @@ struct Kind {
 struct Params {
   AttentionParams a;
   KvQuantCache c;          // the 8-bit cache
-  int cost_two;            // of a key tile of a block of two tiles
   const float* q_scale;    // of the rows of its queries' parts, [t_total, hq], with scale and log2 e
   int group, tile_tok;     // G, tokens per query tile
   int n_cta;
@@ -680,7 +680,7 @@ __device__ __forceinline__ int block_lead(const Params& p, const Item& it) {
 // What a key tile of it counts.
 template <bool QUANT>
 __device__ __forceinline__ int tile_cost(const Params& p, const Item& it) {
-  if constexpr (QUANT) return it.n_tok > p.tile_tok ? p.cost_two : is_narrow(it.n_tok, p.group) ? COST_NARROW8 : COST_ONE8;
+  if constexpr (QUANT) return it.n_tok > p.tile_tok ? COST_TWO8 : is_narrow(it.n_tok, p.group) ? COST_NARROW8 : COST_ONE8;
   return 1;
 }
 template <bool QUANT>
@@ -2665,7 +2665,6 @@ int launch_attention_quant(const AttentionParams& a, const KvQuantCache& c, bool
   Params p = {};
   plan_call(p, a, workspace);
   p.c = c;
-  p.cost_two = fp16 ? 6 : 6;
   p.min_piece *= COST_NARROW8;
   const int page = 1 << a.page_shift, box = page < KT ? page : KT, parts = fp16 ? Q_PARTS<true> : Q_PARTS<false>;
   p.group_bytes = 1024;
