@@ -46,7 +46,7 @@ def test_a_block_grows():
     assert scales[0, 0, 0] == 2.0 ** -7 and (cache[0, 2] == 128).all()
     quant.append(cache, scales, np.full((1, 1, 128), 3000.0), [3])
     assert scales[0, 0, 0] == 8 and (cache[0, :2] == 0.375).all() and (cache[0, 2] == 0.125).all()
-    assert np.array_equal(quant.values(cache, scales)[0, :4, 0, 0], [3, 3, 1, 3072])
+    assert np.array_equal(quant.values(cache, scales)[0, :4, 0, 0], [3, 3, 1, 384 * 8])
     quant.append(cache, scales, np.full((1, 1, 128), 1.0), [0])  # a new tenant of the block
     assert scales[0, 0, 0] == 2.0 ** -8
 
