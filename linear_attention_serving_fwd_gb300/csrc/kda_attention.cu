@@ -1043,8 +1043,8 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
         const int mine = odd ? 0 : n_tiles;
         const uint32_t n_qk = columns(oct, Q_PARTS<FP16>), n_pv = columns(oct, W_PARTS<FP16>);
         const uint32_t id_s = idesc_f8(KT, n_qk, E4M3, E4M3), id_o = idesc_f8(D, n_pv, E4M3, E5M2) | A_MN_MAJOR | B_MN_MAJOR;
-        const uint32_t place = narrow_blocks & 1;
-        if (!odd) await(&qs.narrow_q_full[place], (narrow_blocks >> 1) & 1);
+        const uint32_t place = narrow_blocks & 1, q_full_parity = (narrow_blocks >> 1) & 1;
+        if (!odd) await(&qs.narrow_q_full[place], q_full_parity);
         ++narrow_blocks;
         const uint64_t q_desc = tc::smem_desc_sw128(q_addr + place * NARROW_Q<FP16>);
         const uint64_t w_desc = tc::smem_desc(q_addr + NARROW_P<FP16> + s * 2 * NARROW_W<FP16>, 128, 2048);
@@ -1111,6 +1111,10 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
             break;
           }
         }
+        // The other stream sees these queries land as well: a wait tells odd fills from
+        // even, and this place's next block may be its own (blocks without keys count in
+        // the streams' turn, so that one stream may lead several in a row).
+        if (odd) await(&qs.narrow_q_full[place], q_full_parity);
         if (elect_one()) {
           if (mine > 0) tc::mma_commit(&sm.o_full[s]);
           else mbar_arrive(&qs.narrow_q_empty[place]);
