@@ -66,12 +66,12 @@
 //   three 8-bit numbers, took 160 and more of them, between the scores and
 //   the product (8192 tokens over 16384 2.06 -> 1.95 ms); widened by the issuing warps,
 //   2.65 ms.
-// - In narrow blocks (see NARROW_ROWS) weights are few and the values many: there a
-//   weight is formed in fp16 and taken as two e5m2 numbers (bf16: 2^-7 of it is left at
-//   most) or three (fp16: 2^-11).  e5m2 has fp16's exponents: thousands of weights
-//   2^-18 of the largest keep their bits, where two e4m3 numbers lost 9 % of them.
-// Outputs are off 64 bits by 1.6e-3 of their norm (bf16) and 2.1e-4 (fp16), all but their
-// own rounding (1.6e-3, 2.0e-4); those of narrow blocks by 2.1e-3 and 2.3e-4.
+// - In narrow blocks (see NARROW_ROWS) weights are few and the values many: there the
+//   values stay in 8 bits and a weight, formed in fp16 as well, is the sum of three e5m2
+//   numbers (see next_part), all of it: e5m2 has fp16's exponents.
+// Outputs are off 64 bits by 1.62e-3 to 1.65e-3 of their norm in bf16, their own rounding,
+// and by 2.1e-4 to 2.3e-4 in fp16, where their own is 2.0e-4: the weights' rounding to fp16
+// is the rest, in blocks of all sizes.
 // So prompt chunks take as many tensor cycles as over 16 bits (fp16: a quarter more),
 // and are bound by the same chain of scores, weights and product, with the values' part
 // in it: of a key tile's 3,300 cycles a stream spends 1,400 on weights, 200 on their
@@ -168,8 +168,7 @@ constexpr int SCALES = 32;  // key tiles whose scales fit
 constexpr int IN_FLIGHT = 5;
 template <bool FP16>
 constexpr int Q_PARTS = FP16 ? 3 : 2;
-template <bool FP16>
-constexpr int W_PARTS = FP16 ? 3 : 2;  // narrow blocks
+constexpr int W_PARTS = 3;  // of a weight in narrow blocks
 template <bool FP16>
 constexpr int STAGES8 = FP16 ? 7 : 9;
 // Narrow blocks: few rows (single tokens, short windows) over an 8-bit cache.  A
@@ -193,8 +192,7 @@ constexpr int NARROW_P = 2 * NARROW_Q<FP16>;
 __device__ __forceinline__ bool is_narrow(int n_tok, int group) { return n_tok * group <= NARROW_ROWS; }
 __device__ __forceinline__ int octets(int n_tok, int group) { return n_tok * group <= 8 ? 1 : 2; }  // of rows
 __host__ __device__ constexpr int columns(int octets, int parts) { return (octets * parts + 1) / 2 * 16; }
-template <bool FP16>
-constexpr int NARROW_W = columns(NARROW_ROWS / 8, W_PARTS<FP16>) * KT;  // bytes of a group's weights
+constexpr int NARROW_W = columns(NARROW_ROWS / 8, W_PARTS) * KT;  // bytes of a group's weights
 struct QuantSmem : Smem {
   uint64_t full8[STAGES8<false>], empty8[STAGES8<false>];
   uint64_t wide_full[STAGES8<false>];  // the values copied to this place are there in fp16
@@ -1041,13 +1039,13 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
         QuantSmem& qs = static_cast<QuantSmem&>(sm);
         const int oct = octets(it.n_tok, p.group), n_tiles = it.i1 - it.i0;
         const int mine = odd ? 0 : n_tiles;
-        const uint32_t n_qk = columns(oct, Q_PARTS<FP16>), n_pv = columns(oct, W_PARTS<FP16>);
+        const uint32_t n_qk = columns(oct, Q_PARTS<FP16>), n_pv = columns(oct, W_PARTS);
         const uint32_t id_s = idesc_f8(KT, n_qk, E4M3, E4M3), id_o = idesc_f8(D, n_pv, E4M3, E5M2) | A_MN_MAJOR | B_MN_MAJOR;
         const uint32_t place = narrow_blocks & 1, q_full_parity = (narrow_blocks >> 1) & 1;
         if (!odd) await(&qs.narrow_q_full[place], q_full_parity);
         ++narrow_blocks;
         const uint64_t q_desc = tc::smem_desc_sw128(q_addr + place * NARROW_Q<FP16>);
-        const uint64_t w_desc = tc::smem_desc(q_addr + NARROW_P<FP16> + s * 2 * NARROW_W<FP16>, 128, 2048);
+        const uint64_t w_desc = tc::smem_desc(q_addr + NARROW_P<FP16> + s * 2 * NARROW_W, 128, 2048);
         int tile = 0, scored_n = 0, done = 0;  // key tiles passed, scored, finished
         Stage at = next, v_at = next;
         v_at.skip(1);
@@ -1067,7 +1065,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Smem& sm, int s, uint3
               const uint64_t vd = v_desc + v_at.at * (K::tile >> 4);
 #pragma unroll
               for (int j = 0; j < KT / 32; ++j)
-                mma_f8(t_o + g * 64, vd + j * 2 * v_step, w_desc + g * (NARROW_W<FP16> >> 4) + j * (512 >> 4), id_o,
+                mma_f8(t_o + g * 64, vd + j * 2 * v_step, w_desc + g * (NARROW_W >> 4) + j * (512 >> 4), id_o,
                        (j > 0 || done > 1) ? 1u : 0u);
               tc::mma_commit(K::empty(sm, v_at.at));
             }
@@ -1454,10 +1452,16 @@ __device__ __forceinline__ long long measure_line(const Params& p, Smem& sm, int
 // A score's factor of its row and its key's block, not 0 (hidden scores are -inf).
 __device__ __forceinline__ float row_factor(float sl, float ks) { return fmaxf(sl * ks, 1e-37f); }
 
-// Weights as sums of PARTS e5m2 numbers, from the largest on: e5m2 is the upper
-// half of fp16 with its exponents, so that small weights keep their relative
-// precision.  Each part takes what is left to its nearest 3 significant bits (half
-// up, in fp16's bits): of an fp16 weight two parts leave at most 2^-7 of it, three 2^-11.
+// Weights as sums of W_PARTS e5m2 numbers, from the largest on: e5m2 is the upper
+// half of fp16 with its exponents.  Each part takes what is left to its nearest 3
+// significant bits (half up, in fp16's bits), and what is left then is taken PART_STEP
+// times larger, which the results' joining takes back: 11 bits are 3 + 4 + 4 with the
+// signs, and at fp16's lower end, where e5m2 ends 8 bits earlier, the steps make up for
+// them.  So three parts are the weight exactly, whatever its size up to LIMIT.  Two parts
+// left up to 2^-7 of it, with the same sign for equal weights (outputs of 256 single
+// tokens in bf16 off by 2.0e-3 of their norm, with three by 1.62e-3), and saved next to
+// nothing: 378 us either way, a mixed batch 156 us instead of 157.
+constexpr float PART_STEP = 16.f;
 // The next part of four weights, two by two in h, which keeps what is left of them
 // where more parts follow.
 template <bool MORE>
@@ -1465,10 +1469,12 @@ __device__ __forceinline__ uint32_t next_part(uint32_t (&h)[2]) {
   uint32_t r[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    r[k] = h[k] + 0x00800080u;
+    r[k] = h[k];
     if constexpr (MORE) {
+      r[k] += 0x00800080u;
       const uint32_t top = r[k] & 0xff00ff00u;
-      const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&h[k]), *reinterpret_cast<const __half2*>(&top));
+      const __half2 rest = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&h[k]), *reinterpret_cast<const __half2*>(&top)),
+                                   __float2half2_rn(PART_STEP));
       h[k] = *reinterpret_cast<const uint32_t*>(&rest);
     }
   }
@@ -1628,7 +1634,7 @@ __device__ __forceinline__ void narrow_block(const Params& p, QuantSmem& sm, con
   const int i0 = it.i0, i1 = it.i1, kv = it.kv, n_rows = it.n_tok * p.group;
   float* factor = reinterpret_cast<float*>(sm.narrow_factor[g]);
   float* ref = reinterpret_cast<float*>(sm.narrow_m[g]);  // the rows' references, in powers of two
-  unsigned char* weights = q_smem + NARROW_P<FP16> + g * NARROW_W<FP16> + r * 16;
+  unsigned char* weights = q_smem + NARROW_P<FP16> + g * NARROW_W + r * 16;
   // what row ``lane`` sees
   const int pos = it.pos + (lane < n_rows ? lane / p.group : 0);
   const int row_hi = max(0, min(pos + 1, kv)), row_lo = p.a.window ? max(0, pos + 1 - p.a.window) : 0;
@@ -1757,7 +1763,7 @@ __device__ __forceinline__ void narrow_block(const Params& p, QuantSmem& sm, con
       }
       if (stepped) {
 #pragma unroll 1
-        for (int part = 0; part < W_PARTS<FP16>; ++part) {
+        for (int part = 0; part < W_PARTS; ++part) {
 #pragma unroll
           for (int o = 0; o < OCT; ++o) {
             uint32_t y[8];
@@ -1784,14 +1790,14 @@ __device__ __forceinline__ void narrow_block(const Params& p, QuantSmem& sm, con
     for (int k = 0; k < RP; ++k) l[k] += sum[k] * iv;
     // key r's weights of all rows, part after part: 16 bytes a line, 128 lines to 16 columns
 #pragma unroll
-    for (int part = 0; part < W_PARTS<FP16>; ++part) {
+    for (int part = 0; part < W_PARTS; ++part) {
 #pragma unroll
       for (int o = 0; o < OCT; ++o) {
         uint32_t y[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           uint32_t h[2] = {w[o * 4 + j * 2], w[o * 4 + j * 2 + 1]};
-          y[j] = part + 1 < W_PARTS<FP16> ? next_part<true>(h) : next_part<false>(h);
+          y[j] = part + 1 < W_PARTS ? next_part<true>(h) : next_part<false>(h);
           w[o * 4 + j * 2] = h[0];
           w[o * 4 + j * 2 + 1] = h[1];
         }
@@ -1814,17 +1820,17 @@ __device__ __forceinline__ void narrow_block(const Params& p, QuantSmem& sm, con
   if (stepped) {
 #pragma unroll
     for (int o = 0; o < OCT; ++o) {
-      uint32_t y[W_PARTS<FP16>][8];
+      uint32_t y[W_PARTS][8];
 #pragma unroll
-      for (int part = 0; part < W_PARTS<FP16>; ++part) tmem_ld8_async(t_o + part * RP + o * 8, y[part]);
+      for (int part = 0; part < W_PARTS; ++part) tmem_ld8_async(t_o + part * RP + o * 8, y[part]);
       tc::tmem_wait_ld();
 #pragma unroll
-      for (int part = 0; part < W_PARTS<FP16>; ++part) tmem_regs8(y[part]);
+      for (int part = 0; part < W_PARTS; ++part) tmem_regs8(y[part]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        float sum = __uint_as_float(y[0][k]);
+        float sum = __uint_as_float(y[W_PARTS - 1][k]);
 #pragma unroll
-        for (int part = 1; part < W_PARTS<FP16>; ++part) sum += __uint_as_float(y[part][k]);
+        for (int part = W_PARTS - 2; part >= 0; --part) sum = fmaf(sum, 1.f / PART_STEP, __uint_as_float(y[part][k]));
         merge[(o * 8 + k) * D + r] = sum;
       }
     }
@@ -2447,8 +2453,8 @@ static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 template <bool FP16>
 constexpr size_t SMEM_BYTES8 = 2 * Kind<FP16, true>::q_tile + STAGES8<FP16> * TILE8_BYTES + sizeof(QuantSmem);
 static_assert(SMEM_BYTES8<false> <= 232448 && SMEM_BYTES8<true> <= 232448, "shared memory of one CTA");
-static_assert(NARROW_P<false> + 4 * NARROW_W<false> <= Kind<false, true>::q_tile &&
-                  NARROW_P<true> + 4 * NARROW_W<true> <= Kind<true, true>::q_tile,
+static_assert(NARROW_P<false> + 4 * NARROW_W <= Kind<false, true>::q_tile &&
+                  NARROW_P<true> + 4 * NARROW_W <= Kind<true, true>::q_tile,
               "narrow blocks' queries and weights in the first tile's place");
 static_assert(4 * NARROW_ROWS * D * 4 <= Kind<false, true>::q_tile, "their results in the second one's");
 
