@@ -647,7 +647,9 @@ typedef struct kda_kv_quant_cache {
  * A negative slot skips the token; a slot past the cache sets
  * KDA_ERR_DEVICE_INDEX and skips it; one in its predecessor's
  * block that does not follow it does so too, for itself and the rest of the
- * block.  Tokens of a block that stand apart race.
+ * block; and so does one that follows a token of no or another block, while its
+ * own block has tokens among the 32 before it (one is skipped in between, or
+ * another request's stand there).  Tokens of a block that stand further apart race.
  */
 int kda_kv_append_quant(const kda_kv_quant_cache* cache, const void* k, int64_t k_stride_tok, int64_t k_stride_head,
                         const void* v, int64_t v_stride_tok, int64_t v_stride_head, const int32_t* slot_map,

@@ -8,11 +8,11 @@
 // precision (e4m3 has an exponent of its own) and make the second rounding of
 // earlier rows, when the scale grows, exact but for numbers below e4m3's normal range.
 //
-// Both are bound by memory where they are large: 32768 tokens of 8 heads are written
-// in 33 us (5.7 TB/s of what is read and written), 75,000 read back in 82 us (5.6
+// Both are bound by memory where they are large: 30352 tokens of 8 heads are written
+// in 34 us (5.5 TB/s of what is read and written), 75,000 read back in 82 us (5.6
 // TB/s, two thirds of it writes).  A decode step's write is a chain of loads: slots,
 // then the new row and the block's scale, then its earlier rows where the scale
-// grows: 256 tokens 5.4 us.
+// grows: 256 tokens 5.65 us.
 #include <cuda_fp8.h>
 
 #include "kda_kv.cuh"
@@ -57,7 +57,8 @@ __device__ __forceinline__ uint32_t max_halves(uint32_t m, uint32_t w) { return 
 // head of k or of v of those blocks: lane l holds 8 dimensions of the rows of
 // one parity, so that a load or store of the warp is two whole rows.  One warp has
 // a block's new rows, its scale and its earlier rows to itself, so nothing is
-// agreed on with others.  Four CTAs an SM (64 registers): 32768 tokens 36.3 -> 33.4 us.
+// agreed on with others.  Four CTAs an SM (64 registers, 48 bytes spilled): 30352 tokens
+// 36.3 -> 33.4 us when it was set.
 template <bool FP16>
 __global__ void __launch_bounds__(256, 4) kv_quant_append_kernel(KvQuantAppendParams p) {
   constexpr uint32_t LARGEST = FP16 ? 0x7bffu : 0x7f7fu;  // finite
@@ -89,9 +90,16 @@ __global__ void __launch_bounds__(256, 4) kv_quant_append_kernel(KvQuantAppendPa
   for (unsigned todo = __ballot_sync(0xffffffffu, first); todo; todo &= todo - 1) {
     const int64_t t = t0 + __ffs(todo) - 1;
     // the block's tokens: those that follow one by one
-    int next = -1;
+    int next = -1, near = -1;
     if (lane < QB && t + lane < p.t_total) next = p.slot_map[t + lane];
+    if (t - 32 + lane >= 0) near = p.slot_map[t - 32 + lane];
     const int slot = __shfl_sync(0xffffffffu, next, 0);
+    // Tokens of the block among the 32 before, that these do not follow: their warp has
+    // it.  (256 tokens 5.4 -> 5.65 us, 30352 tokens 33.8 -> 34.05 us.)
+    if (__any_sync(0xffffffffu, near >= 0 && near / QB == slot / QB)) {
+      if (lane == 0) set_error(p.err, ERR_INDEX);
+      continue;
+    }
     const int r0 = slot & (QB - 1);
     const unsigned run = __ballot_sync(0xffffffffu, lane < QB - r0 && next == slot + lane);
     const int n = __ffs(~run) - 1;

@@ -215,7 +215,8 @@ def kda_kv_append(cache: KvCache, k, v, slot_map, *, stream=None) -> None:
     """Write k and v [T, Hkv, 128] to the slots ``slot_map`` [T] (int32, -1
     skips the token).  In an 8-bit cache the scales of the tokens' blocks are
     set or grown; the tokens of one block stand side by side, as
-    :func:`kda_kv_extend` lays them out."""
+    :func:`kda_kv_extend` lays them out (others near by are reported by
+    :func:`kda_device_status` and not written)."""
     index = cache._index
     t, _, kp, kt, kh = _rows(k, "k", cache.dtype, index, cache.n_kv_heads)
     tv, _, vp, vt, vh = _rows(v, "v", cache.dtype, index, cache.n_kv_heads)
