@@ -673,6 +673,11 @@ int kda_kv_read_quant(const kda_kv_quant_cache* cache, const int32_t* slot_map, 
  * and the results are those of kda_paged_attention.  A query row with an
  * infinity or a NaN counts as NaN.  A visible scale outside [2^-48, 2^48] (or
  * NaN) sets KDA_ERR_DEVICE_RANGE and counts as the nearest number inside (1).
+ * Rounded to fewer than 32 bits: a weight to fp16 (2^-11 of it; below 2^-21 of the
+ * row's largest, value scales included, 2^-32 of that), the sum that divides takes it
+ * unrounded; elements of a query row below 2^-10 of the row's largest, by at most
+ * 2^-17 of that; the results.  Keys, values and scales that are powers of two are
+ * taken exactly.
  *   workspace   16-byte aligned, kda_paged_attention_quant_workspace_bytes(t_total,
  *               hq) bytes or more, else as kda_paged_attention's: one workspace
  *               serves both

@@ -55,8 +55,9 @@
 // keys of a head, v_j likewise; tiles of 16 KB.
 // - The keys go to the tensor cores as they are, as operands of 8 bits, twice as many
 //   of which are multiplied at once; a query row is a power of two times the sum of
-//   two e4m3 numbers (bf16: exact) or three (fp16), by a kernel of its own,
-//   split_queries_kernel.
+//   two e4m3 numbers (bf16) or three (fp16), by a kernel of its own,
+//   split_queries_kernel: exact, but for elements below 2^-10 of the row's largest,
+//   which are off by at most 2^-17 of it.
 // - The keys' scale and the row's are a factor of the score.  The values' is part
 //   of it: p_j = 2^(a s_j + log2 v_scale - m) is what the tensor cores take, and
 //   p_j / v_scale what the row's sum takes.
@@ -76,9 +77,9 @@
 // and are bound by the same chain of scores, weights and product, with the values' part
 // in it: of a key tile's 3,300 cycles a stream spends 1,400 on weights, 200 on their
 // store and the rest on the next scores, during which it widens values.  8192 tokens over
-// 16384 of 32 heads 1.93 to 1.99 ms (1425 to 1380 TFLOP/s).
+// 16384 of 32 heads 1.93 to 1.99 ms (1425 to 1380 TFLOP/s), in fp16 2.28 ms.
 // Single tokens read half the bytes: see NARROW_ROWS.  256 requests over 2.2 GB
-// 372 us, 5.9 TB/s; copies alone take 350 to 377 us by the chip (rows of 128 bytes, 1 KB
+// 372 to 378 us, 5.9 TB/s; copies alone take 350 to 377 us by the chip (rows of 128 bytes, 1 KB
 // apart; 256-byte rows run at 6.9 TB/s in the same ring).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -180,7 +181,11 @@ constexpr int STAGES8 = FP16 ? 7 : 9;
 // one begins while the other ends; a stream's two warpgroups take its key tiles in
 // turn, each with a reference, sums and an O^T of its own, and their results are
 // joined in shared memory.  256 single tokens of four heads a key head: 530 us with
-// a row a lane, 372 so, the tensor cores 4 % busy.
+// a row a lane, 372 so, the tensor cores 6 % busy.
+// With 9 to 16 rows, which no longer wait in registers, it still is where caches are
+// long: 64 requests of four tokens by four heads over 512 to 8191 cached 163 us with a
+// row a lane and 121 so (fp16 192 and 124), 128 of 16 heads 166 and 123 (199 and 127); 200
+// requests of up to 64 cached 80 and 83, one of 4096 19.4 and 21.1.
 constexpr int NARROW_ROWS = 16;
 // In the queries' buffer: those of two narrow blocks, so that the next one's are
 // there when it begins, and behind them the weights.
@@ -768,7 +773,8 @@ __device__ __forceinline__ void load_role(const Params& p, const Maps& maps, Sme
     };
     int pg = QUANT ? -1 : page_of(it.i0);
     // Queries: their buffer is free only when the item before is through, so the
-    // first keys and values go ahead of them while there is room.
+    // first keys and values go ahead of them while there is room.  (Not those of the
+    // CTA's first item: its buffer is free, and in 8 bits they wait for the split.)
     bool asked = false;
     const bool narrow = QUANT && is_narrow(it.n_tok, p.group);
     auto queries_free = [&]() {
@@ -1460,7 +1466,7 @@ __device__ __forceinline__ float row_factor(float sl, float ks) { return fmaxf(s
 // them.  So three parts are the weight exactly, whatever its size up to LIMIT.  Two parts
 // left up to 2^-7 of it, with the same sign for equal weights (outputs of 256 single
 // tokens in bf16 off by 2.0e-3 of their norm, with three by 1.62e-3), and saved next to
-// nothing: 378 us either way, a mixed batch 156 us instead of 157.
+// nothing: 378 us either way, a mixed batch 149 us instead of 150.
 constexpr float PART_STEP = 16.f;
 // The next part of four weights, two by two in h, which keeps what is left of them
 // where more parts follow.

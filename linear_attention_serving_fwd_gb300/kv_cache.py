@@ -280,7 +280,9 @@ def kda_paged_attention(cache: KvCache, q, cu_seqlens, kv_lens, block_table, *, 
     them, and the first ``sinks``.  Returns (out [T, Hq, 128], lse fp32
     [T, Hq] or None).  ``workspace``: :func:`paged_attention_workspace`, made
     for the call when not given.  What the call makes belongs to ``stream``, as
-    in :func:`kda_kv_extend`."""
+    in :func:`kda_kv_extend`.  Over an 8-bit cache keys and values are what it
+    stands for, weights are rounded to fp16, and so much of a query row's
+    smallest elements is dropped as include/kda.h says."""
     index = cache._index
     if stream is not None:
         _check_stream(stream, index)
