@@ -77,7 +77,7 @@
 // and are bound by the same chain of scores, weights and product, with the values' part
 // in it: of a key tile's 3,300 cycles a stream spends 1,400 on weights, 200 on their
 // store and the rest on the next scores, during which it widens values.  8192 tokens over
-// 16384 of 32 heads 1.93 to 1.99 ms (1425 to 1380 TFLOP/s), in fp16 2.28 ms.
+// 16384 of 32 heads 1.93 to 2.01 ms (1425 to 1370 TFLOP/s), in fp16 2.28 ms.
 // Single tokens read half the bytes: see NARROW_ROWS.  256 requests over 2.2 GB
 // 372 to 378 us, 5.9 TB/s; copies alone take 350 to 377 us by the chip (rows of 128 bytes, 1 KB
 // apart; 256-byte rows run at 6.9 TB/s in the same ring).
